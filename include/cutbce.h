@@ -296,6 +296,124 @@ cutbce_status cutbce_topk(const void* Q, int64_t B, const void* E, int64_t V, in
 cutbce_status cutbce_hit_at_k(const int32_t* ids, int64_t B, int k, const int32_t* targets, int64_t L, int32_t* hits,
                               cutbce_stream_t stream);
 
+/* ------------------------------------------------------------------ item rows
+ * Rows of the item table going into a model, and their gradient.
+ *
+ * cutbce_embed_forward:  X[n] = scale * E[ids[n]], rounded once; an id of -1 is an
+ * empty entry (padding) and gives a zero row.  E [V, D] and X [N, D], row-major,
+ * bf16 or fp32 (dtype), aligned to an element; 16-byte aligned arrays whose rows
+ * are a multiple of 16 bytes take the fast path.  1 <= D <= 16384, N < 2^28,
+ * V < 2^31 - 1.  status: device int32 that is set to CUTBCE_ERR_TARGET_RANGE (and
+ * never cleared) if an id is neither -1 nor in [0, V) -- that entry's row is zero
+ * -- or NULL.  Asynchronous on `stream`; one kernel, no workspace. */
+cutbce_status cutbce_embed_forward(const void* E, int64_t V, int64_t D, int32_t dtype, const int32_t* ids, int64_t N,
+                                   float scale, void* X, int32_t* status, cutbce_stream_t stream);
+
+/* The gradient of cutbce_embed_forward with respect to E:
+ *   dE[v] = scale * sum_{n : ids[n] = v} dX[n]        (accumulate = 0: every row of dE is written)
+ *   dE[v] += the same                                  (accumulate = 1: only rows with an entry are touched)
+ * dX [N, D] bf16 or fp32 (dtype); dE [V, D] fp32 or bf16 (grad_dtype,
+ * CUTBCE_GRAD_*).  The entries are sorted by id (stable) and summed in fp32 in a
+ * fixed order, so the result is bit-reproducible and hot ids do not serialise; each
+ * output is rounded once (with accumulate the fp32 sum is added to the old value
+ * and that is rounded).  accumulate = 1 with the dE of a loss gives the gradient
+ * of a table that is both the model's input and its output.  A bad id sets the
+ * workspace status word (cutbce_read_status); dE is then unspecified.
+ * ws: cutbce_embed_workspace_size bytes (about 16 N + N D / 4), 256-byte aligned. */
+cutbce_status cutbce_embed_workspace_size(int64_t N, int64_t V, int64_t D, size_t* bytes);
+cutbce_status cutbce_embed_backward(const void* dX, int32_t dtype, const int32_t* ids, int64_t N, int64_t V, int64_t D,
+                                    float scale, void* dE, int32_t grad_dtype, int32_t accumulate, void* ws,
+                                    size_t ws_bytes, cutbce_stream_t stream);
+
+/* ------------------------------------------------------------------ softmax losses
+ * Losses with a softmax over the whole item table.  As for the BCE loss, the
+ * logits z_tv = h_t . e_v and their gradient never reach device memory: tiles of
+ * them are formed in tensor memory and consumed there.  H, E bf16 (D a multiple of
+ * 8, at most 256, 16-byte aligned); T < 2^24 - 255, V < 2^31 - 1, T K < 2^28.
+ * With p_t = softmax(z_t / tau), every gradient has the form
+ *   dz_tv = w_t (p_tv - q_tv),   dH = dz E,   dE = dz^T H.
+ * The dense part w p is rounded to bf16 once, as the operand of the second tensor
+ * contraction; the sparse part w q stays in fp32.  Deterministic.
+ *
+ * Gradient options (NULL: fp32, overwrite). */
+typedef struct {
+  int32_t grad_dtype;        /* CUTBCE_GRAD_F32 or CUTBCE_GRAD_BF16: dtype of dH and dE */
+  int32_t accumulate;        /* bits CUTBCE_ACCUMULATE_DH / _DE: add to the old contents, rounded once */
+} cutbce_grad_options;
+
+/* Distillation from a teacher's top logits (for example the ids and scores that
+ * cutbce_topk gives for a teacher's states).  Position t has K slots (id, logit):
+ *   q_t   = softmax over its non-empty slots of logit / tau
+ *   lse_t = ln sum_{v < V} exp(z_tv / tau)
+ *   loss  = s * sum_t w_t tau^2 sum_k q_tk (ln q_tk - z_{t, id_k} / tau + lse_t)
+ *   dz_tv = g s w_t tau (p_tv - sum_{k : id_k = v} q_tk)
+ * i.e. tau^2 KL(q || p); s = 1 / (positions that count) or 1 (CUTBCE_SUM). */
+typedef struct {
+  int64_t T, V, D, K;        /* K slots per position, 1..128 */
+  int32_t dtype;             /* CUTBCE_BF16 */
+  int32_t reduction;         /* CUTBCE_MEAN_VALID_POSITIONS or CUTBCE_SUM */
+  const void* H;             /* [T, D] student states */
+  const void* E;             /* [V, D] item table */
+  const int32_t* ids;        /* [T, K] teacher's ids; -1 empty.  An id may repeat: its weights add */
+  const float* logits;       /* [T, K] teacher's logits; -infinity gives weight 0; ignored in empty slots.
+                                NaN and +infinity in a filled slot make the position's terms NaN */
+  const uint8_t* mask;       /* [T] 1 = counts, or NULL */
+  const float* weights;      /* [T] factor of each position, any sign, or NULL; 0 is padding */
+  float temperature;         /* tau > 0 */
+} cutbce_distill_problem;
+/* A position does not count (no loss, a zero dH row, lse 0, not in the mean) if it
+ * is masked, its weight is 0, or all its slots are empty or -infinity; ids and
+ * logits of masked and zero-weight positions are not looked at. */
+
+/* Bytes of workspace for a call with the given outputs (CUTBCE_OUT_LOSS | _DH | _DE). */
+cutbce_status cutbce_distill_workspace_size(const cutbce_distill_problem* prob, int outputs, size_t* bytes);
+/* loss: device double; lse: device float [T]; either may be NULL. */
+cutbce_status cutbce_distill_forward(const cutbce_distill_problem* prob, double* loss, float* lse, void* ws,
+                                     size_t ws_bytes, cutbce_stream_t stream);
+/* Gradients, given the lse that a forward on the same inputs wrote.  grad_loss:
+ * device float g or NULL for 1; dH [T, D] or dE [V, D] may be NULL. */
+cutbce_status cutbce_distill_backward(const cutbce_distill_problem* prob, const cutbce_grad_options* opts,
+                                      const float* lse, const float* grad_loss, void* dH, void* dE, void* ws,
+                                      size_t ws_bytes, cutbce_stream_t stream);
+/* Both in one call; any output may be NULL, but not all. */
+cutbce_status cutbce_distill_forward_backward(const cutbce_distill_problem* prob, const cutbce_grad_options* opts,
+                                              const float* grad_loss, double* loss, float* lse, void* dH, void* dE,
+                                              void* ws, size_t ws_bytes, cutbce_stream_t stream);
+
+/* Preference loss over pairs of item sequences (paired log ratios against a
+ * reference model).  The T positions hold 2P packed sequences of any length, zero
+ * included: sequence i is [offsets[i], offsets[i + 1]); pair p is sequence 2p
+ * (chosen) and 2p + 1 (rejected).  ids[t] is the item that followed position t.
+ *   L_i  = sum over the positions of sequence i of (z_{t, ids_t} - lse_t)
+ *   x_p  = beta ((L_2p - L_2p+1) - (R_2p - R_2p+1))
+ *   loss = s * sum_p ln(1 + e^-x_p),   s = 1 / P or 1 (CUTBCE_SUM)
+ * The sequences' log-probabilities L are an output too: a forward with the
+ * reference model's H and E and no ref_logp gives R. */
+typedef struct {
+  int64_t T, V, D, P;        /* P pairs */
+  int32_t dtype;             /* CUTBCE_BF16 */
+  int32_t reduction;         /* CUTBCE_MEAN_VALID_POSITIONS (mean over the pairs) or CUTBCE_SUM */
+  const void* H;             /* [T, D] */
+  const void* E;             /* [V, D] */
+  const int32_t* ids;        /* [T]; -1 = the position does not count */
+  const int32_t* offsets;    /* [2P + 1] ascending, in [0, T]; positions outside [offsets[0], offsets[2P]) do not count */
+  const float* ref_logp;     /* [2P] R, or NULL for 0 */
+  const uint8_t* mask;       /* [T] 1 = counts, or NULL */
+  float beta;
+} cutbce_preference_problem;
+/* Offsets that descend or leave [0, T] are a data error (CUTBCE_ERR_TARGET_RANGE). */
+cutbce_status cutbce_preference_workspace_size(const cutbce_preference_problem* prob, int outputs, size_t* bytes);
+/* loss: device double; logp: device float [2P]; lse: device float [T] (0 where a position does not count). */
+cutbce_status cutbce_preference_forward(const cutbce_preference_problem* prob, double* loss, float* logp, float* lse,
+                                        void* ws, size_t ws_bytes, cutbce_stream_t stream);
+cutbce_status cutbce_preference_backward(const cutbce_preference_problem* prob, const cutbce_grad_options* opts,
+                                         const float* lse, const float* grad_loss, void* dH, void* dE, void* ws,
+                                         size_t ws_bytes, cutbce_stream_t stream);
+cutbce_status cutbce_preference_forward_backward(const cutbce_preference_problem* prob,
+                                                 const cutbce_grad_options* opts, const float* grad_loss, double* loss,
+                                                 float* logp, float* lse, void* dH, void* dE, void* ws,
+                                                 size_t ws_bytes, cutbce_stream_t stream);
+
 /* Synchronises `stream` and returns the device status word of the last call
  * that used this workspace (CUTBCE_OK, TARGET_RANGE or TIMEOUT). */
 cutbce_status cutbce_read_status(const void* ws, cutbce_stream_t stream);
@@ -325,7 +443,15 @@ enum {
   CUTBCE_KERNEL_TOPK = 8,           /* cutbce_topk: tensor-core scores and per-thread candidate lists */
   CUTBCE_KERNEL_TOPK_MERGE = 9,     /* cutbce_topk: fixed-order merge of the candidate lists */
   CUTBCE_KERNEL_COL_SUMS = 10,      /* column sums of E and of the compacted H: the loss's linear half */
-  CUTBCE_NUM_KERNEL_KINDS = 11
+  CUTBCE_KERNEL_EMBED = 11,         /* cutbce_embed_forward */
+  CUTBCE_KERNEL_ID_SORT = 12,       /* entries ordered by item id: all passes */
+  CUTBCE_KERNEL_SEGMENT_SUM = 13,   /* rows summed by item id */
+  CUTBCE_KERNEL_HEAD_PREP = 14,     /* softmax losses: row rules, compaction, sparse targets */
+  CUTBCE_KERNEL_HEAD_LSE_PASS = 15, /* softmax losses: tensor-core pass for the log-sum-exps */
+  CUTBCE_KERNEL_HEAD_ROW_PASS = 16, /* softmax losses: tensor-core pass for dH */
+  CUTBCE_KERNEL_HEAD_ITEM_PASS = 17,/* softmax losses: tensor-core pass for dE */
+  CUTBCE_KERNEL_HEAD_FINISH = 18,   /* softmax losses: row joins, loss, dH */
+  CUTBCE_NUM_KERNEL_KINDS = 19
 };
 
 /* Per-kernel device timing for benchmarks.  While enabled (process-wide),

@@ -5,13 +5,16 @@ libcutbce's kernels (see include/cutbce.h).
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Optional
 
 import torch
 
 from . import binding as B
 
-__all__ = ["forward", "backward", "forward_backward", "cut_bce", "Workspace"]
+__all__ = ["forward", "backward", "forward_backward", "cut_bce", "Workspace", "embed", "embed_forward",
+           "embed_backward", "distill_loss", "distill_forward", "distill_backward", "distill_forward_backward",
+           "preference_loss", "preference_forward", "preference_backward", "preference_forward_backward"]
 
 
 class Workspace:
@@ -119,3 +122,305 @@ class _CutBCE(torch.autograd.Function):
 def cut_bce(H, E, targets, mask=None, reduction: str = "mean") -> torch.Tensor:
     """Differentiable fused BCE loss over the full vocabulary (autograd-aware)."""
     return _CutBCE.apply(H, E, targets, mask, reduction)
+
+
+# ---------------------------------------------------------------- item rows and softmax losses
+# These calls run on the device of their tensors and on that device's current
+# stream, and take their workspace from torch's caching allocator per call, so
+# calls on several streams, and captured graphs, never share one.
+
+def _on(t: torch.Tensor):
+    if t.device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, not {t.device}")
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def _ids32(ids: torch.Tensor) -> torch.Tensor:
+    if ids.dtype == torch.int32:
+        return ids.contiguous()
+    if ids.dtype not in (torch.int64, torch.int16, torch.int8, torch.uint8):
+        raise ValueError(f"ids must be integers, not {ids.dtype}")
+    if ids.dtype == torch.int64:
+        ids = ids.clamp(-2, 2 ** 31 - 1)          # a far id stays out of range instead of wrapping
+    return ids.to(torch.int32).contiguous()
+
+
+def _scalar_grad(g: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    return None if g is None else g.detach().to(torch.float32).reshape(())
+
+
+def _workspace(nbytes: int, device: torch.device, given: Optional[torch.Tensor]) -> torch.Tensor:
+    return given if given is not None else torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def embed_forward(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, status: Optional[torch.Tensor] = None):
+    """scale * E[ids] (any shape of ids; -1 gives a zero row), in E's dtype (bf16 or fp32)."""
+    if E.dim() != 2:
+        raise ValueError("E must be [V, D]")
+    with _on(E):
+        X = torch.empty(ids.shape + E.shape[1:], dtype=E.dtype, device=E.device)
+        if ids.numel() > 0:
+            B.cutbce_embed_forward(E.detach().contiguous(), _ids32(ids).reshape(-1), X.view(-1, E.shape[1]), scale,
+                                   status)
+    return X
+
+
+def embed_backward(dX: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 1.0,
+                   grad_dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None,
+                   accumulate: bool = False, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dE [V, D] of embed_forward: dE[v] = scale * sum of dX over the entries with id v.
+
+    `out` (contiguous, [V, D]) is written instead of a new tensor; with accumulate the
+    sums are added to it and rows without an entry keep their value."""
+    D = dX.shape[-1]
+    if dX.shape[:-1] != ids.shape:
+        raise ValueError("dX must be ids.shape + [D]")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    if out is not None and tuple(out.shape) != (V, D):
+        raise ValueError(f"out must be [{V}, {D}]")
+    with _on(dX):
+        if ids.numel() == 0:
+            if out is None:
+                return torch.zeros((V, D), dtype=grad_dtype, device=dX.device)
+            return out if accumulate else out.zero_()
+        dE = out if out is not None else torch.empty((V, D), dtype=grad_dtype, device=dX.device)
+        ws = _workspace(B.cutbce_embed_workspace_size(ids.numel(), V, D), dX.device, workspace)
+        B.cutbce_embed_backward(dX.detach().contiguous().view(-1, D), _ids32(ids).reshape(-1), dE, ws, scale,
+                                accumulate)
+    return dE
+
+
+class _Embed(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, E, ids, scale):
+        ids = _ids32(ids)
+        ctx.save_for_backward(ids)
+        ctx.shape, ctx.dtype, ctx.scale = E.shape, E.dtype, scale
+        return embed_forward(E, ids, scale)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dX):
+        (ids,) = ctx.saved_tensors
+        return embed_backward(dX, ids, ctx.shape[0], ctx.scale, grad_dtype=ctx.dtype), None, None
+
+
+def embed(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
+    """Differentiable scale * E[ids]; the gradient with respect to E is dense, in E's dtype."""
+    return _Embed.apply(E, ids, float(scale))
+
+
+def _rows(H: torch.Tensor, *rest: Optional[torch.Tensor]):
+    """H [.., D] and per-position tensors flattened to T rows."""
+    lead = H.dim() - 1
+    out = [H.detach().contiguous().view(-1, H.shape[-1])]
+    for t in rest:
+        if t is not None and t.shape[:lead] != H.shape[:lead]:
+            raise ValueError(f"leading sizes {tuple(t.shape[:lead])} and {tuple(H.shape[:lead])} do not fit")
+        out.append(None if t is None else t.detach().reshape((-1,) + tuple(t.shape[lead:])).contiguous())
+    return out
+
+
+def _distill_problem(H, E, ids, logits, mask, weights, temperature, reduction):
+    """The problem and the tensors it points to (to be kept until the launch)."""
+    if logits.shape != ids.shape:
+        raise ValueError("teacher ids and logits must have one shape")
+    H2, ids2, lg, m, w = _rows(H, _ids32(ids), logits.to(torch.float32), mask,
+                               None if weights is None else weights.to(torch.float32))
+    E2 = E.detach().contiguous()
+    keep = (H2, E2, ids2, lg, m, w)
+    return B.make_distill_problem(H2, E2, ids2, lg, m, w, temperature, reduction), keep
+
+
+def _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction):
+    H2, ids2, m = _rows(H, _ids32(ids), mask)
+    if offsets is None:
+        if H.dim() != 3:
+            raise ValueError("without offsets H must be [2P, N, D]")
+        offsets = torch.arange(0, H2.shape[0] + 1, H.shape[1], dtype=torch.int32, device=H.device)
+    E2 = E.detach().contiguous()
+    off = offsets.to(torch.int32).contiguous()
+    ref = None if ref_logp is None else ref_logp.detach().to(torch.float32).reshape(-1).contiguous()
+    keep = (H2, E2, ids2, off, ref, m)
+    return B.make_preference_problem(H2, E2, ids2, off, ref, m, beta, reduction), keep
+
+
+def _grad_outputs(H, E, want_dH, want_dE, grad_dtype, dE_out, accumulate_dE):
+    if accumulate_dE and dE_out is None:
+        raise ValueError("accumulate_dE needs dE_out")
+    if dE_out is not None and tuple(dE_out.shape) != tuple(E.shape):
+        raise ValueError("dE_out must have E's shape")
+    if not want_dH and not want_dE:
+        raise ValueError("neither gradient is wanted")
+    B._same_device(H, dE_out)
+    dH = torch.empty(H.shape, dtype=grad_dtype, device=H.device) if want_dH else None
+    dE = None
+    if want_dE:
+        dE = dE_out if dE_out is not None else torch.empty(E.shape, dtype=grad_dtype, device=E.device)
+    return dH, dE, B.make_grad_options(dH, dE, B.ACCUMULATE_DE if accumulate_dE else 0)
+
+
+def _bits(dH, dE) -> int:
+    return (B.OUT_DH if dH is not None else 0) | (B.OUT_DE if dE is not None else 0)
+
+
+def _lse_rows(lse: torch.Tensor, H: torch.Tensor) -> torch.Tensor:
+    if lse.dtype != torch.float32 or lse.shape != H.shape[:-1] or lse.device != H.device:
+        raise ValueError("lse must be the float32 tensor of a forward on the same inputs")
+    return lse.contiguous()
+
+
+def distill_forward(H, E, teacher_ids, teacher_logits, mask=None, weights=None, temperature: float = 1.0,
+                    reduction: str = "mean", workspace: Optional[torch.Tensor] = None):
+    """Distillation loss (0-d float64) and the rows' log-sum-exps of z / temperature (float32, H.shape[:-1]).
+
+    H [T, D] or [B, N, D] and E [V, D] bf16; teacher_ids [.., K] (-1 empty) and teacher_logits [.., K]
+    the teacher's top items and logits of each position; mask 1 = counts; weights a factor per position."""
+    with _on(H):
+        prob, keep = _distill_problem(H, E, teacher_ids, teacher_logits, mask, weights, temperature, reduction)
+        ws = _workspace(B.cutbce_distill_workspace_size(prob, B.OUT_LOSS), H.device, workspace)
+        loss = torch.empty((), dtype=torch.float64, device=H.device)
+        lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
+        B.cutbce_distill_forward(prob, loss, lse, ws)
+    return loss, lse
+
+
+def distill_backward(H, E, teacher_ids, teacher_logits, lse, mask=None, weights=None, temperature: float = 1.0,
+                     reduction: str = "mean", grad_loss=None, want_dH: bool = True, want_dE: bool = True,
+                     grad_dtype: torch.dtype = torch.float32, dE_out=None, accumulate_dE: bool = False,
+                     workspace: Optional[torch.Tensor] = None):
+    """(dH, dE) given the lse of distill_forward on the same inputs."""
+    with _on(H):
+        prob, keep = _distill_problem(H, E, teacher_ids, teacher_logits, mask, weights, temperature, reduction)
+        dH, dE, opts = _grad_outputs(H, E, want_dH, want_dE, grad_dtype, dE_out, accumulate_dE)
+        ws = _workspace(B.cutbce_distill_workspace_size(prob, _bits(dH, dE)), H.device, workspace)
+        g = _scalar_grad(grad_loss)
+        B.cutbce_distill_backward(prob, opts, _lse_rows(lse, H), g, dH, dE, ws)
+    return dH, dE
+
+
+def distill_forward_backward(H, E, teacher_ids, teacher_logits, mask=None, weights=None, temperature: float = 1.0,
+                             reduction: str = "mean", grad_loss=None, want_dH: bool = True, want_dE: bool = True,
+                             grad_dtype: torch.dtype = torch.float32, dE_out=None, accumulate_dE: bool = False,
+                             workspace: Optional[torch.Tensor] = None):
+    """(loss, lse, dH, dE) in one call; None for a gradient that is not wanted.
+
+    dE_out ([V, D], contiguous) is written instead of a new tensor, or added to with accumulate_dE."""
+    with _on(H):
+        prob, keep = _distill_problem(H, E, teacher_ids, teacher_logits, mask, weights, temperature, reduction)
+        dH, dE, opts = _grad_outputs(H, E, want_dH, want_dE, grad_dtype, dE_out, accumulate_dE)
+        ws = _workspace(B.cutbce_distill_workspace_size(prob, B.OUT_LOSS | _bits(dH, dE)), H.device, workspace)
+        loss = torch.empty((), dtype=torch.float64, device=H.device)
+        lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
+        g = _scalar_grad(grad_loss)
+        B.cutbce_distill_forward_backward(prob, opts, g, loss, lse, dH, dE, ws)
+    return loss, lse, dH, dE
+
+
+def preference_forward(H, E, ids, offsets=None, ref_logp=None, mask=None, beta: float = 0.1, reduction: str = "mean",
+                       workspace: Optional[torch.Tensor] = None):
+    """Preference loss (0-d float64), the sequences' log-probabilities (float32 [2P]) and the rows'
+    log-sum-exps (float32).
+
+    H [T, D] with offsets [2P + 1] of the packed sequences (2p chosen, 2p + 1 rejected), or H [2P, N, D]
+    without; ids: the item that followed each position (-1: does not count); ref_logp [2P]: the
+    sequences' log-probabilities under the reference model (the second output of this call with
+    that model's H and E), or None for 0."""
+    with _on(H):
+        prob, keep = _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction)
+        ws = _workspace(B.cutbce_preference_workspace_size(prob, B.OUT_LOSS), H.device, workspace)
+        loss = torch.empty((), dtype=torch.float64, device=H.device)
+        logp = torch.empty(2 * prob.P, dtype=torch.float32, device=H.device)
+        lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
+        B.cutbce_preference_forward(prob, loss, logp, lse, ws)
+    return loss, logp, lse
+
+
+def preference_backward(H, E, ids, lse, offsets=None, ref_logp=None, mask=None, beta: float = 0.1,
+                        reduction: str = "mean", grad_loss=None, want_dH: bool = True, want_dE: bool = True,
+                        grad_dtype: torch.dtype = torch.float32, dE_out=None, accumulate_dE: bool = False,
+                        workspace: Optional[torch.Tensor] = None):
+    """(dH, dE) given the lse of preference_forward on the same inputs."""
+    with _on(H):
+        prob, keep = _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction)
+        dH, dE, opts = _grad_outputs(H, E, want_dH, want_dE, grad_dtype, dE_out, accumulate_dE)
+        ws = _workspace(B.cutbce_preference_workspace_size(prob, _bits(dH, dE)), H.device, workspace)
+        g = _scalar_grad(grad_loss)
+        B.cutbce_preference_backward(prob, opts, _lse_rows(lse, H), g, dH, dE, ws)
+    return dH, dE
+
+
+def preference_forward_backward(H, E, ids, offsets=None, ref_logp=None, mask=None, beta: float = 0.1,
+                                reduction: str = "mean", grad_loss=None, want_dH: bool = True, want_dE: bool = True,
+                                grad_dtype: torch.dtype = torch.float32, dE_out=None, accumulate_dE: bool = False,
+                                workspace: Optional[torch.Tensor] = None):
+    """(loss, logp, lse, dH, dE) in one call; None for a gradient that is not wanted."""
+    with _on(H):
+        prob, keep = _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction)
+        dH, dE, opts = _grad_outputs(H, E, want_dH, want_dE, grad_dtype, dE_out, accumulate_dE)
+        ws = _workspace(B.cutbce_preference_workspace_size(prob, B.OUT_LOSS | _bits(dH, dE)), H.device, workspace)
+        loss = torch.empty((), dtype=torch.float64, device=H.device)
+        logp = torch.empty(2 * prob.P, dtype=torch.float32, device=H.device)
+        lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
+        g = _scalar_grad(grad_loss)
+        B.cutbce_preference_forward_backward(prob, opts, g, loss, logp, lse, dH, dE, ws)
+    return loss, logp, lse, dH, dE
+
+
+def _no_grad_for(**tensors):
+    for name, t in tensors.items():
+        if t is not None and t.requires_grad:
+            raise ValueError(f"{name} gets no gradient: detach it")
+
+
+class _Distill(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, H, E, ids, logits, mask, weights, temperature, reduction):
+        loss, lse = distill_forward(H, E, ids, logits, mask, weights, temperature, reduction)
+        ctx.save_for_backward(H, E, ids, logits, mask, weights, lse)
+        ctx.args = temperature, reduction
+        return loss.to(torch.float32)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        H, E, ids, logits, mask, weights, lse = ctx.saved_tensors
+        dH, dE = distill_backward(H, E, ids, logits, lse, mask, weights, *ctx.args, grad_loss=grad,
+                                  want_dH=ctx.needs_input_grad[0], want_dE=ctx.needs_input_grad[1], grad_dtype=H.dtype)
+        return dH, dE, None, None, None, None, None, None
+
+
+def distill_loss(H, E, teacher_ids, teacher_logits, mask=None, weights=None, temperature: float = 1.0,
+                 reduction: str = "mean") -> torch.Tensor:
+    """Differentiable distillation loss (float32); gradients with respect to H and E, in bf16."""
+    _no_grad_for(teacher_logits=teacher_logits, weights=weights)
+    return _Distill.apply(H, E, teacher_ids, teacher_logits, mask, weights, float(temperature), reduction)
+
+
+class _Preference(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, H, E, ids, offsets, ref_logp, mask, beta, reduction):
+        loss, logp, lse = preference_forward(H, E, ids, offsets, ref_logp, mask, beta, reduction)
+        ctx.save_for_backward(H, E, ids, offsets, ref_logp, mask, lse)
+        ctx.args = beta, reduction
+        ctx.mark_non_differentiable(logp)
+        return loss.to(torch.float32), logp
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad, _):
+        H, E, ids, offsets, ref_logp, mask, lse = ctx.saved_tensors
+        dH, dE = preference_backward(H, E, ids, lse, offsets, ref_logp, mask, *ctx.args, grad_loss=grad,
+                                     want_dH=ctx.needs_input_grad[0], want_dE=ctx.needs_input_grad[1],
+                                     grad_dtype=H.dtype)
+        return dH, dE, None, None, None, None, None, None
+
+
+def preference_loss(H, E, ids, offsets=None, ref_logp=None, mask=None, beta: float = 0.1, reduction: str = "mean"):
+    """Differentiable preference loss (float32) and the sequences' log-probabilities (float32 [2P],
+    not differentiable); gradients with respect to H and E, in bf16."""
+    _no_grad_for(ref_logp=ref_logp)
+    return _Preference.apply(H, E, ids, offsets, ref_logp, mask, float(beta), reduction)

@@ -25,6 +25,11 @@ __all__ = [
     "cutbce_read_counts", "cutbce_kernel_launches", "cutbce_status_string",
     "cutbce_selftest_wait_timeout", "cutbce_selftest_element_math", "cutbce_topk_workspace_size", "cutbce_topk",
     "cutbce_hit_at_k", "cutbce_profile_enable", "cutbce_profile_read", "REDUCTIONS",
+    "cutbce_grad_options", "cutbce_distill_problem", "cutbce_preference_problem", "make_distill_problem",
+    "make_preference_problem", "cutbce_embed_forward", "cutbce_embed_workspace_size", "cutbce_embed_backward",
+    "cutbce_distill_workspace_size", "cutbce_distill_forward", "cutbce_distill_backward",
+    "cutbce_distill_forward_backward", "cutbce_preference_workspace_size", "cutbce_preference_forward",
+    "cutbce_preference_backward", "cutbce_preference_forward_backward",
     "KERNEL_KINDS", "cutbce_probe_scratch_bytes", "cutbce_probe_pipe_rate", "PROBES", "cutbce_probe_mma",
 ]
 
@@ -52,6 +57,28 @@ class cutbce_problem(ctypes.Structure):
 class cutbce_options(ctypes.Structure):
     _fields_ = [("metrics", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("grad_dtype", ctypes.c_int32),
                 ("accumulate", ctypes.c_int32), ("vocab_offset", ctypes.c_int64), ("V_total", ctypes.c_int64)]
+
+
+class cutbce_grad_options(ctypes.Structure):
+    _fields_ = [("grad_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+
+
+class cutbce_distill_problem(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64), ("V", ctypes.c_int64), ("D", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("reduction", ctypes.c_int32),
+        ("H", ctypes.c_void_p), ("E", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("logits", ctypes.c_void_p),
+        ("mask", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("temperature", ctypes.c_float),
+    ]
+
+
+class cutbce_preference_problem(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64), ("V", ctypes.c_int64), ("D", ctypes.c_int64), ("P", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("reduction", ctypes.c_int32),
+        ("H", ctypes.c_void_p), ("E", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+        ("ref_logp", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("beta", ctypes.c_float),
+    ]
 
 
 GRAD_F32, GRAD_BF16 = 0, 1
@@ -106,13 +133,25 @@ _SIGS = {
     "cutbce_profile_read": (_i32, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i64), ctypes.c_int]),
     "cutbce_probe_scratch_bytes": (_sz, []),
     "cutbce_probe_pipe_rate": (_i32, [ctypes.c_int, _vp, _sz, ctypes.POINTER(ctypes.c_double), _vp]),
+    "cutbce_embed_forward": (_i32, [_vp, _i64, _i64, _i32, _vp, _i64, ctypes.c_float, _vp, _vp, _vp]),
+    "cutbce_embed_workspace_size": (_i32, [_i64, _i64, _i64, ctypes.POINTER(_sz)]),
+    "cutbce_embed_backward": (_i32, [_vp, _i32, _vp, _i64, _i64, _i64, ctypes.c_float, _vp, _i32, _i32, _vp, _sz, _vp]),
+    "cutbce_distill_workspace_size": (_i32, [_vp, ctypes.c_int, ctypes.POINTER(_sz)]),
+    "cutbce_distill_forward": (_i32, [_vp, _vp, _vp, _vp, _sz, _vp]),
+    "cutbce_distill_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "cutbce_distill_forward_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "cutbce_preference_workspace_size": (_i32, [_vp, ctypes.c_int, ctypes.POINTER(_sz)]),
+    "cutbce_preference_forward": (_i32, [_vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "cutbce_preference_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "cutbce_preference_forward_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "cutbce_probe_mma": (_i32, [ctypes.c_int, ctypes.c_int, _i64, _vp, _sz, ctypes.POINTER(ctypes.c_double),
                                 ctypes.POINTER(ctypes.c_double), _vp]),
 }
 PROBES = ["ffma", "ffma2", "ex2", "rcp", "tanh", "lg2", "cvt_bf16x2", "fmax", "add2", "iadd", "prmt",
           "ex2_f16x2", "ex2_bf16x2", "tanh_f16x2", "hfma2", "cvt_f16x2", "ffma_sat", "select", "lop", "fmul2"]
 KERNEL_KINDS = ["prep_rows", "prep_scan", "prep_gather", "csc_offsets", "item_pass", "position_pass", "finish",
-                "pair_sort", "topk", "topk_merge", "col_sums"]
+                "pair_sort", "topk", "topk_merge", "col_sums", "embed", "id_sort", "segment_sum", "head_prep",
+                "head_lse_pass", "head_row_pass", "head_item_pass", "head_finish"]
 
 
 def load_library() -> ctypes.CDLL:
@@ -316,6 +355,193 @@ def cutbce_hit_at_k(ids: torch.Tensor, targets: torch.Tensor, stream=None) -> to
     _check(load_library().cutbce_hit_at_k(ids.data_ptr(), B, int(k), targets.data_ptr(), targets.shape[1],
                                           hits.data_ptr(), _stream(stream)), "cutbce_hit_at_k")
     return hits
+
+
+# ---------------------------------------------------------------- item rows
+_DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
+_GRADS = {torch.float32: GRAD_F32, torch.bfloat16: GRAD_BF16}
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _dense(t: Optional[torch.Tensor], name: str, dtypes, shape=None) -> None:
+    """Raises unless t is None or a contiguous tensor of one of `dtypes` (and of `shape`)."""
+    if t is None:
+        return
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _same_device(*tensors: Optional[torch.Tensor]) -> None:
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) > 1:
+        raise ValueError(f"all tensors must be on one device, not {sorted(map(str, devices))}")
+
+
+def cutbce_embed_forward(E: torch.Tensor, ids: torch.Tensor, X: torch.Tensor, scale: float = 1.0,
+                         status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """X[n] = scale * E[ids[n]] (E [V, D], X [N, D] bf16 or fp32, ids int32 [N], -1 empty)."""
+    _dense(E, "E", tuple(_DTYPES))
+    _dense(ids, "ids", (torch.int32,))
+    _dense(X, "X", (E.dtype,), (ids.numel(), E.shape[1]))
+    _dense(status, "status", (torch.int32,))
+    _same_device(E, ids, X, status)
+    _check(load_library().cutbce_embed_forward(E.data_ptr(), E.shape[0], E.shape[1], _DTYPES[E.dtype], ids.data_ptr(),
+                                               ids.numel(), float(scale), X.data_ptr(), _ptr(status),
+                                               _stream(stream)), "cutbce_embed_forward")
+
+
+def cutbce_embed_workspace_size(N: int, V: int, D: int) -> int:
+    n = _sz(0)
+    _check(load_library().cutbce_embed_workspace_size(int(N), int(V), int(D), ctypes.byref(n)),
+           "cutbce_embed_workspace_size")
+    return int(n.value)
+
+
+def cutbce_embed_backward(dX: torch.Tensor, ids: torch.Tensor, dE: torch.Tensor, ws: torch.Tensor, scale: float = 1.0,
+                          accumulate: bool = False, stream=None) -> None:
+    """dE[v] (+)= scale * sum of dX[n] over ids[n] = v (dX [N, D], dE [V, D] bf16 or fp32)."""
+    _dense(dX, "dX", tuple(_DTYPES))
+    _dense(ids, "ids", (torch.int32,))
+    _dense(dE, "dE", tuple(_GRADS))
+    if dX.dim() != 2 or dE.dim() != 2 or dX.shape[0] != ids.numel() or dX.shape[1] != dE.shape[1]:
+        raise ValueError("dX [N, D], ids [N] and dE [V, D] do not fit")
+    _same_device(dX, ids, dE, ws)
+    _check(load_library().cutbce_embed_backward(
+        dX.data_ptr(), _DTYPES[dX.dtype], ids.data_ptr(), ids.numel(), dE.shape[0], dE.shape[1], float(scale),
+        dE.data_ptr(), _GRADS[dE.dtype], 1 if accumulate else 0, ws.data_ptr(), ws.numel(), _stream(stream)),
+        "cutbce_embed_backward")
+
+
+# ---------------------------------------------------------------- softmax losses
+_HEAD_REDUCTIONS = {"mean": 0, "sum": 1}
+
+
+def _head_tensors(H, E, ids, mask):
+    if H.dim() != 2 or E.dim() != 2 or H.shape[1] != E.shape[1]:
+        raise ValueError("H [T, D] and E [V, D] do not fit")
+    _dense(H, "H", (torch.bfloat16,))
+    _dense(E, "E", (torch.bfloat16,))
+    _dense(ids, "ids", (torch.int32,))
+    _dense(mask, "mask", (torch.uint8, torch.bool), (H.shape[0],))
+
+
+def _head_reduction(reduction) -> int:
+    if reduction not in _HEAD_REDUCTIONS:
+        raise ValueError("reduction must be 'mean' or 'sum'")
+    return _HEAD_REDUCTIONS[reduction]
+
+
+def make_distill_problem(H: torch.Tensor, E: torch.Tensor, ids: torch.Tensor, logits: torch.Tensor,
+                         mask: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None,
+                         temperature: float = 1.0, reduction: str = "mean") -> cutbce_distill_problem:
+    """H [T, D], E [V, D] bf16; teacher ids int32 [T, K] and logits float32 [T, K]; mask [T]; weights float32 [T]."""
+    _head_tensors(H, E, ids, mask)
+    if ids.dim() != 2 or ids.shape[0] != H.shape[0]:
+        raise ValueError("ids must be [T, K]")
+    _dense(logits, "logits", (torch.float32,), ids.shape)
+    _dense(weights, "weights", (torch.float32,), (H.shape[0],))
+    _same_device(H, E, ids, logits, mask, weights)
+    return cutbce_distill_problem(H.shape[0], E.shape[0], H.shape[1], ids.shape[1], BF16, _head_reduction(reduction),
+                                  H.data_ptr(), E.data_ptr(), ids.data_ptr(), logits.data_ptr(), _ptr(mask),
+                                  _ptr(weights), float(temperature))
+
+
+def make_preference_problem(H: torch.Tensor, E: torch.Tensor, ids: torch.Tensor, offsets: torch.Tensor,
+                            ref_logp: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                            beta: float = 0.1, reduction: str = "mean") -> cutbce_preference_problem:
+    """H [T, D], E [V, D] bf16; ids int32 [T]; offsets int32 [2P + 1]; ref_logp float32 [2P]; mask [T]."""
+    _head_tensors(H, E, ids, mask)
+    if ids.numel() != H.shape[0]:
+        raise ValueError("ids must be [T]")
+    _dense(offsets, "offsets", (torch.int32,))
+    if offsets.dim() != 1 or offsets.numel() < 3 or offsets.numel() % 2 == 0:
+        raise ValueError("offsets must be [2P + 1] with P >= 1")
+    P = (offsets.numel() - 1) // 2
+    _dense(ref_logp, "ref_logp", (torch.float32,), (2 * P,))
+    _same_device(H, E, ids, offsets, ref_logp, mask)
+    return cutbce_preference_problem(H.shape[0], E.shape[0], H.shape[1], P, BF16, _head_reduction(reduction),
+                                     H.data_ptr(), E.data_ptr(), ids.data_ptr(), offsets.data_ptr(), _ptr(ref_logp),
+                                     _ptr(mask), float(beta))
+
+
+def make_grad_options(dH: Optional[torch.Tensor], dE: Optional[torch.Tensor], accumulate: int = 0) -> cutbce_grad_options:
+    """Options for these output tensors (both fp32 or both bf16)."""
+    kinds = {t.dtype for t in (dH, dE) if t is not None}
+    if len(kinds) != 1 or not kinds <= set(_GRADS):
+        raise ValueError("dH and dE must both be float32 or both bfloat16")
+    for t in (dH, dE):
+        if t is not None and not t.is_contiguous():
+            raise ValueError("dH and dE must be contiguous")
+    return cutbce_grad_options(_GRADS[kinds.pop()], int(accumulate))
+
+
+def _head_size(fn: str, prob, outputs: int) -> int:
+    n = _sz(0)
+    _check(getattr(load_library(), fn)(ctypes.byref(prob), int(outputs), ctypes.byref(n)), fn)
+    return int(n.value)
+
+
+def cutbce_distill_workspace_size(prob: cutbce_distill_problem, outputs: int) -> int:
+    return _head_size("cutbce_distill_workspace_size", prob, outputs)
+
+
+def cutbce_preference_workspace_size(prob: cutbce_preference_problem, outputs: int) -> int:
+    return _head_size("cutbce_preference_workspace_size", prob, outputs)
+
+
+def cutbce_distill_forward(prob, loss: Optional[torch.Tensor], lse: Optional[torch.Tensor], ws: torch.Tensor,
+                           stream=None) -> None:
+    _check(load_library().cutbce_distill_forward(ctypes.byref(prob), _ptr(loss), _ptr(lse), ws.data_ptr(), ws.numel(),
+                                                 _stream(stream)), "cutbce_distill_forward")
+
+
+def cutbce_distill_backward(prob, opts: Optional[cutbce_grad_options], lse: torch.Tensor,
+                            grad_loss: Optional[torch.Tensor], dH: Optional[torch.Tensor],
+                            dE: Optional[torch.Tensor], ws: torch.Tensor, stream=None) -> None:
+    _check(load_library().cutbce_distill_backward(
+        ctypes.byref(prob), ctypes.byref(opts) if opts is not None else None, _ptr(lse), _ptr(grad_loss), _ptr(dH),
+        _ptr(dE), ws.data_ptr(), ws.numel(), _stream(stream)), "cutbce_distill_backward")
+
+
+def cutbce_distill_forward_backward(prob, opts: Optional[cutbce_grad_options], grad_loss: Optional[torch.Tensor],
+                                    loss: Optional[torch.Tensor], lse: Optional[torch.Tensor],
+                                    dH: Optional[torch.Tensor], dE: Optional[torch.Tensor], ws: torch.Tensor,
+                                    stream=None) -> None:
+    _check(load_library().cutbce_distill_forward_backward(
+        ctypes.byref(prob), ctypes.byref(opts) if opts is not None else None, _ptr(grad_loss), _ptr(loss), _ptr(lse),
+        _ptr(dH), _ptr(dE), ws.data_ptr(), ws.numel(), _stream(stream)), "cutbce_distill_forward_backward")
+
+
+def cutbce_preference_forward(prob, loss: Optional[torch.Tensor], logp: Optional[torch.Tensor],
+                              lse: Optional[torch.Tensor], ws: torch.Tensor, stream=None) -> None:
+    _check(load_library().cutbce_preference_forward(ctypes.byref(prob), _ptr(loss), _ptr(logp), _ptr(lse),
+                                                    ws.data_ptr(), ws.numel(), _stream(stream)),
+           "cutbce_preference_forward")
+
+
+def cutbce_preference_backward(prob, opts: Optional[cutbce_grad_options], lse: torch.Tensor,
+                               grad_loss: Optional[torch.Tensor], dH: Optional[torch.Tensor],
+                               dE: Optional[torch.Tensor], ws: torch.Tensor, stream=None) -> None:
+    _check(load_library().cutbce_preference_backward(
+        ctypes.byref(prob), ctypes.byref(opts) if opts is not None else None, _ptr(lse), _ptr(grad_loss), _ptr(dH),
+        _ptr(dE), ws.data_ptr(), ws.numel(), _stream(stream)), "cutbce_preference_backward")
+
+
+def cutbce_preference_forward_backward(prob, opts: Optional[cutbce_grad_options], grad_loss: Optional[torch.Tensor],
+                                       loss: Optional[torch.Tensor], logp: Optional[torch.Tensor],
+                                       lse: Optional[torch.Tensor], dH: Optional[torch.Tensor],
+                                       dE: Optional[torch.Tensor], ws: torch.Tensor, stream=None) -> None:
+    _check(load_library().cutbce_preference_forward_backward(
+        ctypes.byref(prob), ctypes.byref(opts) if opts is not None else None, _ptr(grad_loss), _ptr(loss), _ptr(logp),
+        _ptr(lse), _ptr(dH), _ptr(dE), ws.data_ptr(), ws.numel(), _stream(stream)),
+        "cutbce_preference_forward_backward")
 
 
 def cutbce_profile_enable(enable: bool) -> None:

@@ -13,9 +13,10 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libcutbce.so")
-SOURCES = ["cutbce_api.cu"]
+SOURCES = ["cutbce_api.cu", "cutbce_heads.cu"]
 DEPS = ["cutbce_api.cu", "common.cuh", "prep_finish.cuh", "pair_sort.cuh", "tile_engine.cuh", "ptx_sm100.cuh", "probes.cuh",
-        "elementwise.cuh", "topk.cuh", "wait.cuh", "host_util.cuh"]
+        "elementwise.cuh", "topk.cuh", "wait.cuh", "host_util.cuh",
+        "cutbce_heads.cu", "id_sort.cuh", "embed.cuh", "softmax_head.cuh", "softmax_engine.cuh"]
 
 
 def nvcc_path() -> str:
@@ -25,7 +26,7 @@ def nvcc_path() -> str:
 
 def command(out: str = LIB, extra: list[str] | None = None) -> list[str]:
     return [nvcc_path(), "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
-            "-Xcompiler", "-fPIC,-O3", "-shared", "-cudart", "static", f"-I{INCLUDE}", f"-I{CSRC}",
+            "-Xcompiler", "-fPIC,-O3", "-shared", "-cudart", "static", "--threads", "0", f"-I{INCLUDE}", f"-I{CSRC}",
             "-o", out] + [os.path.join(CSRC, s) for s in SOURCES] + (extra or [])
 
 

@@ -19,6 +19,7 @@ enum : int { kMeanValidPositions = 0, kSum = 1, kMeanElements = 2 };
 
 constexpr int kMaxK = 128;            // target slots per position
 constexpr int kMaxDim = 256;          // feature width
+constexpr int kMaxEmbedDim = 16384;   // row width of the lookup
 constexpr int kTileM = 128;           // stationary rows per tile = TMEM lanes
 constexpr int kMaxCtas = 256;         // upper bound of a persistent grid
 constexpr int kMaxSplits = 64;        // dH partial splits over the vocabulary

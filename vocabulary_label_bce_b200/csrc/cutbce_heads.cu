@@ -1,0 +1,633 @@
+// Host side of the item-table operators: row lookup and its gradient, and the
+// softmax losses over the whole table (distillation, preference).  Argument
+// checks, workspace layouts and launch sequences; no device memory is allocated.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include "cutbce.h"
+#include "common.cuh"
+#include "host_util.cuh"
+#include "id_sort.cuh"
+#include "embed.cuh"
+#include "softmax_head.cuh"
+#include "softmax_engine.cuh"
+
+namespace {
+using namespace cutbce;
+
+#define CUTBCE_CK(x)                                \
+  do {                                              \
+    if ((x) != cudaSuccess) return CUTBCE_ERR_CUDA; \
+  } while (0)
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Offsets of a workspace, 256-byte aligned pieces in order.
+struct Layout {
+  size_t total = 0;
+  size_t take(size_t bytes) {
+    const size_t at = total;
+    total = align256(total + bytes);
+    return at;
+  }
+};
+
+cutbce_status check_device() {
+  DeviceFacts dev;
+  const cutbce_status s = device_facts(dev);
+  if (s != CUTBCE_OK) return s;
+  return dev.major == 10 && dev.minor == 0 ? CUTBCE_OK : CUTBCE_ERR_UNSUPPORTED;
+}
+
+// ---------------------------------------------------------------- sort and segment sums
+constexpr int64_t kMaxSortEntries = int64_t(1) << 28;
+
+// Buffers of the sort and of the sums over N entries.
+struct SortBuffers {
+  SortPlan sp;
+  int64_t chunks;
+  size_t o_hist, o_total, o_k[2], o_v[2], o_part;
+};
+
+void plan_sort(int64_t N, int64_t V, int64_t D, SortBuffers& b, Layout& l) {
+  make_sort_plan(N, V, b.sp);
+  b.chunks = ceil_div(N, kSumChunk);
+  b.o_hist = l.take(b.sp.hist_bytes);                 // right after the header: one memset clears both
+  b.o_total = l.take(sizeof(int) * (size_t(1) << b.sp.bits));
+  for (int i = 0; i < 2; ++i) {
+    b.o_k[i] = l.take(4 * static_cast<size_t>(N));
+    b.o_v[i] = l.take(4 * static_cast<size_t>(N));
+  }
+  b.o_part = l.take(4 * 2 * static_cast<size_t>(b.chunks) * D);
+}
+
+// Sorts the entries by id; the sorted keys and entry indices end in *keys, *vals.
+template <int IPT>
+cutbce_status run_sort_ipt(const SortBuffers& b, const int32_t* ids, int V, void* ws, int* status, cudaStream_t st,
+                           const int** keys, const int** vals) {
+  const SortPlan& sp = b.sp;
+  const size_t pass_hist = static_cast<size_t>(sp.nblk) << sp.bits;
+  int* hist = at<int>(ws, b.o_hist);
+  int* total = at<int>(ws, b.o_total);
+  k_sort_keys<IPT><<<sp.nblk, kSortThreads, 0, st>>>(ids, sp.N, V, sp.bits, hist, status);
+  const int* kin = ids;
+  const int* vin = nullptr;
+  for (int p = 0; p < sp.passes; ++p) {
+    int* h = hist + p * pass_hist;
+    int* next = p + 1 < sp.passes ? h + pass_hist : nullptr;
+    if (sp.scan) k_sort_scan<<<static_cast<unsigned>(ceil_div(1 << sp.bits, 128)), 128, 0, st>>>(h, total, 1 << sp.bits, sp.nblk);
+    int* ko = at<int>(ws, b.o_k[p & 1]);
+    int* vo = at<int>(ws, b.o_v[p & 1]);
+    k_sort_scatter<IPT><<<sp.nblk, kSortThreads, 0, st>>>(kin, vin, sp.N, V, p * sp.bits, sp.bits, sp.nblk, h,
+                                                          sp.scan ? total : nullptr, ko, vo, next, status);
+    kin = ko;
+    vin = vo;
+  }
+  *keys = kin;
+  *vals = vin;
+  return cudaGetLastError() == cudaSuccess ? CUTBCE_OK : CUTBCE_ERR_CUDA;
+}
+
+cutbce_status run_sort(const SortBuffers& b, const int32_t* ids, int V, void* ws, int* status, cudaStream_t st,
+                       const int** keys, const int** vals) {
+  LaunchScope ls(CUTBCE_KERNEL_ID_SORT, st);
+  if (b.sp.ipt == 4) return run_sort_ipt<4>(b, ids, V, ws, status, st, keys, vals);
+  if (b.sp.ipt == 16) return run_sort_ipt<16>(b, ids, V, ws, status, st, keys, vals);
+  return run_sort_ipt<64>(b, ids, V, ws, status, st, keys, vals);
+}
+
+template <int VEC, typename TIn, typename TOut>
+cutbce_status run_sums_t(const SegmentParams& p, int64_t chunks, cudaStream_t st) {
+  // lanes per chunk: the row's pieces, rounded up to a power of two; wider rows take several slices
+  const int pieces = static_cast<int>(ceil_div(p.D, VEC));
+  int lanes = 1;
+  while (lanes < pieces && lanes < 32) lanes <<= 1;
+  const int slices = static_cast<int>(ceil_div(pieces, lanes));
+  const int64_t threads = chunks * slices * lanes;
+  const int64_t blocks = ceil_div(threads, 256);
+  if (blocks >= (int64_t(1) << 31)) return CUTBCE_ERR_UNSUPPORTED;
+  LaunchScope ls(CUTBCE_KERNEL_SEGMENT_SUM, st);
+  k_segment_sum<VEC, TIn, TOut><<<static_cast<unsigned>(blocks), 256, 0, st>>>(p, lanes, slices);
+  if (chunks > 1) k_segment_join<VEC == 8 ? 4 : VEC, TOut><<<static_cast<unsigned>(chunks - 1), 256, 0, st>>>(p, chunks);
+  return cudaGetLastError() == cudaSuccess ? CUTBCE_OK : CUTBCE_ERR_CUDA;
+}
+
+template <typename TIn, typename TOut>
+cutbce_status run_sums_vec(const SegmentParams& p, int64_t chunks, cudaStream_t st) {
+  constexpr int VEC = 16 / sizeof(TIn);
+  if (p.D % VEC == 0 && aligned(p.src, 16)) return run_sums_t<VEC, TIn, TOut>(p, chunks, st);
+  return run_sums_t<1, TIn, TOut>(p, chunks, st);
+}
+
+cutbce_status run_sums(const SegmentParams& p, bool in_bf16, int64_t chunks, cudaStream_t st) {
+  if (p.first != nullptr) return run_sums_vec<__nv_bfloat16, float>(p, chunks, st);
+  if (in_bf16) {
+    return p.out_bf16 ? run_sums_vec<__nv_bfloat16, __nv_bfloat16>(p, chunks, st)
+                      : run_sums_vec<__nv_bfloat16, float>(p, chunks, st);
+  }
+  return p.out_bf16 ? run_sums_vec<float, __nv_bfloat16>(p, chunks, st) : run_sums_vec<float, float>(p, chunks, st);
+}
+
+// ---------------------------------------------------------------- row lookup
+cutbce_status check_embed(int64_t N, int64_t V, int64_t D, int32_t dtype) {
+  if (N <= 0 || V <= 0 || D <= 0) return CUTBCE_ERR_INVALID_ARG;
+  if (dtype != CUTBCE_BF16 && dtype != CUTBCE_F32) return CUTBCE_ERR_UNSUPPORTED;
+  if (V >= (int64_t(1) << 31) - 1 || D > kMaxEmbedDim || N >= kMaxSortEntries) return CUTBCE_ERR_UNSUPPORTED;
+  return CUTBCE_OK;
+}
+
+struct EmbedPlan {
+  size_t o_hdr;
+  SortBuffers sort;
+  size_t total;
+};
+
+void plan_embed(int64_t N, int64_t V, int64_t D, EmbedPlan& pl) {
+  Layout l;
+  pl.o_hdr = l.take(256);
+  plan_sort(N, V, D, pl.sort, l);
+  pl.total = l.total;
+}
+
+template <int VEC, typename T>
+cutbce_status launch_embed(const void* E, int64_t V, const int32_t* ids, int64_t N, int64_t D, float scale, void* X,
+                           int32_t* status, cudaStream_t st) {
+  const int64_t blocks = ceil_div(N * (D / VEC), 256);
+  if (blocks >= (int64_t(1) << 31)) return CUTBCE_ERR_UNSUPPORTED;
+  LaunchScope ls(CUTBCE_KERNEL_EMBED, st);
+  k_embed<VEC, T><<<static_cast<unsigned>(blocks), 256, 0, st>>>(static_cast<const T*>(E), V, ids, N,
+                                                                 static_cast<int>(D), scale, static_cast<T*>(X), status);
+  return cudaGetLastError() == cudaSuccess ? CUTBCE_OK : CUTBCE_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- softmax heads
+struct HeadProblem {
+  int kind;
+  int64_t T, V, D, K, P;
+  int32_t dtype, reduction;
+  const void *H, *E;
+  const int32_t* ids;
+  const float* logits;
+  const int32_t* offsets;
+  const float* ref;
+  const uint8_t* mask;
+  const float* weights;
+  float tau, beta;
+};
+
+HeadProblem head_problem(const cutbce_distill_problem* p) {
+  return HeadProblem{kHeadDistill, p->T, p->V, p->D, p->K, 0, p->dtype, p->reduction, p->H, p->E, p->ids, p->logits,
+                     nullptr, nullptr, p->mask, p->weights, p->temperature, 1.f};
+}
+HeadProblem head_problem(const cutbce_preference_problem* p) {
+  return HeadProblem{kHeadPreference, p->T, p->V, p->D, 1, p->P, p->dtype, p->reduction, p->H, p->E, p->ids, nullptr,
+                     p->offsets, p->ref_logp, p->mask, nullptr, 1.f, p->beta};
+}
+
+cutbce_status check_head(const HeadProblem& p, bool need_data) {
+  if (p.T <= 0 || p.V <= 0 || p.D <= 0 || p.K <= 0) return CUTBCE_ERR_INVALID_ARG;
+  if (p.dtype != CUTBCE_BF16) return CUTBCE_ERR_UNSUPPORTED;
+  if (p.reduction != CUTBCE_MEAN_VALID_POSITIONS && p.reduction != CUTBCE_SUM) return CUTBCE_ERR_INVALID_ARG;
+  if (p.K > kMaxK || p.D > kMaxDim || p.D % 8 != 0) return CUTBCE_ERR_UNSUPPORTED;
+  if (p.V >= (int64_t(1) << 31) - 1 || p.T >= (int64_t(1) << 24) - 255 || p.T * p.K >= kMaxSortEntries)
+    return CUTBCE_ERR_UNSUPPORTED;
+  if (p.kind == kHeadDistill) {
+    const float c = kLog2eF / p.tau;
+    if (!(p.tau > 0.f) || !std::isfinite(c) || !std::isfinite(p.tau * p.tau)) return CUTBCE_ERR_INVALID_ARG;
+  } else {
+    if (p.P <= 0 || !std::isfinite(p.beta)) return CUTBCE_ERR_INVALID_ARG;
+    if (p.P >= (int64_t(1) << 30)) return CUTBCE_ERR_UNSUPPORTED;
+  }
+  if (need_data) {
+    if (p.H == nullptr || p.E == nullptr || p.ids == nullptr) return CUTBCE_ERR_INVALID_ARG;
+    if (p.kind == kHeadDistill ? p.logits == nullptr : p.offsets == nullptr) return CUTBCE_ERR_INVALID_ARG;
+    if (!aligned(p.H, 16) || !aligned(p.E, 16) || !aligned(p.ids, 4) || !aligned(p.logits, 4) ||
+        !aligned(p.offsets, 4) || !aligned(p.ref, 4) || !aligned(p.weights, 4))
+      return CUTBCE_ERR_INVALID_ARG;
+  }
+  return CUTBCE_OK;
+}
+
+constexpr int kMaxHeadSplits = 148;
+
+struct HeadPlan {
+  int DP, BN, S, tps, n_vtiles, n_blk;
+  int64_t Tc;
+  size_t o_hdr, o_blk, o_cls, o_cidx, o_orig, o_coef, o_b2, o_lse2, o_term, o_hc, o_lpart, o_part, o_sparse, o_dhpart,
+      o_keys, o_share, o_usum, o_first, total;
+  SortBuffers sort;
+  size_t clear_bytes;            // header and histograms
+};
+
+// dH partials per position: about 16 work items per SM, at most kMaxSplits splits;
+// with few position tiles enough splits for one work item per SM.
+void plan_head(const HeadProblem& p, bool dH, bool dE, bool lse_pass, HeadPlan& pl) {
+  pl.DP = static_cast<int>(round_up(p.D, 64));
+  pl.BN = pl.DP > 128 ? 64 : 128;
+  pl.n_vtiles = static_cast<int>(ceil_div(p.V, pl.BN));
+  pl.n_blk = static_cast<int>(ceil_div(p.T, 256));
+  pl.Tc = round_up(p.T, kTileM) + kTileM;
+  const int64_t nT = ceil_div(p.T, kTileM);
+  int64_t s0 = std::max<int64_t>(std::min<int64_t>(ceil_div(16 * 148, nT), kMaxSplits),
+                                 std::min<int64_t>(ceil_div(148, nT), kMaxHeadSplits));
+  s0 = std::max<int64_t>(1, std::min<int64_t>(s0, pl.n_vtiles));
+  pl.tps = static_cast<int>(ceil_div(pl.n_vtiles, s0));
+  pl.S = static_cast<int>(ceil_div(pl.n_vtiles, pl.tps));
+  const size_t T = static_cast<size_t>(p.T), Tc = static_cast<size_t>(pl.Tc), TK = T * p.K;
+  Layout l;
+  pl.o_hdr = l.take(256);
+  pl.sort = SortBuffers{};
+  if (dE) plan_sort(p.T * p.K, p.V, p.D, pl.sort, l);
+  pl.clear_bytes = dE ? pl.sort.o_hist + pl.sort.sp.hist_bytes : 256;
+  pl.o_blk = l.take(8 * static_cast<size_t>(pl.n_blk));
+  pl.o_cls = l.take(T);
+  pl.o_cidx = l.take(4 * T);
+  pl.o_orig = l.take(4 * Tc);
+  pl.o_coef = l.take(4 * T);
+  pl.o_b2 = l.take(4 * Tc);
+  pl.o_lse2 = l.take(4 * Tc);
+  pl.o_term = l.take(8 * Tc);
+  pl.o_hc = l.take(2 * Tc * pl.DP);
+  pl.o_lpart = l.take(8 * std::max<size_t>(static_cast<size_t>(p.P), Tc / kLseThreads));
+  pl.o_part = lse_pass ? l.take(8 * static_cast<size_t>(pl.S) * 4 * Tc) : 0;
+  pl.o_sparse = dH ? l.take(4 * Tc * pl.DP) : 0;
+  pl.o_dhpart = dH ? l.take(4 * static_cast<size_t>(pl.S) * Tc * pl.DP) : 0;
+  pl.o_keys = dE ? l.take(4 * TK) : 0;
+  pl.o_share = dE ? l.take(4 * TK) : 0;
+  pl.o_usum = dE ? l.take(4 * TK * p.D) : 0;
+  pl.o_first = dE ? l.take(4 * static_cast<size_t>(p.V)) : 0;
+  pl.total = l.total;
+}
+
+template <int DP, int kPass>
+cudaError_t launch_softmax(int grid, const CUtensorMap& s, const CUtensorMap& x, const SoftmaxParams& sp,
+                           cudaStream_t st) {
+  auto kern = k_softmax<DP, kPass>;
+  constexpr uint32_t smem = SoftmaxCfg<DP, kPass != kPassLse>::SMEM_BYTES;
+  static std::atomic<uint64_t> configured{0};   // the attribute belongs to the current device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  const uint64_t bit = uint64_t(1) << dev;
+  if ((configured.load(std::memory_order_acquire) & bit) == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  kern<<<grid, kTileThreads, smem, st>>>(s, x, sp);
+  return cudaGetLastError();
+}
+
+template <int kPass>
+cudaError_t launch_softmax_dp(int DP, int grid, const CUtensorMap& s, const CUtensorMap& x, const SoftmaxParams& sp,
+                              cudaStream_t st) {
+  switch (DP) {
+    case 64: return launch_softmax<64, kPass>(grid, s, x, sp, st);
+    case 128: return launch_softmax<128, kPass>(grid, s, x, sp, st);
+    case 192: return launch_softmax<192, kPass>(grid, s, x, sp, st);
+    case 256: return launch_softmax<256, kPass>(grid, s, x, sp, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+struct HeadOutputs {
+  double* loss = nullptr;
+  float* lse = nullptr;
+  float* logp = nullptr;
+  void* dH = nullptr;
+  void* dE = nullptr;
+  int grad_dtype = CUTBCE_GRAD_F32, accumulate = 0;
+};
+
+cutbce_status check_grad_options(const cutbce_grad_options* o, HeadOutputs& out) {
+  if (o == nullptr) return CUTBCE_OK;
+  if (o->grad_dtype != CUTBCE_GRAD_F32 && o->grad_dtype != CUTBCE_GRAD_BF16) return CUTBCE_ERR_UNSUPPORTED;
+  if (o->accumulate < 0 || o->accumulate > (CUTBCE_ACCUMULATE_DH | CUTBCE_ACCUMULATE_DE)) return CUTBCE_ERR_INVALID_ARG;
+  out.grad_dtype = o->grad_dtype;
+  out.accumulate = o->accumulate;
+  return CUTBCE_OK;
+}
+
+// lse_in: the log-sum-exps of an earlier forward on the same inputs, or null (then
+// they are computed first).
+cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* grad_loss, const HeadOutputs& out,
+                       void* ws, size_t ws_bytes, cudaStream_t st) {
+  cutbce_status s = check_head(p, true);
+  if (s != CUTBCE_OK) return s;
+  const bool dH = out.dH != nullptr, dE = out.dE != nullptr;
+  if (ws == nullptr || !aligned(ws, 256) || !aligned(out.dH, 16) || !aligned(out.dE, 16) || !aligned(out.loss, 8) ||
+      !aligned(out.lse, 4) || !aligned(out.logp, 4) || !aligned(lse_in, 4) || !aligned(grad_loss, 4))
+    return CUTBCE_ERR_INVALID_ARG;
+  HeadPlan pl;
+  plan_head(p, dH, dE, lse_in == nullptr, pl);
+  if (ws_bytes < pl.total) return CUTBCE_ERR_WORKSPACE;
+  if ((s = check_device()) != CUTBCE_OK) return s;
+  DeviceFacts dev;
+  if ((s = device_facts(dev)) != CUTBCE_OK) return s;
+
+  HeadParams hp{};
+  hp.kind = p.kind;
+  hp.T = static_cast<int>(p.T);
+  hp.V = static_cast<int>(p.V);
+  hp.D = static_cast<int>(p.D);
+  hp.DP = pl.DP;
+  hp.K = static_cast<int>(p.K);
+  hp.P = static_cast<int>(p.P);
+  hp.H = static_cast<const __nv_bfloat16*>(p.H);
+  hp.E = static_cast<const __nv_bfloat16*>(p.E);
+  hp.ids = p.ids;
+  hp.logits = p.logits;
+  hp.offsets = p.offsets;
+  hp.ref = p.ref;
+  hp.mask = p.mask;
+  hp.weights = p.weights;
+  hp.tau = p.tau;
+  hp.inv_tau = 1.f / p.tau;
+  hp.beta = p.beta;
+  hp.reduction = p.reduction;
+  hp.grad_loss = grad_loss;
+  hp.hdr = at<HeadHeader>(ws, pl.o_hdr);
+  hp.cls = at<uint8_t>(ws, pl.o_cls);
+  hp.blk = at<int>(ws, pl.o_blk);
+  hp.n_blk = pl.n_blk;
+  hp.cidx = at<int>(ws, pl.o_cidx);
+  hp.orig = at<int>(ws, pl.o_orig);
+  hp.Hc = at<__nv_bfloat16>(ws, pl.o_hc);
+  hp.rowterm = at<double>(ws, pl.o_term);
+  hp.sparse = dH ? at<float>(ws, pl.o_sparse) : nullptr;
+  hp.keys = dE ? at<int>(ws, pl.o_keys) : nullptr;
+  hp.share = dE ? at<float>(ws, pl.o_share) : nullptr;
+  hp.coef = at<float>(ws, pl.o_coef);
+  hp.b2 = at<float>(ws, pl.o_b2);
+  hp.lse2 = at<float>(ws, pl.o_lse2);
+  hp.lse_in = lse_in;
+  hp.part = lse_in == nullptr ? at<float2>(ws, pl.o_part) : nullptr;
+  hp.slots = 4 * pl.S;
+  hp.Tc = pl.Tc;
+  hp.loss_part = at<double>(ws, pl.o_lpart);
+  hp.loss = out.loss;
+  hp.lse_out = out.lse;
+  hp.logp_out = out.logp;
+  int* status = &hp.hdr->w.status;
+
+  CUTBCE_CK(cudaMemsetAsync(hp.hdr, 0, pl.clear_bytes, st));
+  {
+    LaunchScope ls(CUTBCE_KERNEL_HEAD_PREP, st);
+    k_head_rows<<<static_cast<unsigned>(pl.n_blk), 256, 0, st>>>(hp);
+    k_head_gather<<<static_cast<unsigned>(ceil_div(p.T + 256, 8)), 256, 0, st>>>(hp);
+    CUTBCE_CK(cudaGetLastError());
+  }
+  SoftmaxParams sp{};
+  sp.V = hp.V;
+  sp.D = hp.D;
+  sp.Tc = pl.Tc;
+  sp.hdr = hp.hdr;
+  sp.c2 = kLog2eF / p.tau;
+  sp.nsplit = pl.S;
+  sp.tiles_per_split = pl.tps;
+  sp.n_item_tiles_bn = pl.n_vtiles;
+  sp.timeout_ns = kDefaultTimeoutNs;
+  CUtensorMap m_rows_s, m_items_x, m_items_s, m_rows_x;   // stationary / streamed maps of H_c and E
+  if (!make_map(&m_rows_s, hp.Hc, pl.DP, pl.Tc, pl.DP, kTileM) || !make_map(&m_items_x, p.E, p.D, p.V, p.D, pl.BN) ||
+      !make_map(&m_items_s, p.E, p.D, p.V, p.D, kTileM) || !make_map(&m_rows_x, hp.Hc, pl.DP, pl.Tc, pl.DP, pl.BN))
+    return CUTBCE_ERR_CUDA;
+  const int64_t row_items = static_cast<int64_t>(pl.S) * (pl.Tc / kTileM);
+  const int row_grid = static_cast<int>(std::min<int64_t>({static_cast<int64_t>(dev.sms), row_items, static_cast<int64_t>(kMaxCtas)}));
+  if (lse_in == nullptr) {
+    LaunchScope ls(CUTBCE_KERNEL_HEAD_LSE_PASS, st);
+    sp.part = at<float2>(ws, pl.o_part);
+    CUTBCE_CK(launch_softmax_dp<kPassLse>(pl.DP, row_grid, m_rows_s, m_items_x, sp, st));
+  }
+  {
+    LaunchScope ls(CUTBCE_KERNEL_HEAD_FINISH, st);
+    k_head_lse<<<static_cast<unsigned>(pl.Tc / kLseThreads), kLseThreads, 0, st>>>(hp);
+    if (p.kind == kHeadPreference) k_head_pairs<<<static_cast<unsigned>(p.P), kPairThreads, 0, st>>>(hp);
+    CUTBCE_CK(cudaGetLastError());
+  }
+  if (dH) {
+    {
+      LaunchScope ls(CUTBCE_KERNEL_HEAD_ROW_PASS, st);
+      sp.off2 = hp.lse2;
+      sp.dh_part = at<float>(ws, pl.o_dhpart);
+      CUTBCE_CK(launch_softmax_dp<kPassRows>(pl.DP, row_grid, m_rows_s, m_items_x, sp, st));
+    }
+    HeadDhParams dp{};
+    dp.T = hp.T;
+    dp.D = hp.D;
+    dp.DP = pl.DP;
+    dp.S = pl.S;
+    dp.Tc = pl.Tc;
+    dp.cidx = hp.cidx;
+    dp.coef = hp.coef;
+    dp.part = at<float>(ws, pl.o_dhpart);
+    dp.sparse = hp.sparse;
+    dp.dH = out.dH;
+    dp.bf16 = out.grad_dtype == CUTBCE_GRAD_BF16;
+    dp.accumulate = (out.accumulate & CUTBCE_ACCUMULATE_DH) != 0;
+    dp.hdr = hp.hdr;
+    LaunchScope ls(CUTBCE_KERNEL_HEAD_FINISH, st);
+    k_head_dh<<<static_cast<unsigned>(ceil_div(p.T * (p.D / 4), 256)), 256, 0, st>>>(dp);
+    CUTBCE_CK(cudaGetLastError());
+  }
+  if (dE) {
+    // the sparse part of dE: sum of coef q h over the pairs of each item, in fp32
+    SegmentParams gp{};
+    if ((s = run_sort(pl.sort, hp.keys, hp.V, ws, status, st, &gp.keys, &gp.vals)) != CUTBCE_OK) return s;
+    gp.N = p.T * p.K;
+    gp.V = hp.V;
+    gp.D = hp.D;
+    gp.src = p.H;
+    gp.K = hp.K;
+    gp.share = hp.share;
+    gp.row_coef = hp.coef;
+    gp.scale = 1.f;
+    gp.part = at<float>(ws, pl.sort.o_part);
+    gp.out = at<float>(ws, pl.o_usum);
+    gp.first = at<int>(ws, pl.o_first);
+    gp.status = status;
+    CUTBCE_CK(cudaMemsetAsync(gp.first, 0xFF, 4 * static_cast<size_t>(p.V), st));
+    if ((s = run_sums(gp, true, pl.sort.chunks, st)) != CUTBCE_OK) return s;
+    sp.off2 = hp.b2;
+    sp.first = gp.first;
+    sp.sparse = at<float>(ws, pl.o_usum);
+    sp.dE = out.dE;
+    sp.de_bf16 = out.grad_dtype == CUTBCE_GRAD_BF16;
+    sp.de_acc = (out.accumulate & CUTBCE_ACCUMULATE_DE) != 0;
+    const int grid = static_cast<int>(std::min<int64_t>({static_cast<int64_t>(dev.sms), ceil_div(p.V, kTileM), static_cast<int64_t>(kMaxCtas)}));
+    LaunchScope ls(CUTBCE_KERNEL_HEAD_ITEM_PASS, st);
+    CUTBCE_CK(launch_softmax_dp<kPassItems>(pl.DP, grid, m_items_s, m_rows_x, sp, st));
+  }
+  return CUTBCE_OK;
+}
+
+cutbce_status head_workspace(const HeadProblem& p, int outputs, size_t* bytes) {
+  if (bytes == nullptr || outputs <= 0 || outputs > (CUTBCE_OUT_LOSS | CUTBCE_OUT_DH | CUTBCE_OUT_DE))
+    return CUTBCE_ERR_INVALID_ARG;
+  const cutbce_status s = check_head(p, false);
+  if (s != CUTBCE_OK) return s;
+  HeadPlan pl;
+  plan_head(p, (outputs & CUTBCE_OUT_DH) != 0, (outputs & CUTBCE_OUT_DE) != 0, (outputs & CUTBCE_OUT_LOSS) != 0, pl);
+  *bytes = pl.total;
+  return CUTBCE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+cutbce_status cutbce_embed_forward(const void* E, int64_t V, int64_t D, int32_t dtype, const int32_t* ids, int64_t N,
+                                   float scale, void* X, int32_t* status, cutbce_stream_t stream) {
+  cutbce_status s = check_embed(N, V, D, dtype);
+  if (s != CUTBCE_OK) return s;
+  const size_t e = dtype == CUTBCE_BF16 ? 2 : 4;
+  if (E == nullptr || ids == nullptr || X == nullptr || !aligned(E, e) || !aligned(X, e) || !aligned(ids, 4) ||
+      !aligned(status, 4))
+    return CUTBCE_ERR_INVALID_ARG;
+  if ((s = check_device()) != CUTBCE_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool wide = aligned(E, 16) && aligned(X, 16);
+  if (dtype == CUTBCE_BF16) {
+    return wide && D % 8 == 0 ? launch_embed<8, __nv_bfloat16>(E, V, ids, N, D, scale, X, status, st)
+                              : launch_embed<1, __nv_bfloat16>(E, V, ids, N, D, scale, X, status, st);
+  }
+  return wide && D % 4 == 0 ? launch_embed<4, float>(E, V, ids, N, D, scale, X, status, st)
+                            : launch_embed<1, float>(E, V, ids, N, D, scale, X, status, st);
+}
+
+cutbce_status cutbce_embed_workspace_size(int64_t N, int64_t V, int64_t D, size_t* bytes) {
+  if (bytes == nullptr) return CUTBCE_ERR_INVALID_ARG;
+  const cutbce_status s = check_embed(N, V, D, CUTBCE_BF16);
+  if (s != CUTBCE_OK) return s;
+  EmbedPlan pl;
+  plan_embed(N, V, D, pl);
+  *bytes = pl.total;
+  return CUTBCE_OK;
+}
+
+cutbce_status cutbce_embed_backward(const void* dX, int32_t dtype, const int32_t* ids, int64_t N, int64_t V, int64_t D,
+                                    float scale, void* dE, int32_t grad_dtype, int32_t accumulate, void* ws,
+                                    size_t ws_bytes, cutbce_stream_t stream) {
+  cutbce_status s = check_embed(N, V, D, dtype);
+  if (s != CUTBCE_OK) return s;
+  if (grad_dtype != CUTBCE_GRAD_F32 && grad_dtype != CUTBCE_GRAD_BF16) return CUTBCE_ERR_UNSUPPORTED;
+  const size_t ei = dtype == CUTBCE_BF16 ? 2 : 4, eo = grad_dtype == CUTBCE_GRAD_BF16 ? 2 : 4;
+  if (dX == nullptr || ids == nullptr || dE == nullptr || ws == nullptr || !aligned(ws, 256) || !aligned(dX, ei) ||
+      !aligned(dE, eo) || !aligned(ids, 4) || (accumulate != 0 && accumulate != 1))
+    return CUTBCE_ERR_INVALID_ARG;
+  EmbedPlan pl;
+  plan_embed(N, V, D, pl);
+  if (ws_bytes < pl.total) return CUTBCE_ERR_WORKSPACE;
+  if ((s = check_device()) != CUTBCE_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  int* status = at<int>(ws, pl.o_hdr);
+  CUTBCE_CK(cudaMemsetAsync(status, 0, pl.sort.o_hist + pl.sort.sp.hist_bytes, st));
+  if (!accumulate) CUTBCE_CK(cudaMemsetAsync(dE, 0, eo * static_cast<size_t>(V) * D, st));
+  SegmentParams p{};
+  if ((s = run_sort(pl.sort, ids, static_cast<int>(V), ws, status, st, &p.keys, &p.vals)) != CUTBCE_OK) return s;
+  p.N = N;
+  p.V = static_cast<int>(V);
+  p.D = static_cast<int>(D);
+  p.src = dX;
+  p.K = 1;
+  p.scale = scale;
+  p.part = at<float>(ws, pl.sort.o_part);
+  p.out = dE;
+  p.out_bf16 = grad_dtype == CUTBCE_GRAD_BF16;
+  p.accumulate = accumulate;
+  p.status = status;
+  return run_sums(p, dtype == CUTBCE_BF16, pl.sort.chunks, st);
+}
+
+cutbce_status cutbce_distill_workspace_size(const cutbce_distill_problem* prob, int outputs, size_t* bytes) {
+  if (prob == nullptr) return CUTBCE_ERR_INVALID_ARG;
+  return head_workspace(head_problem(prob), outputs, bytes);
+}
+
+cutbce_status cutbce_distill_forward(const cutbce_distill_problem* prob, double* loss, float* lse, void* ws,
+                                     size_t ws_bytes, cutbce_stream_t stream) {
+  if (prob == nullptr || (loss == nullptr && lse == nullptr)) return CUTBCE_ERR_INVALID_ARG;
+  HeadOutputs o;
+  o.loss = loss;
+  o.lse = lse;
+  return run_head(head_problem(prob), nullptr, nullptr, o, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+cutbce_status cutbce_distill_backward(const cutbce_distill_problem* prob, const cutbce_grad_options* opts,
+                                      const float* lse, const float* grad_loss, void* dH, void* dE, void* ws,
+                                      size_t ws_bytes, cutbce_stream_t stream) {
+  if (prob == nullptr || lse == nullptr || (dH == nullptr && dE == nullptr)) return CUTBCE_ERR_INVALID_ARG;
+  HeadOutputs o;
+  const cutbce_status s = check_grad_options(opts, o);
+  if (s != CUTBCE_OK) return s;
+  o.dH = dH;
+  o.dE = dE;
+  return run_head(head_problem(prob), lse, grad_loss, o, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+cutbce_status cutbce_distill_forward_backward(const cutbce_distill_problem* prob, const cutbce_grad_options* opts,
+                                              const float* grad_loss, double* loss, float* lse, void* dH, void* dE,
+                                              void* ws, size_t ws_bytes, cutbce_stream_t stream) {
+  if (prob == nullptr || (loss == nullptr && lse == nullptr && dH == nullptr && dE == nullptr))
+    return CUTBCE_ERR_INVALID_ARG;
+  HeadOutputs o;
+  const cutbce_status s = check_grad_options(opts, o);
+  if (s != CUTBCE_OK) return s;
+  o.loss = loss;
+  o.lse = lse;
+  o.dH = dH;
+  o.dE = dE;
+  return run_head(head_problem(prob), nullptr, grad_loss, o, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+cutbce_status cutbce_preference_workspace_size(const cutbce_preference_problem* prob, int outputs, size_t* bytes) {
+  if (prob == nullptr) return CUTBCE_ERR_INVALID_ARG;
+  return head_workspace(head_problem(prob), outputs, bytes);
+}
+
+cutbce_status cutbce_preference_forward(const cutbce_preference_problem* prob, double* loss, float* logp, float* lse,
+                                        void* ws, size_t ws_bytes, cutbce_stream_t stream) {
+  if (prob == nullptr || (loss == nullptr && logp == nullptr && lse == nullptr)) return CUTBCE_ERR_INVALID_ARG;
+  HeadOutputs o;
+  o.loss = loss;
+  o.logp = logp;
+  o.lse = lse;
+  return run_head(head_problem(prob), nullptr, nullptr, o, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+cutbce_status cutbce_preference_backward(const cutbce_preference_problem* prob, const cutbce_grad_options* opts,
+                                         const float* lse, const float* grad_loss, void* dH, void* dE, void* ws,
+                                         size_t ws_bytes, cutbce_stream_t stream) {
+  if (prob == nullptr || lse == nullptr || (dH == nullptr && dE == nullptr)) return CUTBCE_ERR_INVALID_ARG;
+  HeadOutputs o;
+  const cutbce_status s = check_grad_options(opts, o);
+  if (s != CUTBCE_OK) return s;
+  o.dH = dH;
+  o.dE = dE;
+  return run_head(head_problem(prob), lse, grad_loss, o, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+cutbce_status cutbce_preference_forward_backward(const cutbce_preference_problem* prob,
+                                                 const cutbce_grad_options* opts, const float* grad_loss, double* loss,
+                                                 float* logp, float* lse, void* dH, void* dE, void* ws,
+                                                 size_t ws_bytes, cutbce_stream_t stream) {
+  if (prob == nullptr || (loss == nullptr && logp == nullptr && lse == nullptr && dH == nullptr && dE == nullptr))
+    return CUTBCE_ERR_INVALID_ARG;
+  HeadOutputs o;
+  const cutbce_status s = check_grad_options(opts, o);
+  if (s != CUTBCE_OK) return s;
+  o.loss = loss;
+  o.logp = logp;
+  o.lse = lse;
+  o.dH = dH;
+  o.dE = dE;
+  return run_head(head_problem(prob), nullptr, grad_loss, o, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,43 @@
+// Row lookup of the item table with a scale: X[n] = s E[id_n], zero for an empty
+// id.  One 16-byte piece of one output row per thread (a scalar per thread where
+// width or alignment forbid it); it moves 2 N D elements and nothing else, so it
+// is bound by HBM for long batches and by launch latency for short ones.
+#pragma once
+#include <cuda_bf16.h>
+#include <cstdint>
+#include "common.cuh"
+#include "id_sort.cuh"
+
+namespace cutbce {
+
+template <int VEC, typename T>
+__global__ void __launch_bounds__(256) k_embed(const T* __restrict__ E, int64_t V, const int32_t* __restrict__ ids,
+                                               int64_t N, int D, float scale, T* __restrict__ X, int* status) {
+  const int per_row = D / VEC;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t n = i / per_row;
+  if (n >= N) return;
+  const int col = static_cast<int>(i - n * per_row) * VEC;
+  const int id = __ldg(ids + n);
+  float x[VEC];
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) x[k] = 0.f;
+  if (id >= 0 && id < V) {
+    load_row<VEC, T>(E + static_cast<int64_t>(id) * D + col, x);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) x[k] *= scale;
+  } else if (id != -1 && status != nullptr && col == 0) {
+    atomicCAS(status, 0, kErrTargetRange);
+  }
+  T* o = X + n * D + col;
+  if constexpr (VEC == 8) {
+    *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  } else if constexpr (VEC == 4) {
+    *reinterpret_cast<float4*>(o) = make_float4(x[0], x[1], x[2], x[3]);
+  } else {
+    *o = T(x[0]);
+  }
+}
+
+}  // namespace cutbce

@@ -1,0 +1,518 @@
+// Tensor-core passes of the softmax losses over the whole item table: one
+// persistent, warp-specialised sm_100a kernel template that forms logit tiles on
+// tcgen05 (accumulators in tensor memory) and takes exponentials of them in
+// registers.  No logit and no probability ever reaches device memory.
+//
+//   kLse   a CTA owns 128 positions and streams the items of one vocabulary
+//          split; each thread keeps a running maximum and sum of one row's slab.
+//   kRows  the same tiles with the exponent's offset known: P = 2^(c z - l_t) is
+//          rounded to bf16, written back over the logits in tensor memory and
+//          contracted with the item tile: dH partial += P E.
+//   kItems a CTA owns 128 items and streams the positions: P = 2^(c z + b_t),
+//          b_t = log2 |w_t| - l_t, and dE += +-P H.  Rows are compacted by the
+//          sign of w_t (the negative ones from a tile boundary on), so the sign
+//          is the negate-A bit of the contraction's instruction descriptor.
+//
+// c = log2(e) / tau.  Warp roles, tensor-memory layout and hand-over of the tiles
+// follow the BCE engine: warp 0 loads by TMA, warp 1 issues the MMAs, 16 epilogue
+// warps in two groups take alternate tiles.  Every wait is bounded.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cstdint>
+#include <type_traits>
+#include "common.cuh"
+#include "elementwise.cuh"
+#include "ptx_sm100.cuh"
+#include "softmax_head.cuh"
+#include "wait.cuh"
+
+namespace cutbce {
+
+enum : int { kPassLse = 0, kPassRows = 1, kPassItems = 2 };
+
+template <int DP, bool kGrad>
+struct SoftmaxCfg {
+  static constexpr int GROUPS = 2;
+  static constexpr int GROUP_WARPS = kNumEpiWarps / GROUPS;
+  static constexpr int SLABS = GROUP_WARPS / 4;
+  static constexpr int BN = DP <= 128 ? 128 : 64;           // streamed rows per tile
+  static constexpr int NKB = DP / 64;
+  static constexpr int NX = DP == 64 ? 12 : DP == 128 ? 5 : DP == 192 ? 7 : 4;
+  static constexpr int NZ = kGrad ? 3 : 4;                  // logit buffers in tensor memory
+  static constexpr uint32_t S_BYTES = kTileM * DP * 2;
+  static constexpr uint32_t X_BYTES = BN * DP * 2;
+  static constexpr int ZC = BN / SLABS;                     // logit columns per epilogue warp (64 or 32)
+  static constexpr int ACC_COL = 3 * BN;
+  static constexpr int S_COL = ACC_COL + DP;
+  static constexpr bool S_IN_TMEM = kGrad && S_COL + DP / 2 <= 512;
+  static constexpr int NUM_BARS = 2 + 2 * NX + 3 * NZ + 3;
+  static constexpr uint32_t SMEM_BYTES = 1024 + S_BYTES + NX * X_BYTES + NUM_BARS * 8 + 16 + 64;
+  static_assert(ACC_COL + DP <= 512 && NZ * BN <= 512, "TMEM budget");
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static_assert(SMEM_BYTES > 232448 / 2, "one CTA per SM keeps the TMEM allocation uncontended");
+};
+
+struct SoftmaxParams {
+  int V, D;
+  int64_t Tc;                  // rows of the compacted buffers
+  HeadHeader* hdr;
+  float c2;                    // log2(e) / tau
+  const float* off2;           // kRows: [Tc] l_t, kItems: [Tc] b_t (log2 domain)
+  float2* part;                // kLse: [splits * groups * slabs, Tc] (maximum, sum)
+  float* dh_part;              // kRows: [splits, Tc, DP]
+  const int* first;            // kItems: [V] row of `sparse` of each item, -1 none
+  const float* sparse;         // kItems: [.., D] sparse part of dE, unscaled
+  void* dE;                    // kItems: [V, D]
+  int de_bf16, de_acc;
+  int nsplit, tiles_per_split, n_item_tiles_bn;
+  long long timeout_ns;
+};
+
+// 32 logits of one row -> their exponentials.  kTail: columns from `valid` on are
+// outside the table and count as -infinity.
+__device__ __forceinline__ void mask_tail(uint32_t (&r)[32], int valid) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (e >= valid) r[e] = 0xFF800000u;
+}
+
+template <int DP, int kPass>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    k_softmax(const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmX, SoftmaxParams p) {
+  constexpr bool kGrad = kPass != kPassLse;
+  constexpr bool kItems = kPass == kPassItems;
+  using Cfg = SoftmaxCfg<DP, kGrad>;
+  constexpr int BN = Cfg::BN, NKB = Cfg::NKB, NX = Cfg::NX, NZ = Cfg::NZ, ZC = Cfg::ZC;
+  constexpr uint32_t S_BYTES = Cfg::S_BYTES, X_BYTES = Cfg::X_BYTES;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sS = smem;
+  uint8_t* sX = sS + S_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sX + NX * X_BYTES);
+  uint64_t* bar_sfull = bars + 0;                 // stationary tile landed (TMA)
+  uint64_t* bar_sempty = bars + 1;                // stationary tile no longer read (commit)
+  uint64_t* bar_xfull = bars + 2;                 // [NX] streamed tile landed
+  uint64_t* bar_xempty = bar_xfull + NX;          // [NX] streamed tile free (commit)
+  uint64_t* bar_zfull = bar_xempty + NX;          // [NZ] logit tile ready (commit)
+  uint64_t* bar_zfree = bar_zfull + NZ;           // [NZ] buffer free: P contracted (commit), or logits loaded (epilogue)
+  uint64_t* bar_pready = bar_zfree + NZ;          // [NZ] P written over the logits (epilogue)
+  uint64_t* bar_accfull = bar_pready + NZ;        // accumulator complete (commit)
+  uint64_t* bar_accempty = bar_accfull + 1;       // accumulator read out (epilogue)
+  uint64_t* bar_drain = bar_accempty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::NUM_BARS);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  WsHeader* hdr = &p.hdr->w;
+  __shared__ int s_status, s_rows, s_neg0;
+  if (threadIdx.x == 0) {
+    s_status = *reinterpret_cast<volatile int*>(&hdr->status);
+    s_rows = p.hdr->n_rows;
+    s_neg0 = p.hdr->neg0;
+  }
+  __syncthreads();
+  if (s_status != 0) return;
+  const int n_rows = s_rows;                      // compacted rows, a multiple of 128
+  const int neg_tile = s_neg0 / BN;               // kItems: first streamed tile of negative rows
+  const int n_row_tiles = n_rows / kTileM;
+  const int n_items = kItems ? static_cast<int>(ceil_div(p.V, kTileM)) : p.nsplit * n_row_tiles;
+  if (kItems && n_rows == 0) {
+    // no position counts: dE is zero
+    if (p.de_acc) return;
+    const int64_t n = static_cast<int64_t>(p.V) * p.D;
+    for (int64_t k = static_cast<int64_t>(blockIdx.x) * kTileThreads + threadIdx.x; k < n;
+         k += static_cast<int64_t>(gridDim.x) * kTileThreads) {
+      if (p.de_bf16) static_cast<__nv_bfloat16*>(p.dE)[k] = __float2bfloat16_rn(0.f);
+      else static_cast<float*>(p.dE)[k] = 0.f;
+    }
+    return;
+  }
+  if (static_cast<int>(blockIdx.x) >= n_items) return;
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar_sfull, 1);
+    mbar_init(bar_sempty, 1);
+    for (int s = 0; s < NX; ++s) {
+      mbar_init(bar_xfull + s, 1);
+      mbar_init(bar_xempty + s, 1);
+    }
+    for (int b = 0; b < NZ; ++b) {
+      mbar_init(bar_zfull + b, 1);
+      mbar_init(bar_zfree + b, kGrad ? 1 : Cfg::GROUP_WARPS * 32);
+      mbar_init(bar_pready + b, Cfg::GROUP_WARPS * 32);
+    }
+    mbar_init(bar_accfull, 1);
+    mbar_init(bar_accempty, Cfg::GROUP_WARPS);
+    mbar_init(bar_drain, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmS);
+    tma_prefetch_desc(&tmX);
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const WaitCtx wc{abort_flag, hdr, p.timeout_ns};
+
+  // work item i: a tile of items (kItems), or (vocabulary split, tile of positions), split-major
+  auto item = [&](int i, int& s_row0, int& x0, int& nx, int& split) {
+    if (kItems) {
+      s_row0 = i * kTileM;
+      x0 = 0;
+      nx = n_rows / BN;
+      split = 0;
+    } else {
+      split = i / n_row_tiles;
+      s_row0 = (i - split * n_row_tiles) * kTileM;
+      x0 = split * p.tiles_per_split;
+      nx = min(p.tiles_per_split, p.n_item_tiles_bn - x0);
+    }
+  };
+
+  if (warp == 0) {
+    // ============================================================ TMA producer
+    if (lane == 0) {
+      uint32_t ic = 0, xc = 0;
+      for (int i = blockIdx.x; i < n_items; i += gridDim.x, ++ic) {
+        int s_row0, x0, nx, split;
+        item(i, s_row0, x0, nx, split);
+        if (!wait_bar(bar_sempty, (ic & 1) ^ 1, wc, wait_tag(1, 1, ic))) break;
+        mbar_arrive_expect_tx(bar_sfull, S_BYTES);
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb) tma_load_2d(sS + kb * (kTileM * 128), &tmS, kb * 64, s_row0, bar_sfull);
+        bool ok = true;
+        for (int j = 0; j < nx; ++j, ++xc) {
+          const uint32_t st = xc % NX;
+          if (!wait_bar(bar_xempty + st, ((xc / NX) & 1) ^ 1, wc, wait_tag(1, 3, xc))) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar_xfull + st, X_BYTES);
+#pragma unroll
+          for (int kb = 0; kb < NKB; ++kb)
+            tma_load_2d(sX + st * X_BYTES + kb * (BN * 128), &tmX, kb * 64, (x0 + j) * BN, bar_xfull + st);
+        }
+        if (!ok) {
+          ++ic;
+          break;
+        }
+      }
+      // wait (bounded) for every copy this thread issued to land
+      if (ic > 0) wait_bar_drain(bar_sfull, (ic - 1) & 1, p.timeout_ns);
+      for (uint32_t st = 0; st < NX; ++st) {
+        const uint32_t issued = xc > st ? (xc - st + NX - 1) / NX : 0;
+        if (issued > 0) wait_bar_drain(bar_xfull + st, (issued - 1) & 1, p.timeout_ns);
+      }
+    }
+  } else if (warp == 1) {
+    // ============================================================ MMA issuer
+    // An event loop over two in-order streams, logit tiles Z(c) into buffer
+    // c mod NZ and contractions of P(c); whichever is ready is issued.  Lanes 0-4
+    // test one barrier each, a ballot gathers the answers.
+    constexpr uint32_t idesc_z = idesc_bf16_f32(kTileM, BN, false, false);
+    constexpr uint32_t idesc_acc = idesc_bf16_f32(kTileM, DP, false, true);
+    constexpr uint32_t kNegateA = 1u << 13;
+    constexpr uint32_t kXStep = X_BYTES >> 4;
+    constexpr int kKsPerSlab = ZC / 16;
+    const uint64_t dS = smem_desc_sw128(smem_u32(sS), 16, 1024);
+    const uint64_t dXk = smem_desc_sw128(smem_u32(sX), 16, 1024);
+    const uint64_t dXmn = smem_desc_sw128(smem_u32(sX), BN * 128, 1024);
+    const uint32_t tAcc = tmem_base + Cfg::ACC_COL, tS = tmem_base + Cfg::S_COL;
+    int zi = blockIdx.x, zj = 0, zn = 0, gi = zi, gj = 0, gn = 0;
+    int row0, x0, split;
+    uint32_t zic = 0, cz = 0, gic = 0, cg = 0;
+    uint32_t zst = 0, zph = 0, gst = 0, zb = 0, zbph = 0, gb = 0, gbph = 0;
+    bool s_ready = false;
+    item(zi, row0, x0, zn, split);
+    gn = zn;
+    uint64_t idle_since = 0;
+    bool ok = true;
+    while (ok && (zi < n_items || (kGrad && gi < n_items))) {
+      bool progressed = false;
+      const bool want_z = zi < n_items;
+      const bool want_g = kGrad && gi < n_items && cg < cz;
+      bool mine = false;
+      if (lane == 0 && want_z && zj == 0 && !s_ready) mine = mbar_test_wait(bar_sfull, zic & 1);
+      if (lane == 1 && want_z) mine = mbar_test_wait(bar_xfull + zst, zph);
+      if (lane == 2 && want_z) mine = mbar_test_wait(bar_zfree + zb, zbph ^ 1);
+      if (lane == 3 && want_g) mine = mbar_test_wait(bar_pready + gb, gbph);
+      if (lane == 4 && want_g && gj == 0) mine = mbar_test_wait(bar_accempty, (gic & 1) ^ 1);
+      const uint32_t ready = __ballot_sync(0xffffffffu, mine);
+      if (want_z) {
+        if (zj == 0 && !s_ready && (ready & 1u)) {
+          tc_fence_after();
+          s_ready = true;
+          if (Cfg::S_IN_TMEM) {
+            if (elect_one()) {
+#pragma unroll
+              for (int ks = 0; ks < DP / 16; ++ks)
+                tmem_cp_128x256b(tS + 8 * ks, dS + static_cast<uint32_t>((ks >> 2) * (kTileM * 8) + (ks & 3) * 2));
+              umma_commit(bar_sempty);
+            }
+            __syncwarp();
+          }
+        }
+        if ((zj > 0 || s_ready) && (ready & 6u) == 6u) {
+          tc_fence_after();
+          const uint64_t dB = dXk + zst * kXStep;
+          const uint32_t tD = tmem_base + zb * BN;
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ++ks) {
+              const uint64_t bd = dB + static_cast<uint32_t>((ks >> 2) * (BN * 8) + (ks & 3) * 2);
+              if (Cfg::S_IN_TMEM) umma_bf16_tmem_a(tD, tS + 8 * ks, bd, idesc_z, ks > 0 ? 1u : 0u);
+              else umma_bf16(tD, dS + static_cast<uint32_t>((ks >> 2) * (kTileM * 8) + (ks & 3) * 2), bd, idesc_z,
+                             ks > 0 ? 1u : 0u);
+            }
+            umma_commit(bar_zfull + zb);
+            if (!kGrad) umma_commit(bar_xempty + zst);
+            if (!Cfg::S_IN_TMEM && zj + 1 == zn) umma_commit(bar_sempty);
+          }
+          __syncwarp();
+          progressed = true;
+          ++cz;
+          if (++zst == static_cast<uint32_t>(NX)) {
+            zst = 0;
+            zph ^= 1;
+          }
+          if (++zb == static_cast<uint32_t>(NZ)) {
+            zb = 0;
+            zbph ^= 1;
+          }
+          if (++zj == zn) {
+            zj = 0;
+            ++zic;
+            s_ready = false;
+            zi += gridDim.x;
+            if (zi < n_items) item(zi, row0, x0, zn, split);
+          }
+        }
+      }
+      if (want_g && (ready & 8u) && (gj > 0 || (ready & 16u))) {
+        tc_fence_after();
+        const uint64_t dB = dXmn + gst * kXStep;
+        const uint32_t tA = tmem_base + gb * BN;
+        const bool last = gj + 1 == gn;
+        const uint32_t idesc = kItems && gj >= neg_tile ? idesc_acc | kNegateA : idesc_acc;
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < BN / 16; ++ks) {
+            // slab k of the P tile sits in the first half of the logit columns of slab k
+            const uint32_t a_col = (ks / kKsPerSlab) * ZC + 8 * (ks % kKsPerSlab);
+            umma_bf16_tmem_a(tAcc, tA + a_col, dB + static_cast<uint32_t>(ks * 128), idesc, (gj > 0 || ks > 0) ? 1u : 0u);
+          }
+          umma_commit(bar_zfree + gb);
+          umma_commit(bar_xempty + gst);
+          if (last) umma_commit(bar_accfull);
+        }
+        __syncwarp();
+        progressed = true;
+        ++cg;
+        if (++gst == static_cast<uint32_t>(NX)) gst = 0;
+        if (++gb == static_cast<uint32_t>(NZ)) {
+          gb = 0;
+          gbph ^= 1;
+        }
+        if (last) {
+          gj = 0;
+          ++gic;
+          gi += gridDim.x;
+          if (gi < n_items) item(gi, row0, x0, gn, split);
+        } else {
+          ++gj;
+        }
+      }
+      if (progressed) {
+        idle_since = 0;
+      } else {
+        // bounded: give up if nothing became ready within the limit
+        const uint64_t now = global_timer_ns();
+        if (idle_since == 0) idle_since = now;
+        int give_up = 0;
+        if (lane == 0) {
+          if (*reinterpret_cast<volatile int*>(abort_flag)) {
+            give_up = 1;
+          } else if (static_cast<long long>(now - idle_since) > p.timeout_ns) {
+            *reinterpret_cast<volatile int*>(abort_flag) = 1;
+            if (atomicCAS(&hdr->status, 0, kErrTimeout) == 0) {
+              hdr->wait_tag = wait_tag(2, 15, cz);
+              hdr->wait_block = static_cast<int>(blockIdx.x);
+            }
+            give_up = 1;
+          }
+        }
+        if (__shfl_sync(0xffffffffu, give_up, 0)) ok = false;
+      }
+    }
+    // every MMA this warp issued has completed once the drain barrier flips
+    if (elect_one()) umma_commit(bar_drain);
+    __syncwarp();
+    if (lane == 0) wait_bar_drain(bar_drain, 0, p.timeout_ns);
+    __syncwarp();
+  } else {
+    // ============================================================ epilogue
+    constexpr int NCH = ZC / 32;                  // chunks of 32 columns per warp and tile
+    constexpr int AC = DP / Cfg::SLABS;           // accumulator columns per warp
+    const int ew = warp - kEpiWarp0;
+    const uint32_t grp = static_cast<uint32_t>(ew / Cfg::GROUP_WARPS);
+    const int q = warp & 3;
+    const int slab = (ew >> 2) % Cfg::SLABS;
+    const int row = q * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+    const float2 c2 = f2(p.c2, p.c2);
+    uint32_t cnt = 0, ic = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x, ++ic) {
+      int s_row0, x0, n, split;
+      item(i, s_row0, x0, n, split);
+      float m = -1e30f, sum = 0.f;                // kLse: running maximum (log2 domain) and sum
+      float off = 0.f;                            // kRows: -l_t
+      if (kPass == kPassRows) off = -__ldg(p.off2 + s_row0 + row);
+      const int j0 = static_cast<int>((grp + Cfg::GROUPS - cnt % Cfg::GROUPS) % Cfg::GROUPS);
+      for (int j = j0; j < n; j += Cfg::GROUPS) {
+        const uint32_t c = cnt + j, bz = c % NZ;
+        if (!wait_bar_warp(bar_zfull + bz, (c / NZ) & 1, wc, wait_tag(4, 4, c))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int tile_col0 = (x0 + j) * BN + slab * ZC;      // item (or compacted position) of the slab's first column
+        const bool tail = !kItems && (x0 + j + 1) * static_cast<int64_t>(BN) > p.V;
+#pragma unroll
+        for (int ch = 0; ch < NCH; ++ch) {
+          uint32_t r[32];
+          tmem_ld32(tmem_base + lane_base + bz * BN + slab * ZC + ch * 32, r);
+          tmem_ld_wait();
+          if (!kGrad && ch == NCH - 1) {
+            tc_fence_before();
+            mbar_arrive(bar_zfree + bz);
+          }
+          const int col = tile_col0 + ch * 32;
+          if (tail) mask_tail(r, p.V - col);
+          if constexpr (kPass == kPassLse) {
+            float mx = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+#pragma unroll
+            for (int e = 2; e < 32; e += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(r[e]), __uint_as_float(r[e + 1])));
+            mx *= p.c2;
+            // the reference moves only when the maximum has grown by 2^8: sums stay far from overflow
+            const float mn = mx > m + 8.f ? mx : m;
+            sum *= ex2_approx(m - mn);
+            m = mn;
+            const float2 nm = f2(-m, -m);
+            float2 s2 = f2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 x = __ffma2_rn(f2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), c2, nm);
+              s2 = __fadd2_rn(s2, f2(ex2_approx(x.x), ex2_approx(x.y)));
+            }
+            sum += s2.x + s2.y;
+          } else {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 o = kItems ? __ldg(reinterpret_cast<const float2*>(p.off2 + col + e)) : f2(off, off);
+              const float2 x = __ffma2_rn(f2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), c2, o);
+              pk[e >> 1] = pack_bf16x2(ex2_approx(x.x), ex2_approx(x.y));
+            }
+            tmem_st16(tmem_base + lane_base + bz * BN + slab * ZC + ch * 16, pk);
+          }
+        }
+        if constexpr (kGrad) {
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(bar_pready + bz);
+        }
+      }
+      if (!ok) break;
+      if constexpr (kPass == kPassLse) {
+        const int slot = (split * Cfg::GROUPS + static_cast<int>(grp)) * Cfg::SLABS + slab;
+        p.part[static_cast<int64_t>(slot) * p.Tc + s_row0 + row] = make_float2(m, sum);
+      }
+      if (kGrad && (cnt + n - 1) % Cfg::GROUPS == grp) {
+        // the group that took the last tile reads the accumulator out
+        if (!wait_bar_warp(bar_accfull, ic & 1, wc, wait_tag(4, 9, ic))) break;
+        tc_fence_after();
+        const int v = s_row0 + row;
+        int64_t sp = -1;
+        float gs = 0.f;
+        if (kItems && v < p.V) {
+          sp = __ldg(p.first + v);
+          gs = hdr->grad_scale;
+        }
+#pragma unroll 1
+        for (int ch = 0; ch < AC / 16; ++ch) {
+          uint32_t r[16];
+          const int col0 = slab * AC + ch * 16;
+          tmem_ld<16>(tmem_base + lane_base + Cfg::ACC_COL + col0, r);
+          tmem_ld_wait();
+          if (!kItems) {
+            float* dst = p.dh_part + (static_cast<int64_t>(split) * p.Tc + s_row0 + row) * DP + col0;
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<float4*>(dst + e) = make_float4(__uint_as_float(r[e]), __uint_as_float(r[e + 1]),
+                                                                __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
+          } else if (v < p.V) {
+            const int64_t o = static_cast<int64_t>(v) * p.D + col0;
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              if (col0 + e >= p.D) continue;
+              float4 g = make_float4(__uint_as_float(r[e]), __uint_as_float(r[e + 1]), __uint_as_float(r[e + 2]),
+                                     __uint_as_float(r[e + 3]));
+              if (sp >= 0) {
+                const float4 s4 = __ldg(reinterpret_cast<const float4*>(p.sparse + sp * p.D + col0 + e));
+                g.x -= s4.x;
+                g.y -= s4.y;
+                g.z -= s4.z;
+                g.w -= s4.w;
+              }
+              g.x = __fmul_rn(g.x, gs);
+              g.y = __fmul_rn(g.y, gs);
+              g.z = __fmul_rn(g.z, gs);
+              g.w = __fmul_rn(g.w, gs);
+              if (p.de_bf16) {
+                uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.dE) + o + e);
+                if (p.de_acc) {
+                  const uint2 old = *dst;
+                  g.x = __fadd_rn(g.x, __uint_as_float(old.x << 16));
+                  g.y = __fadd_rn(g.y, __uint_as_float(old.x & 0xFFFF0000u));
+                  g.z = __fadd_rn(g.z, __uint_as_float(old.y << 16));
+                  g.w = __fadd_rn(g.w, __uint_as_float(old.y & 0xFFFF0000u));
+                }
+                *dst = make_uint2(pack_bf16x2(g.x, g.y), pack_bf16x2(g.z, g.w));
+              } else {
+                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.dE) + o + e);
+                if (p.de_acc) {
+                  const float4 old = *dst;
+                  g.x = __fadd_rn(g.x, old.x);
+                  g.y = __fadd_rn(g.y, old.y);
+                  g.z = __fadd_rn(g.z, old.z);
+                  g.w = __fadd_rn(g.w, old.w);
+                }
+                *dst = g;
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_accempty);
+      }
+      cnt += n;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+}  // namespace cutbce

@@ -1,0 +1,549 @@
+// CUDA-core kernels around the softmax tile engine (softmax_engine.cuh): the
+// losses with a softmax over the whole item table.
+//
+//   rows    which positions count, their class (sign of their gradient's factor),
+//           the checks of ids and offsets, and the normalisation;
+//   gather  compacts the rows of H (positive class first, the negative class from
+//           the next multiple of 128 rows), takes the logits of the sparse
+//           targets and their part of dH in fp32;
+//   lse     joins the log-sum-exp partials of a row, and the distillation loss;
+//   pairs   the preference loss, from the sums over each sequence;
+//   dh      adds the split partials of dH, subtracts the sparse part, scales.
+//
+// With p = softmax(z / tau) and q the sparse target weights of a position, the
+// gradient of every such loss is  dz = w (p - q).  The dense part w p is formed
+// in the tile engine and rounded to bf16 there; the sparse part w q never passes
+// through bf16: it is summed in fp32 (here for dH, over sorted ids for dE) and
+// joined to the dense part before the one rounding of the output.
+#pragma once
+#include <cuda_bf16.h>
+#include <cstdint>
+#include "common.cuh"
+#include "id_sort.cuh"
+#include "ptx_sm100.cuh"
+
+namespace cutbce {
+
+enum : int { kHeadDistill = 0, kHeadPreference = 1 };
+
+// First 256 bytes of a softmax head's workspace.
+struct HeadHeader {
+  WsHeader w;               // status first; n_valid, grad_scale, waits
+  int n_pos;                // rows of the positive class: compacted rows [0, n_pos)
+  int n_neg;                // rows of the negative class: [neg0, neg0 + n_neg)
+  int neg0;                 // first row of the negative class (a multiple of 128)
+  int n_rows;               // compacted rows with padding (a multiple of 128)
+  int rows_ticket;          // blocks done, per kernel that has a last block
+  int lse_ticket;
+  int pairs_ticket;
+};
+static_assert(sizeof(HeadHeader) <= 256, "the workspace header is 256 bytes");
+
+struct HeadParams {
+  int kind;
+  int T, V, D, DP, K;
+  int P;                         // preference pairs
+  const __nv_bfloat16* H;
+  const __nv_bfloat16* E;
+  const int32_t* ids;            // [T, K]
+  const float* logits;           // [T, K] teacher logits (distillation)
+  const int32_t* offsets;        // [2P + 1] (preference)
+  const float* ref;              // [2P] reference log-probabilities, or null
+  const uint8_t* mask;
+  const float* weights;          // [T], or null (distillation)
+  float inv_tau, tau, beta;
+  int reduction;
+  const float* grad_loss;
+  HeadHeader* hdr;
+  uint8_t* cls;                  // [T] 0 none, 1 positive, 2 negative
+  int* blk;                      // [2 * ceil(T / 256)] rows per class and block, then their prefix
+  int n_blk;
+  int* cidx;                     // [T] compacted row or -1
+  int* orig;                     // [Tc] position of a compacted row, -1 padding
+  __nv_bfloat16* Hc;             // [Tc, DP]
+  double* rowterm;               // [Tc] distillation: sum_k q (ln q - z / tau); preference: z_y
+  float* sparse;                 // [Tc, DP] sum_k q_k e_k, or null
+  int* keys;                     // [T * K] ids of the pairs (-1 none), or null
+  float* share;                  // [T * K] q of the pairs, or null
+  float* coef;                   // [T] signed factor of the row's gradient
+  float* b2;                     // [Tc] log2 |factor| - log2-domain lse (-inf for padding)
+  float* lse2;                   // [Tc] lse in the log2 domain
+  const float* lse_in;           // [T] lse of an earlier forward, or null
+  const float2* part;            // [slots, Tc] (max, sum) partials in the log2 domain
+  int slots;
+  int64_t Tc;                    // rows of the compacted buffers
+  double* loss_part;             // per-block (distillation) or per-pair (preference) partials
+  double* loss;                  // output or null
+  float* lse_out;                // [T] output or null
+  float* logp_out;               // [2P] output or null
+};
+
+__device__ __forceinline__ int head_blocks_of(int T) { return (T + 255) / 256; }
+
+// ------------------------------------------------------------------ rows
+__global__ void __launch_bounds__(256) k_head_rows(const HeadParams p) {
+  __shared__ int cnt[2];
+  __shared__ int last;
+  __shared__ int tot[2][256];
+  HeadHeader* hdr = p.hdr;
+  const int tid = threadIdx.x;
+  const int t = blockIdx.x * 256 + tid;
+  if (tid < 2) cnt[tid] = 0;
+  __syncthreads();
+  int cls = 0;
+  bool bad = false;
+  if (t < p.T && (p.mask == nullptr || p.mask[t] != 0)) {
+    if (p.kind == kHeadDistill) {
+      const float w = p.weights != nullptr ? p.weights[t] : 1.f;
+      if (w != 0.f) {
+        const int64_t r = static_cast<int64_t>(t) * p.K;
+        bool any = false;
+        for (int k = 0; k < p.K; ++k) {
+          const int id = __ldg(p.ids + r + k);
+          if (id == -1) continue;
+          if (id < 0 || id >= p.V) bad = true;
+          any |= !(__ldg(p.logits + r + k) == -INFINITY);
+        }
+        if (any) cls = w < 0.f ? 2 : 1;
+      }
+    } else {
+      const int id = p.ids[t];
+      const int o0 = p.offsets[0], o1 = p.offsets[2 * p.P];
+      if (id != -1 && t >= o0 && t < o1) {
+        if (id < 0 || id >= p.V) bad = true;
+        int lo = 0, hi = 2 * p.P;                     // the last sequence that starts at or before t
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (__ldg(p.offsets + mid) <= t) lo = mid;
+          else hi = mid;
+        }
+        cls = 1 + (lo & 1);
+      }
+    }
+  }
+  if (p.kind == kHeadPreference) {
+    for (int64_t i = t; i <= 2 * static_cast<int64_t>(p.P); i += static_cast<int64_t>(gridDim.x) * 256) {
+      const int o = p.offsets[i];
+      if (o < 0 || o > p.T || (i > 0 && p.offsets[i - 1] > o)) bad = true;
+    }
+  }
+  if (bad) atomicCAS(&hdr->w.status, 0, kErrTargetRange);
+  if (t < p.T) p.cls[t] = static_cast<uint8_t>(cls);
+  const unsigned b1 = __ballot_sync(0xffffffffu, cls == 1), b2 = __ballot_sync(0xffffffffu, cls == 2);
+  if ((tid & 31) == 0) {
+    atomicAdd(&cnt[0], __popc(b1));
+    atomicAdd(&cnt[1], __popc(b2));
+  }
+  __syncthreads();
+  if (tid == 0) {
+    p.blk[2 * blockIdx.x] = cnt[0];
+    p.blk[2 * blockIdx.x + 1] = cnt[1];
+    __threadfence();
+    last = atomicAdd(&hdr->rows_ticket, 1) == static_cast<int>(gridDim.x) - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  // the last block: exclusive prefix of the block counts, then the header
+  const int per = (p.n_blk + 255) / 256;
+  const int a = min(p.n_blk, tid * per), e = min(p.n_blk, a + per);
+  int s0 = 0, s1 = 0;
+  for (int i = a; i < e; ++i) {
+    s0 += __ldcg(p.blk + 2 * i);
+    s1 += __ldcg(p.blk + 2 * i + 1);
+  }
+  tot[0][tid] = s0;
+  tot[1][tid] = s1;
+  __syncthreads();
+  for (int off = 1; off < 256; off <<= 1) {
+    const int x0 = tid >= off ? tot[0][tid - off] : 0, x1 = tid >= off ? tot[1][tid - off] : 0;
+    __syncthreads();
+    tot[0][tid] += x0;
+    tot[1][tid] += x1;
+    __syncthreads();
+  }
+  int r0 = tot[0][tid] - s0, r1 = tot[1][tid] - s1;
+  for (int i = a; i < e; ++i) {
+    const int c0 = __ldcg(p.blk + 2 * i), c1 = __ldcg(p.blk + 2 * i + 1);
+    p.blk[2 * i] = r0;
+    p.blk[2 * i + 1] = r1;
+    r0 += c0;
+    r1 += c1;
+  }
+  if (tid == 0) {
+    const int np = tot[0][255], nn = tot[1][255];
+    const int neg0 = (np + kTileM - 1) / kTileM * kTileM;
+    hdr->n_pos = np;
+    hdr->n_neg = nn;
+    hdr->neg0 = neg0;
+    hdr->n_rows = neg0 + (nn + kTileM - 1) / kTileM * kTileM;
+    hdr->w.n_valid = np + nn;
+    double s = 1.0;
+    if (p.reduction == kMeanValidPositions) {
+      const int n = p.kind == kHeadDistill ? np + nn : p.P;
+      s = n > 0 ? 1.0 / n : 0.0;
+    }
+    const double g = p.grad_loss != nullptr ? static_cast<double>(*p.grad_loss) : 1.0;
+    hdr->w.loss_scale = s;
+    hdr->w.grad_scale = static_cast<float>(g * s * (p.kind == kHeadDistill ? p.tau : p.beta));
+  }
+}
+
+// ------------------------------------------------------------------ gather
+// One warp per position, then one warp per padding row (256 of them at most).
+// Lane l holds the column pairs l, l + 32, ... of the row.  The targets' rows of
+// E are read kGatherU at a time.
+constexpr int kGatherU = 4;
+
+__global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
+  const HeadHeader* hdr = p.hdr;
+  if (hdr->w.status != 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + warp;
+  const int pairs = p.DP / 64;                  // column pairs per lane (1 .. 4)
+  if (t >= p.T) {
+    // padding rows: [n_pos, neg0) and [neg0 + n_neg, n_rows)
+    const int j = static_cast<int>(t - p.T);
+    const int gap = hdr->neg0 - hdr->n_pos;
+    const int64_t c = j < gap ? hdr->n_pos + j : hdr->neg0 + hdr->n_neg + (j - gap);
+    if (c >= hdr->n_rows) return;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.Hc + c * p.DP);
+    for (int i = 0; i < pairs; ++i) dst[lane + 32 * i] = 0u;
+    if (lane == 0) {
+      p.orig[c] = -1;
+      p.b2[c] = -INFINITY;
+      p.lse2[c] = 0.f;
+    }
+    return;
+  }
+  const int cls = p.cls[t];
+  const int64_t r = t * p.K;
+  if (cls == 0) {
+    if (p.keys != nullptr)
+      for (int k = lane; k < p.K; k += 32) {
+        p.keys[r + k] = -1;
+        p.share[r + k] = 0.f;
+      }
+    if (lane == 0) {
+      p.cidx[t] = -1;
+      p.coef[t] = 0.f;
+      if (p.lse_out != nullptr) p.lse_out[t] = 0.f;
+    }
+    return;
+  }
+  // compacted row: this block's prefix plus the rows of the class before t in its 256
+  int64_t c;
+  {
+    const int b = static_cast<int>(t >> 8);
+    int before = 0;
+    for (int i = lane; i < static_cast<int>(t & 255); i += 32) before += p.cls[(static_cast<int64_t>(b) << 8) + i] == cls;
+    before = __reduce_add_sync(0xffffffffu, before);
+    c = p.blk[2 * b + cls - 1] + before + (cls == 2 ? hdr->neg0 : 0);
+  }
+  float2 h[4], sp[4];
+  {
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(p.H + t * p.D);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.Hc + c * p.DP);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[i] = sp[i] = make_float2(0.f, 0.f);
+      if (i >= pairs) continue;
+      const int j = lane + 32 * i;
+      const uint32_t u = 2 * j < p.D ? __ldg(src + j) : 0u;
+      dst[j] = u;
+      h[i] = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+    }
+  }
+  // the teacher's weights: slot k = lane + 32 j
+  float q[4], lq[4];
+  int id[4];
+  if (p.kind == kHeadDistill) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = lane + 32 * j;
+      id[j] = k < p.K ? __ldg(p.ids + r + k) : -1;
+      lq[j] = id[j] >= 0 ? __ldg(p.logits + r + k) * p.inv_tau : -INFINITY;
+      m = fmaxf(m, lq[j]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      lq[j] -= m;
+      q[j] = expf(lq[j]);                        // an empty slot: e^-inf = 0
+      s += q[j];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const float ls = logf(s);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      q[j] /= s;
+      lq[j] -= ls;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      q[j] = j == 0 && lane == 0 ? 1.f : 0.f;
+      lq[j] = 0.f;
+      id[j] = -1;
+    }
+    if (lane == 0) id[0] = __ldg(p.ids + t);
+  }
+  double term = 0.0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int n = min(32, p.K - 32 * j);
+    if (n <= 0) break;
+    if (p.keys != nullptr && lane < n) {
+      p.keys[r + 32 * j + lane] = q[j] == 0.f ? -1 : id[j];
+      p.share[r + 32 * j + lane] = q[j];
+    }
+    for (int k = 0; k < n; k += kGatherU) {
+      float z[kGatherU], w[kGatherU], lw[kGatherU];
+      float2 e[kGatherU][4];
+#pragma unroll
+      for (int u = 0; u < kGatherU; ++u) {
+        const int from = min(k + u, 31);
+        const int v = __shfl_sync(0xffffffffu, id[j], from);
+        w[u] = __shfl_sync(0xffffffffu, q[j], from);
+        lw[u] = __shfl_sync(0xffffffffu, lq[j], from);
+        z[u] = 0.f;
+        if (k + u >= n || v < 0) w[u] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          e[u][i] = make_float2(0.f, 0.f);
+          if (i >= pairs || w[u] == 0.f) continue;
+          const int col = lane + 32 * i;
+          const uint32_t x = 2 * col < p.D ? __ldg(reinterpret_cast<const uint32_t*>(p.E + static_cast<int64_t>(v) * p.D) + col) : 0u;
+          e[u][i] = make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kGatherU; ++u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          z[u] = fmaf(h[i].x, e[u][i].x, fmaf(h[i].y, e[u][i].y, z[u]));
+          sp[i].x = fmaf(w[u], e[u][i].x, sp[i].x);
+          sp[i].y = fmaf(w[u], e[u][i].y, sp[i].y);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < kGatherU; ++u) z[u] += __shfl_xor_sync(0xffffffffu, z[u], o);
+#pragma unroll
+      for (int u = 0; u < kGatherU; ++u) {
+        if (w[u] == 0.f) continue;
+        term += p.kind == kHeadDistill
+                    ? static_cast<double>(w[u]) * (static_cast<double>(lw[u]) - static_cast<double>(z[u]) * p.inv_tau)
+                    : static_cast<double>(z[u]);
+      }
+    }
+  }
+  if (p.sparse != nullptr) {
+    float2* o = reinterpret_cast<float2*>(p.sparse + c * p.DP);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < pairs) o[lane + 32 * i] = sp[i];
+  }
+  if (lane == 0) {
+    p.cidx[t] = static_cast<int>(c);
+    p.orig[c] = static_cast<int>(t);
+    p.rowterm[c] = term;
+    if (p.kind == kHeadDistill) p.coef[t] = p.weights != nullptr ? p.weights[t] : 1.f;
+  }
+}
+
+// Sum over the block in a fixed order (contiguous values per thread, then a tree).
+__device__ __forceinline__ double head_block_sum(double v, double* red) {
+  red[threadIdx.x] = v;
+  __syncthreads();
+  for (int s = blockDim.x / 2; s > 0; s >>= 1) {
+    if (threadIdx.x < s) red[threadIdx.x] += red[threadIdx.x + s];
+    __syncthreads();
+  }
+  const double r = red[0];
+  __syncthreads();
+  return r;
+}
+
+// ------------------------------------------------------------------ lse
+// One thread per compacted row: joins the (max, sum) partials of the row's splits
+// and slabs (or takes the lse of an earlier forward), writes lse, the exponent
+// offset of the item-owned pass and the row's share of the distillation loss,
+// which the last block adds up in block order.
+constexpr int kLseThreads = 128;
+
+__global__ void __launch_bounds__(kLseThreads) k_head_lse(const HeadParams p) {
+  __shared__ double red[kLseThreads];
+  __shared__ int last;
+  HeadHeader* hdr = p.hdr;
+  if (hdr->w.status != 0) return;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kLseThreads + threadIdx.x;
+  double row_loss = 0.0;
+  const int t = c < hdr->n_rows ? p.orig[c] : -1;
+  if (t >= 0) {
+    float l2;
+    if (p.lse_in != nullptr) {
+      l2 = p.lse_in[t] * 1.4426950408889634f;
+    } else {
+      float m = -3.0e38f;
+      for (int s = 0; s < p.slots; ++s) m = fmaxf(m, p.part[s * p.Tc + c].x);
+      float sum = 0.f;
+      for (int s = 0; s < p.slots; ++s) {
+        const float2 v = p.part[s * p.Tc + c];
+        sum += v.y * exp2f(v.x - m);
+      }
+      l2 = m + log2f(sum);
+      if (sum != sum || m != m) l2 = NAN;
+    }
+    p.lse2[c] = l2;
+    const double lse = static_cast<double>(l2) * 0.6931471805599453;
+    if (p.lse_out != nullptr) p.lse_out[t] = static_cast<float>(lse);
+    if (p.kind == kHeadDistill) {
+      const float w = p.weights != nullptr ? p.weights[t] : 1.f;
+      p.b2[c] = (p.weights != nullptr ? log2f(fabsf(w)) : 0.f) - l2;
+      row_loss = static_cast<double>(w) * p.tau * p.tau * (p.rowterm[c] + lse);
+    }
+  }
+  if (p.kind != kHeadDistill || p.loss == nullptr) return;
+  const double b = head_block_sum(row_loss, red);
+  if (threadIdx.x == 0) {
+    p.loss_part[blockIdx.x] = b;
+    __threadfence();
+    last = atomicAdd(&hdr->lse_ticket, 1) == static_cast<int>(gridDim.x) - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  double a = 0.0;
+  for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += kLseThreads) a += __ldcg(p.loss_part + i);
+  const double all = head_block_sum(a, red);
+  if (threadIdx.x == 0) *p.loss = hdr->w.loss_scale * all;
+}
+
+// ------------------------------------------------------------------ pairs
+// One block per preference pair: the log-probability of both sequences (fixed
+// order), x = beta ((Lc - Lr) - (Rc - Rr)), the loss softplus(-x), and the factor
+// sigmoid(-x) of the pair's rows (positive for the chosen sequence).
+constexpr int kPairThreads = 128;
+
+__global__ void __launch_bounds__(kPairThreads) k_head_pairs(const HeadParams p) {
+  __shared__ double red[kPairThreads];
+  __shared__ int last;
+  HeadHeader* hdr = p.hdr;
+  if (hdr->w.status != 0) return;
+  const int pr = blockIdx.x;
+  double L[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int a = p.offsets[2 * pr + q], b = p.offsets[2 * pr + q + 1];
+    double s = 0.0;
+    for (int t = a + static_cast<int>(threadIdx.x); t < b; t += kPairThreads) {
+      const int c = p.cidx[t];
+      if (c >= 0) s += p.rowterm[c] - static_cast<double>(p.lse2[c]) * 0.6931471805599453;
+    }
+    L[q] = head_block_sum(s, red);
+  }
+  double x = L[0] - L[1];
+  if (p.ref != nullptr) x -= static_cast<double>(p.ref[2 * pr]) - static_cast<double>(p.ref[2 * pr + 1]);
+  x *= p.beta;
+  const double ex = exp(-fabs(x));
+  const double sig = (x >= 0.0 ? ex : 1.0) / (1.0 + ex);           // sigmoid(-x)
+  const float f = static_cast<float>(sig);
+  const float lf = log2f(f);
+  for (int q = 0; q < 2; ++q) {
+    const int a = p.offsets[2 * pr + q], b = p.offsets[2 * pr + q + 1];
+    for (int t = a + static_cast<int>(threadIdx.x); t < b; t += kPairThreads) {
+      const int c = p.cidx[t];
+      if (c < 0) continue;
+      p.coef[t] = q == 0 ? f : -f;
+      p.b2[c] = lf - p.lse2[c];
+    }
+  }
+  if (threadIdx.x == 0) {
+    if (p.logp_out != nullptr) {
+      p.logp_out[2 * pr] = static_cast<float>(L[0]);
+      p.logp_out[2 * pr + 1] = static_cast<float>(L[1]);
+    }
+    p.loss_part[pr] = fmax(-x, 0.0) + log1p(ex) + (x != x ? x : 0.0);
+    __threadfence();
+    last = atomicAdd(&hdr->pairs_ticket, 1) == static_cast<int>(gridDim.x) - 1;
+  }
+  __syncthreads();
+  if (!last || p.loss == nullptr) return;
+  __threadfence();
+  double a = 0.0;
+  for (int i = threadIdx.x; i < p.P; i += kPairThreads) a += __ldcg(p.loss_part + i);
+  const double all = head_block_sum(a, red);
+  if (threadIdx.x == 0) *p.loss = hdr->w.loss_scale * all;
+}
+
+// ------------------------------------------------------------------ dh
+// dH[t] = g s w_t (sum over splits of the dense part - the sparse part), four
+// columns per thread; rows that do not count are zero.
+struct HeadDhParams {
+  int T, D, DP, S;
+  int64_t Tc;
+  const int* cidx;
+  const float* coef;
+  const float* part;      // [S, Tc, DP]
+  const float* sparse;    // [Tc, DP]
+  void* dH;
+  int bf16, accumulate;
+  const HeadHeader* hdr;
+};
+
+__global__ void __launch_bounds__(256) k_head_dh(const HeadDhParams p) {
+  if (p.hdr->w.status != 0) return;
+  const int per_row = p.D / 4;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t t = i / per_row;
+  if (t >= p.T) return;
+  const int col = static_cast<int>(i - t * per_row) * 4;
+  const int c = p.cidx[t];
+  float4 g = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c >= 0) {
+    const float* src = p.part + static_cast<int64_t>(c) * p.DP + col;
+    const int64_t stride = p.Tc * p.DP;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < p.S; ++s) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(src + s * stride));
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
+    }
+    const float4 q = __ldg(reinterpret_cast<const float4*>(p.sparse + static_cast<int64_t>(c) * p.DP + col));
+    const float f = p.hdr->w.grad_scale * p.coef[t];
+    g = make_float4(__fmul_rn(a.x - q.x, f), __fmul_rn(a.y - q.y, f), __fmul_rn(a.z - q.z, f), __fmul_rn(a.w - q.w, f));
+  }
+  const int64_t o = t * p.D + col;
+  if (p.bf16) {
+    uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.dH) + o);
+    if (p.accumulate) {
+      const uint2 old = *dst;
+      g.x = __fadd_rn(g.x, __uint_as_float(old.x << 16));
+      g.y = __fadd_rn(g.y, __uint_as_float(old.x & 0xFFFF0000u));
+      g.z = __fadd_rn(g.z, __uint_as_float(old.y << 16));
+      g.w = __fadd_rn(g.w, __uint_as_float(old.y & 0xFFFF0000u));
+    }
+    *dst = make_uint2(pack_bf16x2(g.x, g.y), pack_bf16x2(g.z, g.w));
+  } else {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.dH) + o);
+    if (p.accumulate) {
+      const float4 old = *dst;
+      g.x = __fadd_rn(g.x, old.x);
+      g.y = __fadd_rn(g.y, old.y);
+      g.z = __fadd_rn(g.z, old.z);
+      g.w = __fadd_rn(g.w, old.w);
+    }
+    *dst = g;
+  }
+}
+
+}  // namespace cutbce
