@@ -218,12 +218,18 @@ constexpr int kMaxHeadSplits = 148;
 
 struct HeadPlan {
   int DP, BN, S, tps, n_vtiles, n_blk;
+  bool fused;                    // the dH pass takes the row sums: no log-sum-exp pass of its own
   int64_t Tc;
-  size_t o_hdr, o_blk, o_cls, o_cidx, o_orig, o_coef, o_b2, o_lse2, o_term, o_hc, o_lpart, o_part, o_sparse, o_dhpart,
+  size_t o_hdr, o_blk, o_cls, o_cidx, o_orig, o_coef, o_off16, o_lse2, o_term, o_hc, o_lpart, o_part, o_wide, o_m2, o_h2, o_low2, o_rescale, o_sparse, o_dhpart,
       o_keys, o_share, o_usum, o_first, total;
   SortBuffers sort;
   size_t clear_bytes;            // header and histograms
 };
+
+// A call that needs both the log-sum-exps and dH can take the row sums in the dH
+// pass, with a bound as the exponentials' reference (k_head_ref): it saves the
+// log-sum-exp pass and costs a read of E's norms and two small launches.
+constexpr int64_t kFusedLogits = 1000000;
 
 // dH partials per position: about 16 work items per SM, at most kMaxSplits splits;
 // with few position tiles enough splits for one work item per SM.
@@ -232,6 +238,7 @@ void plan_head(const HeadProblem& p, bool dH, bool dE, bool lse_pass, HeadPlan& 
   pl.BN = pl.DP > 128 ? 64 : 128;
   pl.n_vtiles = static_cast<int>(ceil_div(p.V, pl.BN));
   pl.n_blk = static_cast<int>(ceil_div(p.T, 256));
+  pl.fused = lse_pass && dH && p.T * p.V >= kFusedLogits;
   pl.Tc = round_up(p.T, kTileM) + kTileM;
   const int64_t nT = ceil_div(p.T, kTileM);
   int64_t s0 = std::max<int64_t>(std::min<int64_t>(ceil_div(16 * 148, nT), kMaxSplits),
@@ -250,12 +257,17 @@ void plan_head(const HeadProblem& p, bool dH, bool dE, bool lse_pass, HeadPlan& 
   pl.o_cidx = l.take(4 * T);
   pl.o_orig = l.take(4 * Tc);
   pl.o_coef = l.take(4 * T);
-  pl.o_b2 = l.take(4 * Tc);
+  pl.o_off16 = dE ? l.take(32 * Tc) : 0;
   pl.o_lse2 = l.take(4 * Tc);
   pl.o_term = l.take(8 * Tc);
   pl.o_hc = l.take(2 * Tc * pl.DP);
   pl.o_lpart = l.take(8 * std::max<size_t>(static_cast<size_t>(p.P), Tc / kLseThreads));
   pl.o_part = lse_pass ? l.take(8 * static_cast<size_t>(pl.S) * 4 * Tc) : 0;
+  pl.o_wide = pl.fused ? l.take(8 * static_cast<size_t>(pl.S) * 4 * Tc) : 0;
+  pl.o_m2 = pl.fused ? l.take(4 * Tc) : 0;
+  pl.o_h2 = pl.fused ? l.take(4 * Tc) : 0;
+  pl.o_low2 = pl.fused ? l.take(4 * Tc) : 0;
+  pl.o_rescale = l.take(4 * Tc);
   pl.o_sparse = dH ? l.take(4 * Tc * pl.DP) : 0;
   pl.o_dhpart = dH ? l.take(4 * static_cast<size_t>(pl.S) * Tc * pl.DP) : 0;
   pl.o_keys = dE ? l.take(4 * TK) : 0;
@@ -266,10 +278,10 @@ void plan_head(const HeadProblem& p, bool dH, bool dE, bool lse_pass, HeadPlan& 
 }
 
 template <int DP, int kPass>
-cudaError_t launch_softmax(int grid, const CUtensorMap& s, const CUtensorMap& x, const SoftmaxParams& sp,
-                           cudaStream_t st) {
+cudaError_t launch_softmax(int grid, const CUtensorMap& s, const CUtensorMap& x, const CUtensorMap& o,
+                           const SoftmaxParams& sp, cudaStream_t st) {
   auto kern = k_softmax<DP, kPass>;
-  constexpr uint32_t smem = SoftmaxCfg<DP, kPass != kPassLse>::SMEM_BYTES;
+  constexpr uint32_t smem = SoftmaxCfg<DP, kPass>::SMEM_BYTES;
   static std::atomic<uint64_t> configured{0};   // the attribute belongs to the current device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -281,18 +293,18 @@ cudaError_t launch_softmax(int grid, const CUtensorMap& s, const CUtensorMap& x,
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_acq_rel);
   }
-  kern<<<grid, kTileThreads, smem, st>>>(s, x, sp);
+  kern<<<grid, kTileThreads, smem, st>>>(s, x, o, sp);
   return cudaGetLastError();
 }
 
 template <int kPass>
-cudaError_t launch_softmax_dp(int DP, int grid, const CUtensorMap& s, const CUtensorMap& x, const SoftmaxParams& sp,
-                              cudaStream_t st) {
+cudaError_t launch_softmax_dp(int DP, int grid, const CUtensorMap& s, const CUtensorMap& x, const CUtensorMap& o,
+                              const SoftmaxParams& sp, cudaStream_t st) {
   switch (DP) {
-    case 64: return launch_softmax<64, kPass>(grid, s, x, sp, st);
-    case 128: return launch_softmax<128, kPass>(grid, s, x, sp, st);
-    case 192: return launch_softmax<192, kPass>(grid, s, x, sp, st);
-    case 256: return launch_softmax<256, kPass>(grid, s, x, sp, st);
+    case 64: return launch_softmax<64, kPass>(grid, s, x, o, sp, st);
+    case 128: return launch_softmax<128, kPass>(grid, s, x, o, sp, st);
+    case 192: return launch_softmax<192, kPass>(grid, s, x, o, sp, st);
+    case 256: return launch_softmax<256, kPass>(grid, s, x, o, sp, st);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -365,9 +377,17 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   hp.keys = dE ? at<int>(ws, pl.o_keys) : nullptr;
   hp.share = dE ? at<float>(ws, pl.o_share) : nullptr;
   hp.coef = at<float>(ws, pl.o_coef);
-  hp.b2 = at<float>(ws, pl.o_b2);
+  hp.off16 = dE ? at<__nv_bfloat16>(ws, pl.o_off16) : nullptr;
   hp.lse2 = at<float>(ws, pl.o_lse2);
   hp.lse_in = lse_in;
+  hp.c2 = kLog2eF / p.tau;
+  if (pl.fused) {
+    hp.m2 = at<float>(ws, pl.o_m2);
+    hp.h2 = at<float>(ws, pl.o_h2);
+    hp.low2 = at<float>(ws, pl.o_low2);
+  }
+  hp.rescale = at<float>(ws, pl.o_rescale);
+  hp.row_blocks = static_cast<int>(ceil_div(p.T + 256, 8));
   hp.part = lse_in == nullptr ? at<float2>(ws, pl.o_part) : nullptr;
   hp.slots = 4 * pl.S;
   hp.Tc = pl.Tc;
@@ -381,7 +401,10 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   {
     LaunchScope ls(CUTBCE_KERNEL_HEAD_PREP, st);
     k_head_rows<<<static_cast<unsigned>(pl.n_blk), 256, 0, st>>>(hp);
-    k_head_gather<<<static_cast<unsigned>(ceil_div(p.T + 256, 8)), 256, 0, st>>>(hp);
+    // the table's norms, when needed: up to 8 blocks an SM beside the positions' blocks
+    const int64_t norm_blocks = pl.fused ? std::min<int64_t>(ceil_div(p.V, 128), 8 * 148) : 0;
+    k_head_gather<<<static_cast<unsigned>(hp.row_blocks + norm_blocks), 256, 0, st>>>(hp);
+    if (pl.fused) k_head_ref<<<static_cast<unsigned>(ceil_div(pl.Tc, 256)), 256, 0, st>>>(hp);
     CUTBCE_CK(cudaGetLastError());
   }
   SoftmaxParams sp{};
@@ -400,10 +423,26 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
     return CUTBCE_ERR_CUDA;
   const int64_t row_items = static_cast<int64_t>(pl.S) * (pl.Tc / kTileM);
   const int row_grid = static_cast<int>(std::min<int64_t>({static_cast<int64_t>(dev.sms), row_items, static_cast<int64_t>(kMaxCtas)}));
+  auto row_pass = [&]() -> cudaError_t {
+    LaunchScope ls(CUTBCE_KERNEL_HEAD_ROW_PASS, st);
+    sp.dh_part = at<float>(ws, pl.o_dhpart);
+    return launch_softmax_dp<kPassRows>(pl.DP, row_grid, m_rows_s, m_items_x, m_items_x, sp, st);
+  };
   if (lse_in == nullptr) {
-    LaunchScope ls(CUTBCE_KERNEL_HEAD_LSE_PASS, st);
-    sp.part = at<float2>(ws, pl.o_part);
-    CUTBCE_CK(launch_softmax_dp<kPassLse>(pl.DP, row_grid, m_rows_s, m_items_x, sp, st));
+    {
+      LaunchScope ls(CUTBCE_KERNEL_HEAD_LSE_PASS, st);
+      sp.part = at<float2>(ws, pl.fused ? pl.o_wide : pl.o_part);
+      sp.only_wide = pl.fused ? 1 : 0;
+      CUTBCE_CK(launch_softmax_dp<kPassLse>(pl.DP, row_grid, m_rows_s, m_items_x, m_items_x, sp, st));
+    }
+    if (pl.fused) {
+      sp.off2 = hp.m2;
+      sp.part = at<float2>(ws, pl.o_part);
+      sp.wide_part = at<float2>(ws, pl.o_wide);
+      CUTBCE_CK(row_pass());
+    }
+    sp.part = nullptr;
+    sp.wide_part = nullptr;
   }
   {
     LaunchScope ls(CUTBCE_KERNEL_HEAD_FINISH, st);
@@ -412,11 +451,9 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
     CUTBCE_CK(cudaGetLastError());
   }
   if (dH) {
-    {
-      LaunchScope ls(CUTBCE_KERNEL_HEAD_ROW_PASS, st);
+    if (!pl.fused) {
       sp.off2 = hp.lse2;
-      sp.dh_part = at<float>(ws, pl.o_dhpart);
-      CUTBCE_CK(launch_softmax_dp<kPassRows>(pl.DP, row_grid, m_rows_s, m_items_x, sp, st));
+      CUTBCE_CK(row_pass());
     }
     HeadDhParams dp{};
     dp.T = hp.T;
@@ -428,6 +465,7 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
     dp.coef = hp.coef;
     dp.part = at<float>(ws, pl.o_dhpart);
     dp.sparse = hp.sparse;
+    dp.rescale = hp.rescale;
     dp.dH = out.dH;
     dp.bf16 = out.grad_dtype == CUTBCE_GRAD_BF16;
     dp.accumulate = (out.accumulate & CUTBCE_ACCUMULATE_DH) != 0;
@@ -454,15 +492,16 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
     gp.status = status;
     CUTBCE_CK(cudaMemsetAsync(gp.first, 0xFF, 4 * static_cast<size_t>(p.V), st));
     if ((s = run_sums(gp, true, pl.sort.chunks, st)) != CUTBCE_OK) return s;
-    sp.off2 = hp.b2;
     sp.first = gp.first;
     sp.sparse = at<float>(ws, pl.o_usum);
     sp.dE = out.dE;
     sp.de_bf16 = out.grad_dtype == CUTBCE_GRAD_BF16;
     sp.de_acc = (out.accumulate & CUTBCE_ACCUMULATE_DE) != 0;
+    CUtensorMap m_off;
+    if (!make_map_sw32(&m_off, hp.off16, pl.Tc, pl.BN)) return CUTBCE_ERR_CUDA;
     const int grid = static_cast<int>(std::min<int64_t>({static_cast<int64_t>(dev.sms), ceil_div(p.V, kTileM), static_cast<int64_t>(kMaxCtas)}));
     LaunchScope ls(CUTBCE_KERNEL_HEAD_ITEM_PASS, st);
-    CUTBCE_CK(launch_softmax_dp<kPassItems>(pl.DP, grid, m_items_s, m_rows_x, sp, st));
+    CUTBCE_CK(launch_softmax_dp<kPassItems>(pl.DP, grid, m_items_s, m_rows_x, m_off, sp, st));
   }
   return CUTBCE_OK;
 }
@@ -473,7 +512,7 @@ cutbce_status head_workspace(const HeadProblem& p, int outputs, size_t* bytes) {
   const cutbce_status s = check_head(p, false);
   if (s != CUTBCE_OK) return s;
   HeadPlan pl;
-  plan_head(p, (outputs & CUTBCE_OUT_DH) != 0, (outputs & CUTBCE_OUT_DE) != 0, (outputs & CUTBCE_OUT_LOSS) != 0, pl);
+  plan_head(p, (outputs & CUTBCE_OUT_DH) != 0, (outputs & CUTBCE_OUT_DE) != 0, true, pl);   // the larger layout
   *bytes = pl.total;
   return CUTBCE_OK;
 }

@@ -80,6 +80,20 @@ inline bool make_map(CUtensorMap* m, const void* base, int64_t cols, int64_t row
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A bf16 matrix [rows, 16] of 32-byte rows, read in boxes of `box_rows` rows with
+// the 32-byte swizzle.
+inline bool make_map_sw32(CUtensorMap* m, const void* base, int64_t rows, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {16, static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {32};
+  cuuint32_t box[2] = {16, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // ---------------------------------------------------------------- launch profiling (benchmarks)
 struct ProfRecord {
   int kind;

@@ -9,9 +9,12 @@
 //          rounded to bf16, written back over the logits in tensor memory and
 //          contracted with the item tile: dH partial += P E.
 //   kItems a CTA owns 128 items and streams the positions: P = 2^(c z + b_t),
-//          b_t = log2 |w_t| - l_t, and dE += +-P H.  Rows are compacted by the
-//          sign of w_t (the negative ones from a tile boundary on), so the sign
-//          is the negate-A bit of the contraction's instruction descriptor.
+//          b_t = log2 |w_t| - l_t, and dE += +-P H.  Here a logit's row offset
+//          runs along the columns of the tile; b_t / c, split into three bf16
+//          values (24 bits), enters as one more K step of the logit MMA against
+//          ones, so the epilogue loads nothing.  Rows are compacted by the sign
+//          of w_t (the negative ones from a tile boundary on), so the sign is
+//          the negate-A bit of the contraction's instruction descriptor.
 //
 // c = log2(e) / tau.  Warp roles, tensor-memory layout and hand-over of the tiles
 // follow the BCE engine: warp 0 loads by TMA, warp 1 issues the MMAs, 16 epilogue
@@ -31,23 +34,27 @@ namespace cutbce {
 
 enum : int { kPassLse = 0, kPassRows = 1, kPassItems = 2 };
 
-template <int DP, bool kGrad>
+template <int DP, int kPass>
 struct SoftmaxCfg {
+  static constexpr bool kGrad = kPass != kPassLse;
+  static constexpr bool kItems = kPass == kPassItems;
   static constexpr int GROUPS = 2;
   static constexpr int GROUP_WARPS = kNumEpiWarps / GROUPS;
   static constexpr int SLABS = GROUP_WARPS / 4;
   static constexpr int BN = DP <= 128 ? 128 : 64;           // streamed rows per tile
   static constexpr int NKB = DP / 64;
-  static constexpr int NX = DP == 64 ? 12 : DP == 128 ? 5 : DP == 192 ? 7 : 4;
+  static constexpr int NX = DP == 64 ? (kItems ? 9 : 12) : DP == 128 ? 5 : DP == 192 ? (kItems ? 6 : 7) : 4;
   static constexpr int NZ = kGrad ? 3 : 4;                  // logit buffers in tensor memory
   static constexpr uint32_t S_BYTES = kTileM * DP * 2;
   static constexpr uint32_t X_BYTES = BN * DP * 2;
+  static constexpr uint32_t O_BYTES = kItems ? BN * 32 : 0;         // exponent offsets of a streamed tile (16 bf16 a row)
+  static constexpr uint32_t ONES_BYTES = kItems ? kTileM * 32 : 0;  // their other operand
   static constexpr int ZC = BN / SLABS;                     // logit columns per epilogue warp (64 or 32)
   static constexpr int ACC_COL = 3 * BN;
   static constexpr int S_COL = ACC_COL + DP;
   static constexpr bool S_IN_TMEM = kGrad && S_COL + DP / 2 <= 512;
   static constexpr int NUM_BARS = 2 + 2 * NX + 3 * NZ + 3;
-  static constexpr uint32_t SMEM_BYTES = 1024 + S_BYTES + NX * X_BYTES + NUM_BARS * 8 + 16 + 64;
+  static constexpr uint32_t SMEM_BYTES = 1024 + S_BYTES + NX * (X_BYTES + O_BYTES) + ONES_BYTES + NUM_BARS * 8 + 16 + 64;
   static_assert(ACC_COL + DP <= 512 && NZ * BN <= 512, "TMEM budget");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static_assert(SMEM_BYTES > 232448 / 2, "one CTA per SM keeps the TMEM allocation uncontended");
@@ -58,8 +65,10 @@ struct SoftmaxParams {
   int64_t Tc;                  // rows of the compacted buffers
   HeadHeader* hdr;
   float c2;                    // log2(e) / tau
-  const float* off2;           // kRows: [Tc] l_t, kItems: [Tc] b_t (log2 domain)
-  float2* part;                // kLse: [splits * groups * slabs, Tc] (maximum, sum)
+  const float* off2;           // kRows: [Tc] l_t (log2 domain)
+  float2* part;                // kLse, and kRows where it takes the sums: [splits * groups * slabs, Tc] (reference, sum)
+  const float2* wide_part;     // kRows: partials of the log-sum-exp pass, the reference where hdr->wide is set
+  int only_wide;               // kLse: run only where hdr->wide is set
   float* dh_part;              // kRows: [splits, Tc, DP]
   const int* first;            // kItems: [V] row of `sparse` of each item, -1 none
   const float* sparse;         // kItems: [.., D] sparse part of dE, unscaled
@@ -68,6 +77,44 @@ struct SoftmaxParams {
   int nsplit, tiles_per_split, n_item_tiles_bn;
   long long timeout_ns;
 };
+
+// Pairs of every 16 whose exponential runs on the FMA pipe instead of the SFU.
+// Measured at T V = 9.0e9 logits, D = 64, for 0 / 2 / 4 / 6 / 8 pairs: log-sum-exp
+// pass 2.41 / 2.23 / 2.10 / 2.16 / 2.42 ms, dH pass 2.52 / 2.36 / 2.43 / 2.60 /
+// 2.65 ms, dE pass 2.56 / 2.44 / 2.53 ms (0 / 2 / 4).
+constexpr int kPolyLse = 4, kPolyRows = 2, kPolyItems = 2;
+// 2^x of a pair on the FMA pipe, x clamped below at -125: as exp2_poly3_pair, with
+// the degree chosen by what the value feeds.  kDegree 3 (relative error 7.5e-5) for
+// values that are rounded to bf16 next, 4 (2.7e-6) for the sums of a log-sum-exp.
+template <int kDegree>
+__device__ __forceinline__ float2 exp2_fma_pair(float2 x) {
+  constexpr float kShift = 12582912.0f;   // 1.5 * 2^23
+  x = f2(fmaxf(x.x, -125.f), fmaxf(x.y, -125.f));
+  const float2 j = __fadd2_rn(x, f2(kShift, kShift));
+  const float2 jr = __fadd2_rn(j, f2(-kShift, -kShift));
+  const float2 f = __ffma2_rn(jr, f2(-1.f, -1.f), x);
+  float2 p;
+  if (kDegree == 3) {
+    p = __ffma2_rn(f2(0.0551716685f, 0.0551716685f), f, f2(0.2426111251f, 0.2426111251f));
+    p = __ffma2_rn(p, f, f2(0.6932609677f, 0.6932609677f));
+    p = __ffma2_rn(p, f, f2(0.9999280572f, 0.9999280572f));
+  } else {
+    p = __ffma2_rn(f2(0.0095701022f, 0.0095701022f), f, f2(0.0559178591f, 0.0559178591f));
+    p = __ffma2_rn(p, f, f2(0.2402474433f, 0.2402474433f));
+    p = __ffma2_rn(p, f, f2(0.6931217909f, 0.6931217909f));
+    p = __ffma2_rn(p, f, f2(0.9999992847f, 0.9999992847f));
+  }
+  uint32_t rx, ry;
+  asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(rx) : "r"(__float_as_uint(j.x)), "r"(1u << 23), "r"(__float_as_uint(p.x)));
+  asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(ry) : "r"(__float_as_uint(j.y)), "r"(1u << 23), "r"(__float_as_uint(p.y)));
+  return f2(__uint_as_float(rx), __uint_as_float(ry));
+}
+// Pair e / 2 of a chunk of 16: `kPoly` of them, evenly spread, run on the FMA pipe.
+template <int kPoly, int kDegree>
+__device__ __forceinline__ float2 exp2_pair(int pair, float2 x) {
+  if ((pair * kPoly) % 16 < kPoly) return exp2_fma_pair<kDegree>(x);
+  return f2(ex2_approx(x.x), ex2_approx(x.y));
+}
 
 // 32 logits of one row -> their exponentials.  kTail: columns from `valid` on are
 // outside the table and count as -infinity.
@@ -79,10 +126,11 @@ __device__ __forceinline__ void mask_tail(uint32_t (&r)[32], int valid) {
 
 template <int DP, int kPass>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    k_softmax(const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmX, SoftmaxParams p) {
+    k_softmax(const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmX,
+              const __grid_constant__ CUtensorMap tmO, SoftmaxParams p) {
   constexpr bool kGrad = kPass != kPassLse;
   constexpr bool kItems = kPass == kPassItems;
-  using Cfg = SoftmaxCfg<DP, kGrad>;
+  using Cfg = SoftmaxCfg<DP, kPass>;
   constexpr int BN = Cfg::BN, NKB = Cfg::NKB, NX = Cfg::NX, NZ = Cfg::NZ, ZC = Cfg::ZC;
   constexpr uint32_t S_BYTES = Cfg::S_BYTES, X_BYTES = Cfg::X_BYTES;
 
@@ -90,7 +138,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sS = smem;
   uint8_t* sX = sS + S_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sX + NX * X_BYTES);
+  uint8_t* sO = sX + NX * X_BYTES;                // kItems: [NX] offsets, 32-byte rows, 32-byte swizzle
+  uint8_t* sOne = sO + NX * Cfg::O_BYTES;         // kItems: 128 rows of (1, 1, 1, 0, ..)
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sOne + Cfg::ONES_BYTES);
   uint64_t* bar_sfull = bars + 0;                 // stationary tile landed (TMA)
   uint64_t* bar_sempty = bars + 1;                // stationary tile no longer read (commit)
   uint64_t* bar_xfull = bars + 2;                 // [NX] streamed tile landed
@@ -106,14 +156,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   WsHeader* hdr = &p.hdr->w;
-  __shared__ int s_status, s_rows, s_neg0;
+  __shared__ int s_status, s_rows, s_neg0, s_wide;
   if (threadIdx.x == 0) {
     s_status = *reinterpret_cast<volatile int*>(&hdr->status);
     s_rows = p.hdr->n_rows;
     s_neg0 = p.hdr->neg0;
+    s_wide = p.hdr->wide;
   }
   __syncthreads();
-  if (s_status != 0) return;
+  if (s_status != 0 || (kPass == kPassLse && p.only_wide && !s_wide)) return;
   const int n_rows = s_rows;                      // compacted rows, a multiple of 128
   const int neg_tile = s_neg0 / BN;               // kItems: first streamed tile of negative rows
   const int n_row_tiles = n_rows / kTileM;
@@ -152,6 +203,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmS);
     tma_prefetch_desc(&tmX);
+    if (kItems) tma_prefetch_desc(&tmO);
+  }
+  if (kItems) {
+    // the two 16-byte halves of a row trade places in rows 4..7 of each 8 (32-byte swizzle)
+    if (threadIdx.x < kTileM) {
+      const int r = threadIdx.x, sw = (r >> 2) & 1;
+      uint4* dst = reinterpret_cast<uint4*>(sOne + 32 * r);
+      dst[sw] = make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u);
+      dst[sw ^ 1] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
   }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
@@ -193,7 +255,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(bar_xfull + st, X_BYTES);
+          mbar_arrive_expect_tx(bar_xfull + st, X_BYTES + Cfg::O_BYTES);
+          if (kItems) tma_load_2d(sO + st * Cfg::O_BYTES, &tmO, 0, (x0 + j) * BN, bar_xfull + st);
 #pragma unroll
           for (int kb = 0; kb < NKB; ++kb)
             tma_load_2d(sX + st * X_BYTES + kb * (BN * 128), &tmX, kb * 64, (x0 + j) * BN, bar_xfull + st);
@@ -222,6 +285,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     constexpr int kKsPerSlab = ZC / 16;
     const uint64_t dS = smem_desc_sw128(smem_u32(sS), 16, 1024);
     const uint64_t dXk = smem_desc_sw128(smem_u32(sX), 16, 1024);
+    const uint64_t dO = smem_desc_sw32(smem_u32(sO)), dOne = smem_desc_sw32(smem_u32(sOne));
     const uint64_t dXmn = smem_desc_sw128(smem_u32(sX), BN * 128, 1024);
     const uint32_t tAcc = tmem_base + Cfg::ACC_COL, tS = tmem_base + Cfg::S_COL;
     int zi = blockIdx.x, zj = 0, zn = 0, gi = zi, gj = 0, gn = 0;
@@ -270,6 +334,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               else umma_bf16(tD, dS + static_cast<uint32_t>((ks >> 2) * (kTileM * 8) + (ks & 3) * 2), bd, idesc_z,
                              ks > 0 ? 1u : 0u);
             }
+            if (kItems) umma_bf16(tD, dOne, dO + zst * (Cfg::O_BYTES >> 4), idesc_z, 1u);
             umma_commit(bar_zfull + zb);
             if (!kGrad) umma_commit(bar_xempty + zst);
             if (!Cfg::S_IN_TMEM && zj + 1 == zn) umma_commit(bar_sempty);
@@ -371,9 +436,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x, ++ic) {
       int s_row0, x0, n, split;
       item(i, s_row0, x0, n, split);
-      float m = -1e30f, sum = 0.f;                // kLse: running maximum (log2 domain) and sum
-      float off = 0.f;                            // kRows: -l_t
-      if (kPass == kPassRows) off = -__ldg(p.off2 + s_row0 + row);
+      float m = -1e30f, sum = 0.f;                // reference (log2 domain) and sum of 2^(x - m)
+      float off = 0.f;                            // kRows: -m
+      if (kPass == kPassRows) {
+        m = __ldg(p.off2 + s_row0 + row);
+        if (p.wide_part != nullptr && s_wide) {
+          // the row's log-sum-exp from the partials of the pass before
+          const int slots = p.nsplit * Cfg::GROUPS * Cfg::SLABS;
+          float mx = -3.0e38f, s = 0.f;
+          for (int k = 0; k < slots; ++k) mx = fmaxf(mx, p.wide_part[k * p.Tc + s_row0 + row].x);
+          for (int k = 0; k < slots; ++k) {
+            const float2 v = p.wide_part[k * p.Tc + s_row0 + row];
+            s += v.y * exp2f(v.x - mx);
+          }
+          m = mx + log2f(s);
+        }
+        off = -m;
+      }
       const int j0 = static_cast<int>((grp + Cfg::GROUPS - cnt % Cfg::GROUPS) % Cfg::GROUPS);
       for (int j = j0; j < n; j += Cfg::GROUPS) {
         const uint32_t c = cnt + j, bz = c % NZ;
@@ -409,18 +488,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               const float2 x = __ffma2_rn(f2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), c2, nm);
-              s2 = __fadd2_rn(s2, f2(ex2_approx(x.x), ex2_approx(x.y)));
+              s2 = __fadd2_rn(s2, exp2_pair<kPolyLse, 4>(e >> 1, x));
             }
             sum += s2.x + s2.y;
           } else {
             uint32_t pk[16];
+            float2 s2 = f2(0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float2 o = kItems ? __ldg(reinterpret_cast<const float2*>(p.off2 + col + e)) : f2(off, off);
-              const float2 x = __ffma2_rn(f2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), c2, o);
-              pk[e >> 1] = pack_bf16x2(ex2_approx(x.x), ex2_approx(x.y));
+              const float2 z = f2(__uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+              const float2 x = kItems ? __fmul2_rn(z, c2) : __ffma2_rn(z, c2, f2(off, off));
+              const float2 y = kItems ? exp2_pair<kPolyItems, 3>(e >> 1, x) : exp2_pair<kPolyRows, 4>(e >> 1, x);
+              if (!kItems) s2 = __fadd2_rn(s2, y);
+              pk[e >> 1] = pack_bf16x2(y.x, y.y);
             }
             tmem_st16(tmem_base + lane_base + bz * BN + slab * ZC + ch * 16, pk);
+            if (!kItems) sum += s2.x + s2.y;
           }
         }
         if constexpr (kGrad) {
@@ -430,7 +513,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       if (!ok) break;
-      if constexpr (kPass == kPassLse) {
+      if (kPass == kPassLse || (kPass == kPassRows && p.part != nullptr)) {
         const int slot = (split * Cfg::GROUPS + static_cast<int>(grp)) * Cfg::SLABS + slab;
         p.part[static_cast<int64_t>(slot) * p.Tc + s_row0 + row] = make_float2(m, sum);
       }

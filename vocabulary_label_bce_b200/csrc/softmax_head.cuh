@@ -36,6 +36,8 @@ struct HeadHeader {
   int rows_ticket;          // blocks done, per kernel that has a last block
   int lse_ticket;
   int pairs_ticket;
+  unsigned emax2;           // bits of max |e_v|^2 (with a dH pass that takes the row sums too)
+  int wide;                 // 1: some row's logits may lie too far below its bound (see k_head_ref)
 };
 static_assert(sizeof(HeadHeader) <= 256, "the workspace header is 256 bytes");
 
@@ -66,10 +68,16 @@ struct HeadParams {
   int* keys;                     // [T * K] ids of the pairs (-1 none), or null
   float* share;                  // [T * K] q of the pairs, or null
   float* coef;                   // [T] signed factor of the row's gradient
-  float* b2;                     // [Tc] log2 |factor| - log2-domain lse (-inf for padding)
+  __nv_bfloat16* off16;          // [Tc, 16] (log2 |factor| - lse) tau in three bf16 pieces, then zeros (with dE)
   float* lse2;                   // [Tc] lse in the log2 domain
   const float* lse_in;           // [T] lse of an earlier forward, or null
-  const float2* part;            // [slots, Tc] (max, sum) partials in the log2 domain
+  float* m2;                     // [Tc] reference of the row's exponentials in the dH pass, or null
+  float* h2;                     // [Tc] |h|^2, with m2
+  float* low2;                   // [Tc] a logit that the row has (log2 domain), with m2
+  float c2;                      // log2(e) / tau
+  int row_blocks;                // blocks of the gather that take positions (the rest read E's norms)
+  float* rescale;                // [Tc] 2^(reference - lse): factor of the dense part of dH
+  const float2* part;            // [slots, Tc] (reference, sum) partials in the log2 domain
   int slots;
   int64_t Tc;                    // rows of the compacted buffers
   double* loss_part;             // per-block (distillation) or per-pair (preference) partials
@@ -78,7 +86,18 @@ struct HeadParams {
   float* logp_out;               // [2P] output or null
 };
 
-__device__ __forceinline__ int head_blocks_of(int T) { return (T + 255) / 256; }
+// The exponent offset u of a row of the item-owned pass as three bf16 values whose
+// sum is u to 24 bits; clamped to +-1e30 (2^(c u) is 0 there, as for padding).
+__device__ __forceinline__ void write_offset(const HeadParams& p, int64_t c, float u) {
+  if (p.off16 == nullptr) return;
+  if (u == u) u = fminf(fmaxf(u, -1e30f), 1e30f);
+  const float a = __bfloat162float(__float2bfloat16_rn(u));
+  const float b = __bfloat162float(__float2bfloat16_rn(u - a));
+  const float d = (u - a) - b;
+  uint4* o = reinterpret_cast<uint4*>(p.off16 + c * 16);
+  o[0] = make_uint4(pack_bf16x2(a, b), pack_bf16x2(d, 0.f), 0u, 0u);
+  o[1] = make_uint4(0u, 0u, 0u, 0u);
+}
 
 // ------------------------------------------------------------------ rows
 __global__ void __launch_bounds__(256) k_head_rows(const HeadParams p) {
@@ -195,9 +214,44 @@ __global__ void __launch_bounds__(256) k_head_rows(const HeadParams p) {
 // E are read kGatherU at a time.
 constexpr int kGatherU = 4;
 
+// Largest |e_v|^2 over the table, by the gather's blocks past the positions: eight
+// lanes a row, 16 bytes a lane.  The maximum is over float bits (all >= 0), so the
+// order of the atomics changes nothing; a NaN stays the maximum.
+__device__ void head_table_norm(const HeadParams& p) {
+  const int sub = threadIdx.x & 7;
+  const int64_t step = (static_cast<int64_t>(gridDim.x) - p.row_blocks) * 32;
+  unsigned best = 0u;
+  // every lane of a warp runs the same trips, so that the sums below are whole
+  for (int64_t v0 = (static_cast<int64_t>(blockIdx.x) - p.row_blocks) * 32; v0 < p.V; v0 += step) {
+    const int64_t v = v0 + (threadIdx.x >> 3);
+    float s = 0.f;
+    if (v < p.V) {
+      const uint4* src = reinterpret_cast<const uint4*>(p.E + v * p.D);
+      for (int i = sub; i < p.D / 8; i += 8) {
+        const uint4 x = __ldg(src + i);
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float a = __uint_as_float(u[k] << 16), b = __uint_as_float(u[k] & 0xFFFF0000u);
+          s = fmaf(a, a, fmaf(b, b, s));
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    best = max(best, __float_as_uint(s) & 0x7FFFFFFFu);
+  }
+  best = __reduce_max_sync(0xffffffffu, best);
+  if ((threadIdx.x & 31) == 0) atomicMax(&p.hdr->emax2, best);
+}
+
 __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
   const HeadHeader* hdr = p.hdr;
   if (hdr->w.status != 0) return;
+  if (static_cast<int>(blockIdx.x) >= p.row_blocks) {
+    head_table_norm(p);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + warp;
   const int pairs = p.DP / 64;                  // column pairs per lane (1 .. 4)
@@ -211,8 +265,9 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
     for (int i = 0; i < pairs; ++i) dst[lane + 32 * i] = 0u;
     if (lane == 0) {
       p.orig[c] = -1;
-      p.b2[c] = -INFINITY;
+      write_offset(p, c, -1e30f);
       p.lse2[c] = 0.f;
+      if (p.m2 != nullptr) p.h2[c] = p.low2[c] = 0.f;
     }
     return;
   }
@@ -293,6 +348,7 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
     if (lane == 0) id[0] = __ldg(p.ids + t);
   }
   double term = 0.0;
+  float zmax = -INFINITY;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int n = min(32, p.K - 32 * j);
@@ -337,6 +393,7 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
 #pragma unroll
       for (int u = 0; u < kGatherU; ++u) {
         if (w[u] == 0.f) continue;
+        zmax = fmaxf(zmax, z[u]);
         term += p.kind == kHeadDistill
                     ? static_cast<double>(w[u]) * (static_cast<double>(lw[u]) - static_cast<double>(z[u]) * p.inv_tau)
                     : static_cast<double>(z[u]);
@@ -348,6 +405,17 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (i < pairs) o[lane + 32 * i] = sp[i];
+  }
+  if (p.m2 != nullptr) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = fmaf(h[i].x, h[i].x, fmaf(h[i].y, h[i].y, s));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) {
+      p.h2[c] = s;
+      p.low2[c] = zmax * p.c2;
+    }
   }
   if (lane == 0) {
     p.cidx[t] = static_cast<int>(c);
@@ -370,6 +438,27 @@ __device__ __forceinline__ double head_block_sum(double v, double* red) {
   return r;
 }
 
+// ------------------------------------------------------------------ ref
+// The reference of a row's exponentials when the dH pass takes the row's sum on
+// the way: m = |h| max|e| c, a bound of every logit (Cauchy-Schwarz), so 2^(x - m)
+// never overflows.  It must not lie too far above the row's largest logit either:
+// terms below 2^-126 are lost, and with a gap of at most 70 (log2) the V < 2^31
+// lost terms are below 2^-25 of the sum.  The gap is bounded by a logit that the
+// row is known to have, its largest sparse target.  Rows beyond it set `wide`, and
+// then the log-sum-exp pass runs first and its result is the reference.
+constexpr float kMaxRefGap = 70.f;
+
+__global__ void __launch_bounds__(256) k_head_ref(const HeadParams p) {
+  HeadHeader* hdr = p.hdr;
+  if (hdr->w.status != 0) return;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (c >= hdr->n_rows) return;
+  const float bound = sqrtf(p.h2[c]) * sqrtf(__uint_as_float(hdr->emax2)) * p.c2;
+  const float m = bound * 1.0001f + 0.01f;                  // above the rounding of the norms
+  p.m2[c] = m;
+  if (!(m - p.low2[c] <= kMaxRefGap)) hdr->wide = 1;       // NaN counts as wide
+}
+
 // ------------------------------------------------------------------ lse
 // One thread per compacted row: joins the (max, sum) partials of the row's splits
 // and slabs (or takes the lse of an earlier forward), writes lse, the exponent
@@ -386,7 +475,7 @@ __global__ void __launch_bounds__(kLseThreads) k_head_lse(const HeadParams p) {
   double row_loss = 0.0;
   const int t = c < hdr->n_rows ? p.orig[c] : -1;
   if (t >= 0) {
-    float l2;
+    float l2, ref = 0.f;
     if (p.lse_in != nullptr) {
       l2 = p.lse_in[t] * 1.4426950408889634f;
     } else {
@@ -399,13 +488,15 @@ __global__ void __launch_bounds__(kLseThreads) k_head_lse(const HeadParams p) {
       }
       l2 = m + log2f(sum);
       if (sum != sum || m != m) l2 = NAN;
+      ref = m;
     }
+    p.rescale[c] = p.m2 != nullptr ? exp2f(ref - l2) : 1.f;
     p.lse2[c] = l2;
     const double lse = static_cast<double>(l2) * 0.6931471805599453;
     if (p.lse_out != nullptr) p.lse_out[t] = static_cast<float>(lse);
     if (p.kind == kHeadDistill) {
       const float w = p.weights != nullptr ? p.weights[t] : 1.f;
-      p.b2[c] = (p.weights != nullptr ? log2f(fabsf(w)) : 0.f) - l2;
+      write_offset(p, c, ((p.weights != nullptr ? log2f(fabsf(w)) : 0.f) - l2) / p.c2);
       row_loss = static_cast<double>(w) * p.tau * p.tau * (p.rowterm[c] + lse);
     }
   }
@@ -461,7 +552,7 @@ __global__ void __launch_bounds__(kPairThreads) k_head_pairs(const HeadParams p)
       const int c = p.cidx[t];
       if (c < 0) continue;
       p.coef[t] = q == 0 ? f : -f;
-      p.b2[c] = lf - p.lse2[c];
+      write_offset(p, c, (lf - p.lse2[c]) / p.c2);
     }
   }
   if (threadIdx.x == 0) {
@@ -492,6 +583,7 @@ struct HeadDhParams {
   const float* coef;
   const float* part;      // [S, Tc, DP]
   const float* sparse;    // [Tc, DP]
+  const float* rescale;   // [Tc] factor of the dense part
   void* dH;
   int bf16, accumulate;
   const HeadHeader* hdr;
@@ -520,7 +612,9 @@ __global__ void __launch_bounds__(256) k_head_dh(const HeadDhParams p) {
     }
     const float4 q = __ldg(reinterpret_cast<const float4*>(p.sparse + static_cast<int64_t>(c) * p.DP + col));
     const float f = p.hdr->w.grad_scale * p.coef[t];
-    g = make_float4(__fmul_rn(a.x - q.x, f), __fmul_rn(a.y - q.y, f), __fmul_rn(a.z - q.z, f), __fmul_rn(a.w - q.w, f));
+    const float r = p.rescale[c];
+    g = make_float4(__fmul_rn(fmaf(a.x, r, -q.x), f), __fmul_rn(fmaf(a.y, r, -q.y), f),
+                    __fmul_rn(fmaf(a.z, r, -q.z), f), __fmul_rn(fmaf(a.w, r, -q.w), f));
   }
   const int64_t o = t * p.D + col;
   if (p.bf16) {
