@@ -78,7 +78,7 @@ struct TileCfg {
   // when it fits, so the logit MMA reads only its B operand from shared memory.
   static constexpr int S_COL = ACC_COL + DP;
   static constexpr bool S_IN_TMEM = S_COL + DP / 2 <= TMEM_COLS;
-  static constexpr int NUM_BARS = 2 + 2 * NX + 3 * NZ + 3;  // see the kernel for the list
+  static constexpr int NUM_BARS = 2 + 2 * NX + 3 * NZ + 2 + GROUPS;  // see the kernel for the list
   // per epilogue warp: positives of its 32 rows, one word per 32 columns of its slab
   static constexpr int MASK_WORDS = ZC >= 32 ? ZC / 32 : 1;
   static constexpr uint32_t MASK_BYTES = kNumEpiWarps * 32 * MASK_WORDS * 4;

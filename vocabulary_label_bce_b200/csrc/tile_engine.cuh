@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint64_t* bar_zfree = bar_zfull + NZ;           // [NZ] buffer free: gradient MMA done (commit), or,
                                                   //      without a gradient, logits loaded (epilogue group)
   uint64_t* bar_gready = bar_zfree + NZ;          // [NZ] G tile written over the logits (epilogue group)
-  uint64_t* bar_accfull = bar_gready + NZ;        // gradient accumulator complete
-  uint64_t* bar_accempty = bar_accfull + 1;       // gradient accumulator read out
+  uint64_t* bar_accfull = bar_gready + NZ;        // [groups] gradient accumulator complete, for the group that reads it
+  uint64_t* bar_accempty = bar_accfull + Cfg::GROUPS;  // gradient accumulator read out
   uint64_t* bar_drain = bar_accempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::NUM_BARS);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(bar_zfree + b, kGrad ? 1 : Cfg::GROUP_WARPS * 32);
       mbar_init(bar_gready + b, Cfg::GROUP_WARPS * 32);
     }
-    mbar_init(bar_accfull, 1);
+    for (int g = 0; g < Cfg::GROUPS; ++g) mbar_init(bar_accfull + g, 1);
     mbar_init(bar_accempty, Cfg::GROUP_WARPS);
     mbar_init(bar_drain, 1);
     *abort_flag = 0;
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               }
               umma_commit(bar_zfree + gb);
               umma_commit(bar_xempty + gst);
-              if (last) umma_commit(bar_accfull);
+              if (last) umma_commit(bar_accfull + cg % Cfg::GROUPS);
             }
             __syncwarp();
             progressed = true;
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
     for (int k = 0; k < Cfg::MASK_WORDS; ++k) wmask[lane * Cfg::MASK_WORDS + k] = 0u;
     __syncwarp();
-    uint32_t cnt = 0, ic = 0;
+    uint32_t cnt = 0, ic = 0, acc_reads = 0;
     bool ok = true;
     for (int i = i_lo + static_cast<int>(blockIdx.x); i < n_items && ok; i += gridDim.x, ++ic) {
       const ItemInfo it = item_info<DP, kDH>(i, n_valid, p);
@@ -716,8 +716,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         p.met_part[static_cast<int64_t>(slot) * p.Tpad + it.s_row0 + row] = make_int2(met_cnt, met_tp);
       }
       if (kGrad && (cnt + n - 1) % Cfg::GROUPS == grp) {
-        // the group that took the item's last tile reads the accumulator out
-        if (!wait_bar_warp(bar_accfull, ic & 1, wc, wait_tag(4, 9, ic))) break;
+        // the group that took the item's last tile reads the accumulator out; each
+        // group has its own barrier, whose phases count that group's read-outs alone (with
+        // one tile an item, a shared barrier could be tested a whole phase early)
+        if (!wait_bar_warp(bar_accfull + grp, acc_reads & 1, wc, wait_tag(4, 9, ic))) break;
+        ++acc_reads;
         tc_fence_after();
 #pragma unroll 1
         for (int ch = 0; ch < AC / 16; ++ch) {
