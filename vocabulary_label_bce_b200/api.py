@@ -208,8 +208,29 @@ class _Embed(torch.autograd.Function):
         return embed_backward(dX, ids, ctx.shape[0], ctx.scale, grad_dtype=ctx.dtype), None, None
 
 
+def _hold_leaves(*tensors):
+    """The gradient nodes of the leaves among `tensors`, each marked with the stream it was made on.
+
+    torch keeps a leaf's gradient node, with its stream, while any autograd graph of the leaf lives.
+    A backward pass that is captured into a CUDA graph while an eager graph on another stream lives
+    would wait across streams and break the capture at its end: it is refused here, at its forward."""
+    if not torch.is_grad_enabled():
+        return None
+    held = []
+    for t in tensors:
+        if t.requires_grad and t.is_leaf and t.device.type == "cuda":
+            node = torch.autograd.graph.get_gradient_edge(t).node
+            here = torch.cuda.current_stream(t.device).cuda_stream
+            if node.metadata.setdefault("cutbce_stream", here) != here and torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("a tensor of this call is also held by an autograd graph that was made on another "
+                                   "stream: drop that graph (its loss), or make it on the stream that is captured")
+            held.append(node)
+    return held
+
+
 def embed(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
     """Differentiable scale * E[ids]; the gradient with respect to E is dense, in E's dtype."""
+    held = _hold_leaves(E)  # noqa: F841  (alive until the graph holds them)
     return _Embed.apply(E, ids, float(scale))
 
 
@@ -397,6 +418,7 @@ def distill_loss(H, E, teacher_ids, teacher_logits, mask=None, weights=None, tem
                  reduction: str = "mean") -> torch.Tensor:
     """Differentiable distillation loss (float32); gradients with respect to H and E, in bf16."""
     _no_grad_for(teacher_logits=teacher_logits, weights=weights)
+    held = _hold_leaves(H, E)  # noqa: F841
     return _Distill.apply(H, E, teacher_ids, teacher_logits, mask, weights, float(temperature), reduction)
 
 
@@ -423,4 +445,5 @@ def preference_loss(H, E, ids, offsets=None, ref_logp=None, mask=None, beta: flo
     """Differentiable preference loss (float32) and the sequences' log-probabilities (float32 [2P],
     not differentiable); gradients with respect to H and E, in bf16."""
     _no_grad_for(ref_logp=ref_logp)
+    held = _hold_leaves(H, E)  # noqa: F841
     return _Preference.apply(H, E, ids, offsets, ref_logp, mask, float(beta), reduction)

@@ -53,7 +53,7 @@ struct SoftmaxCfg {
   static constexpr int ACC_COL = 3 * BN;
   static constexpr int S_COL = ACC_COL + DP;
   static constexpr bool S_IN_TMEM = kGrad && S_COL + DP / 2 <= 512;
-  static constexpr int NUM_BARS = 2 + 2 * NX + 3 * NZ + 3;
+  static constexpr int NUM_BARS = 2 + 2 * NX + 3 * NZ + 2 + GROUPS;
   static constexpr uint32_t SMEM_BYTES = 1024 + S_BYTES + NX * (X_BYTES + O_BYTES) + ONES_BYTES + NUM_BARS * 8 + 16 + 64;
   static_assert(ACC_COL + DP <= 512 && NZ * BN <= 512, "TMEM budget");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -148,8 +148,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint64_t* bar_zfull = bar_xempty + NX;          // [NZ] logit tile ready (commit)
   uint64_t* bar_zfree = bar_zfull + NZ;           // [NZ] buffer free: P contracted (commit), or logits loaded (epilogue)
   uint64_t* bar_pready = bar_zfree + NZ;          // [NZ] P written over the logits (epilogue)
-  uint64_t* bar_accfull = bar_pready + NZ;        // accumulator complete (commit)
-  uint64_t* bar_accempty = bar_accfull + 1;       // accumulator read out (epilogue)
+  uint64_t* bar_accfull = bar_pready + NZ;        // [groups] accumulator complete, for the group that reads it (commit)
+  uint64_t* bar_accempty = bar_accfull + Cfg::GROUPS;  // accumulator read out (epilogue)
   uint64_t* bar_drain = bar_accempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::NUM_BARS);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(bar_zfree + b, kGrad ? 1 : Cfg::GROUP_WARPS * 32);
       mbar_init(bar_pready + b, Cfg::GROUP_WARPS * 32);
     }
-    mbar_init(bar_accfull, 1);
+    for (int g = 0; g < Cfg::GROUPS; ++g) mbar_init(bar_accfull + g, 1);
     mbar_init(bar_accempty, Cfg::GROUP_WARPS);
     mbar_init(bar_drain, 1);
     *abort_flag = 0;
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           umma_commit(bar_zfree + gb);
           umma_commit(bar_xempty + gst);
-          if (last) umma_commit(bar_accfull);
+          if (last) umma_commit(bar_accfull + cg % Cfg::GROUPS);
         }
         __syncwarp();
         progressed = true;
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int row = q * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     const float2 c2 = f2(p.c2, p.c2);
-    uint32_t cnt = 0, ic = 0;
+    uint32_t cnt = 0, ic = 0, acc_reads = 0;
     bool ok = true;
     for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x, ++ic) {
       int s_row0, x0, n, split;
@@ -518,8 +518,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         p.part[static_cast<int64_t>(slot) * p.Tc + s_row0 + row] = make_float2(m, sum);
       }
       if (kGrad && (cnt + n - 1) % Cfg::GROUPS == grp) {
-        // the group that took the last tile reads the accumulator out
-        if (!wait_bar_warp(bar_accfull, ic & 1, wc, wait_tag(4, 9, ic))) break;
+        // the group that took the last tile reads the accumulator out; each group's
+        // barrier counts its own read-outs (with one tile an item, a shared barrier could
+        // be tested a whole phase early)
+        if (!wait_bar_warp(bar_accfull + grp, acc_reads & 1, wc, wait_tag(4, 9, ic))) break;
+        ++acc_reads;
         tc_fence_after();
         const int v = s_row0 + row;
         int64_t sp = -1;

@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
         w[u] = __shfl_sync(0xffffffffu, q[j], from);
         lw[u] = __shfl_sync(0xffffffffu, lq[j], from);
         z[u] = 0.f;
-        if (k + u >= n || v < 0) w[u] = 0.f;
+        if (k + u >= n || v < 0 || v >= p.V) w[u] = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           e[u][i] = make_float2(0.f, 0.f);
