@@ -129,12 +129,18 @@ def cut_bce(H, E, targets, mask=None, reduction: str = "mean") -> torch.Tensor:
 # stream, and take their workspace from torch's caching allocator per call, so
 # calls on several streams, and captured graphs, never share one.
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(t: torch.Tensor):
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"tensors must be on a CUDA device, not {t.device}")
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
+    return _HERE if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def _plain(t: torch.Tensor) -> torch.Tensor:
+    """t without its graph, contiguous."""
+    return (t.detach() if t.requires_grad else t).contiguous()
 
 
 def _ids32(ids: torch.Tensor) -> torch.Tensor:
@@ -162,8 +168,7 @@ def embed_forward(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, status
     with _on(E):
         X = torch.empty(ids.shape + E.shape[1:], dtype=E.dtype, device=E.device)
         if ids.numel() > 0:
-            B.cutbce_embed_forward(E.detach().contiguous(), _ids32(ids).reshape(-1), X.view(-1, E.shape[1]), scale,
-                                   status)
+            B.cutbce_embed_forward(_plain(E), _ids32(ids), X, scale, status)
     return X
 
 
@@ -188,7 +193,7 @@ def embed_backward(dX: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 1
             return out if accumulate else out.zero_()
         dE = out if out is not None else torch.empty((V, D), dtype=grad_dtype, device=dX.device)
         ws = _workspace(B.cutbce_embed_workspace_size(ids.numel(), V, D), dX.device, workspace)
-        B.cutbce_embed_backward(dX.detach().contiguous().view(-1, D), _ids32(ids).reshape(-1), dE, ws, scale,
+        B.cutbce_embed_backward(_plain(dX).view(-1, D), _ids32(ids), dE, ws, scale,
                                 accumulate)
     return dE
 
@@ -237,11 +242,13 @@ def embed(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0) -> torch.Tenso
 def _rows(H: torch.Tensor, *rest: Optional[torch.Tensor]):
     """H [.., D] and per-position tensors flattened to T rows."""
     lead = H.dim() - 1
-    out = [H.detach().contiguous().view(-1, H.shape[-1])]
+    out = [_plain(H) if lead == 1 else _plain(H).view(-1, H.shape[-1])]
     for t in rest:
-        if t is not None and t.shape[:lead] != H.shape[:lead]:
-            raise ValueError(f"leading sizes {tuple(t.shape[:lead])} and {tuple(H.shape[:lead])} do not fit")
-        out.append(None if t is None else t.detach().reshape((-1,) + tuple(t.shape[lead:])).contiguous())
+        if t is not None:
+            if t.shape[:lead] != H.shape[:lead]:
+                raise ValueError(f"leading sizes {tuple(t.shape[:lead])} and {tuple(H.shape[:lead])} do not fit")
+            t = _plain(t) if lead == 1 else _plain(t).view((-1,) + t.shape[lead:])
+        out.append(t)
     return out
 
 
@@ -251,7 +258,7 @@ def _distill_problem(H, E, ids, logits, mask, weights, temperature, reduction):
         raise ValueError("teacher ids and logits must have one shape")
     H2, ids2, lg, m, w = _rows(H, _ids32(ids), logits.to(torch.float32), mask,
                                None if weights is None else weights.to(torch.float32))
-    E2 = E.detach().contiguous()
+    E2 = _plain(E)
     keep = (H2, E2, ids2, lg, m, w)
     return B.make_distill_problem(H2, E2, ids2, lg, m, w, temperature, reduction), keep
 
@@ -262,9 +269,9 @@ def _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction):
         if H.dim() != 3:
             raise ValueError("without offsets H must be [2P, N, D]")
         offsets = torch.arange(0, H2.shape[0] + 1, H.shape[1], dtype=torch.int32, device=H.device)
-    E2 = E.detach().contiguous()
+    E2 = _plain(E)
     off = offsets.to(torch.int32).contiguous()
-    ref = None if ref_logp is None else ref_logp.detach().to(torch.float32).reshape(-1).contiguous()
+    ref = None if ref_logp is None else _plain(ref_logp).to(torch.float32).view(-1)
     keep = (H2, E2, ids2, off, ref, m)
     return B.make_preference_problem(H2, E2, ids2, off, ref, m, beta, reduction), keep
 

@@ -182,8 +182,13 @@ def _check(status: int, where: str) -> None:
         raise CutBCEError(status, where)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -368,28 +373,32 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _dense(t: Optional[torch.Tensor], name: str, dtypes, shape=None) -> None:
     """Raises unless t is None or a contiguous tensor of one of `dtypes` (and of `shape`)."""
-    if t is None:
+    if t is None or (t.dtype in dtypes and t.is_contiguous() and (shape is None or t.shape == shape)):
         return
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
 def _same_device(*tensors: Optional[torch.Tensor]) -> None:
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) > 1:
-        raise ValueError(f"all tensors must be on one device, not {sorted(map(str, devices))}")
+    index = None
+    for t in tensors:
+        if t is None:
+            continue
+        if index is None:
+            index = t.get_device()
+        elif t.get_device() != index:
+            raise ValueError(f"all tensors must be on one device, not {[str(x.device) for x in tensors if x is not None]}")
 
 
 def cutbce_embed_forward(E: torch.Tensor, ids: torch.Tensor, X: torch.Tensor, scale: float = 1.0,
                          status: Optional[torch.Tensor] = None, stream=None) -> None:
-    """X[n] = scale * E[ids[n]] (E [V, D], X [N, D] bf16 or fp32, ids int32 [N], -1 empty)."""
+    """X[n] = scale * E[ids[n]] (E [V, D] and X ids.shape + [D] bf16 or fp32, ids int32, -1 empty)."""
     _dense(E, "E", tuple(_DTYPES))
     _dense(ids, "ids", (torch.int32,))
-    _dense(X, "X", (E.dtype,), (ids.numel(), E.shape[1]))
+    _dense(X, "X", (E.dtype,), ids.shape + E.shape[1:])
     _dense(status, "status", (torch.int32,))
     _same_device(E, ids, X, status)
     _check(load_library().cutbce_embed_forward(E.data_ptr(), E.shape[0], E.shape[1], _DTYPES[E.dtype], ids.data_ptr(),

@@ -46,25 +46,24 @@ cutbce_status check_device() {
 }
 
 // ---------------------------------------------------------------- sort and segment sums
+constexpr size_t kSideFillBytes = size_t(16) << 20;
 constexpr int64_t kMaxSortEntries = int64_t(1) << 28;
 
 // Buffers of the sort and of the sums over N entries.
 struct SortBuffers {
   SortPlan sp;
-  int64_t chunks;
   size_t o_hist, o_total, o_k[2], o_v[2], o_part;
 };
 
 void plan_sort(int64_t N, int64_t V, int64_t D, SortBuffers& b, Layout& l) {
   make_sort_plan(N, V, b.sp);
-  b.chunks = ceil_div(N, kSumChunk);
   b.o_hist = l.take(b.sp.hist_bytes);                 // right after the header: one memset clears both
   b.o_total = l.take(sizeof(int) * (size_t(1) << b.sp.bits));
   for (int i = 0; i < 2; ++i) {
     b.o_k[i] = l.take(4 * static_cast<size_t>(N));
     b.o_v[i] = l.take(4 * static_cast<size_t>(N));
   }
-  b.o_part = l.take(4 * 2 * static_cast<size_t>(b.chunks) * D);
+  b.o_part = l.take(4 * 2 * static_cast<size_t>(ceil_div(N, kMinChunk)) * D);   // the most blocks of any geometry
 }
 
 // Sorts the entries by id; the sorted keys and entry indices end in *keys, *vals.
@@ -103,35 +102,30 @@ cutbce_status run_sort(const SortBuffers& b, const int32_t* ids, int V, void* ws
 }
 
 template <int VEC, typename TIn, typename TOut>
-cutbce_status run_sums_t(const SegmentParams& p, int64_t chunks, cudaStream_t st) {
-  // lanes per chunk: the row's pieces, rounded up to a power of two; wider rows take several slices
-  const int pieces = static_cast<int>(ceil_div(p.D, VEC));
-  int lanes = 1;
-  while (lanes < pieces && lanes < 32) lanes <<= 1;
-  const int slices = static_cast<int>(ceil_div(pieces, lanes));
-  const int64_t threads = chunks * slices * lanes;
-  const int64_t blocks = ceil_div(threads, 256);
-  if (blocks >= (int64_t(1) << 31)) return CUTBCE_ERR_UNSUPPORTED;
+cutbce_status run_sums_t(const SegmentParams& p, cudaStream_t st) {
+  const SumGeometry g = sum_geometry(p.N, p.D, VEC);
   LaunchScope ls(CUTBCE_KERNEL_SEGMENT_SUM, st);
-  k_segment_sum<VEC, TIn, TOut><<<static_cast<unsigned>(blocks), 256, 0, st>>>(p, lanes, slices);
-  if (chunks > 1) k_segment_join<VEC == 8 ? 4 : VEC, TOut><<<static_cast<unsigned>(chunks - 1), 256, 0, st>>>(p, chunks);
+  k_segment_sum<VEC, TIn, TOut><<<dim3(static_cast<unsigned>(g.chunks), static_cast<unsigned>(g.slices)),
+                                  g.lanes * g.subs, 0, st>>>(p, g.lanes, g.subs, g.rounds);
+  if (g.chunks > 1)
+    k_segment_join<VEC == 8 ? 4 : VEC, TOut><<<static_cast<unsigned>(g.chunks - 1), 256, 0, st>>>(p, g.chunk);
   return cudaGetLastError() == cudaSuccess ? CUTBCE_OK : CUTBCE_ERR_CUDA;
 }
 
 template <typename TIn, typename TOut>
-cutbce_status run_sums_vec(const SegmentParams& p, int64_t chunks, cudaStream_t st) {
+cutbce_status run_sums_vec(const SegmentParams& p, cudaStream_t st) {
   constexpr int VEC = 16 / sizeof(TIn);
-  if (p.D % VEC == 0 && aligned(p.src, 16)) return run_sums_t<VEC, TIn, TOut>(p, chunks, st);
-  return run_sums_t<1, TIn, TOut>(p, chunks, st);
+  if (p.D % VEC == 0 && aligned(p.src, 16) && aligned(p.out, 16)) return run_sums_t<VEC, TIn, TOut>(p, st);
+  return run_sums_t<1, TIn, TOut>(p, st);
 }
 
-cutbce_status run_sums(const SegmentParams& p, bool in_bf16, int64_t chunks, cudaStream_t st) {
-  if (p.first != nullptr) return run_sums_vec<__nv_bfloat16, float>(p, chunks, st);
+cutbce_status run_sums(const SegmentParams& p, bool in_bf16, cudaStream_t st) {
+  if (p.first != nullptr) return run_sums_vec<__nv_bfloat16, float>(p, st);
   if (in_bf16) {
-    return p.out_bf16 ? run_sums_vec<__nv_bfloat16, __nv_bfloat16>(p, chunks, st)
-                      : run_sums_vec<__nv_bfloat16, float>(p, chunks, st);
+    return p.out_bf16 ? run_sums_vec<__nv_bfloat16, __nv_bfloat16>(p, st)
+                      : run_sums_vec<__nv_bfloat16, float>(p, st);
   }
-  return p.out_bf16 ? run_sums_vec<float, __nv_bfloat16>(p, chunks, st) : run_sums_vec<float, float>(p, chunks, st);
+  return p.out_bf16 ? run_sums_vec<float, __nv_bfloat16>(p, st) : run_sums_vec<float, float>(p, st);
 }
 
 // ---------------------------------------------------------------- row lookup
@@ -261,7 +255,7 @@ void plan_head(const HeadProblem& p, bool dH, bool dE, bool lse_pass, HeadPlan& 
   pl.o_lse2 = l.take(4 * Tc);
   pl.o_term = l.take(8 * Tc);
   pl.o_hc = l.take(2 * Tc * pl.DP);
-  pl.o_lpart = l.take(8 * std::max<size_t>(static_cast<size_t>(p.P), Tc / kLseThreads));
+  pl.o_lpart = l.take(8 * std::max<size_t>(static_cast<size_t>(p.P), Tc / kLseRows));
   pl.o_part = lse_pass ? l.take(8 * static_cast<size_t>(pl.S) * 4 * Tc) : 0;
   pl.o_wide = pl.fused ? l.take(8 * static_cast<size_t>(pl.S) * 4 * Tc) : 0;
   pl.o_m2 = pl.fused ? l.take(4 * Tc) : 0;
@@ -446,7 +440,7 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   }
   {
     LaunchScope ls(CUTBCE_KERNEL_HEAD_FINISH, st);
-    k_head_lse<<<static_cast<unsigned>(pl.Tc / kLseThreads), kLseThreads, 0, st>>>(hp);
+    k_head_lse<<<static_cast<unsigned>(pl.Tc / kLseRows), kLseThreads, 0, st>>>(hp);
     if (p.kind == kHeadPreference) k_head_pairs<<<static_cast<unsigned>(p.P), kPairThreads, 0, st>>>(hp);
     CUTBCE_CK(cudaGetLastError());
   }
@@ -491,7 +485,7 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
     gp.first = at<int>(ws, pl.o_first);
     gp.status = status;
     CUTBCE_CK(cudaMemsetAsync(gp.first, 0xFF, 4 * static_cast<size_t>(p.V), st));
-    if ((s = run_sums(gp, true, pl.sort.chunks, st)) != CUTBCE_OK) return s;
+    if ((s = run_sums(gp, true, st)) != CUTBCE_OK) return s;
     sp.first = gp.first;
     sp.sparse = at<float>(ws, pl.o_usum);
     sp.dE = out.dE;
@@ -567,9 +561,25 @@ cutbce_status cutbce_embed_backward(const void* dX, int32_t dtype, const int32_t
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int* status = at<int>(ws, pl.o_hdr);
   CUTBCE_CK(cudaMemsetAsync(status, 0, pl.sort.o_hist + pl.sort.sp.hist_bytes, st));
-  if (!accumulate) CUTBCE_CK(cudaMemsetAsync(dE, 0, eo * static_cast<size_t>(V) * D, st));
+  // a large dE is cleared on a second stream while the entries are sorted
+  const size_t de_bytes = eo * static_cast<size_t>(V) * D;
+  SideStreamLease side;
+  if (!accumulate) {
+    cudaStream_t fill = st;
+    if (de_bytes >= kSideFillBytes) {
+      if ((s = take_side_stream(side.s)) != CUTBCE_OK) return s;
+      side.held = true;
+      CUTBCE_CK(cudaEventRecord(side.s.ev, st));
+      CUTBCE_CK(cudaStreamWaitEvent(side.s.s, side.s.ev, 0));
+      fill = side.s.s;
+    }
+    CUTBCE_CK(cudaMemsetAsync(dE, 0, de_bytes, fill));
+    if (side.held) CUTBCE_CK(cudaEventRecord(side.s.ev2, side.s.s));
+  }
   SegmentParams p{};
-  if ((s = run_sort(pl.sort, ids, static_cast<int>(V), ws, status, st, &p.keys, &p.vals)) != CUTBCE_OK) return s;
+  s = run_sort(pl.sort, ids, static_cast<int>(V), ws, status, st, &p.keys, &p.vals);
+  if (side.held) CUTBCE_CK(cudaStreamWaitEvent(st, side.s.ev2, 0));   // joined on every path
+  if (s != CUTBCE_OK) return s;
   p.N = N;
   p.V = static_cast<int>(V);
   p.D = static_cast<int>(D);
@@ -581,7 +591,7 @@ cutbce_status cutbce_embed_backward(const void* dX, int32_t dtype, const int32_t
   p.out_bf16 = grad_dtype == CUTBCE_GRAD_BF16;
   p.accumulate = accumulate;
   p.status = status;
-  return run_sums(p, dtype == CUTBCE_BF16, pl.sort.chunks, st);
+  return run_sums(p, dtype == CUTBCE_BF16, st);
 }
 
 cutbce_status cutbce_distill_workspace_size(const cutbce_distill_problem* prob, int outputs, size_t* bytes) {

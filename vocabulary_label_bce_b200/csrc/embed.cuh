@@ -23,7 +23,9 @@ __global__ void __launch_bounds__(256) k_embed(const T* __restrict__ E, int64_t 
 #pragma unroll
   for (int k = 0; k < VEC; ++k) x[k] = 0.f;
   if (id >= 0 && id < V) {
-    load_row<VEC, T>(E + static_cast<int64_t>(id) * D + col, x);
+    RowPiece<VEC, T> piece;
+    piece.load(E + static_cast<int64_t>(id) * D + col);
+    piece.values(x);
 #pragma unroll
     for (int k = 0; k < VEC; ++k) x[k] *= scale;
   } else if (id != -1 && status != nullptr && col == 0) {

@@ -10,11 +10,12 @@
 // histogram of the next with integer atomics, whose order changes nothing.
 // An entry without a row (an empty id) has the key V and sorts to the end.
 //
-// Sums: the sorted entries are cut into chunks of kSumChunk; a group of lanes
-// adds the rows of one chunk in order.  A segment (equal ids) inside one chunk is
-// written at once; one that crosses chunks leaves one partial per chunk, and
-// k_segment_join adds those in chunk order (eight interleaved running sums, then
-// a fixed order), so hot ids neither serialise on one lane group nor need atomics.
+// Sums: a block takes a chunk of consecutive sorted entries, cut into sub-chunks;
+// the lanes of a row add the rows of their sub-chunk in order, eight in flight.  A
+// segment (equal ids) inside a sub-chunk is written at once; one that crosses
+// sub-chunks is joined in shared memory, in order; one that crosses blocks leaves
+// one partial per block, and k_segment_join adds those (eight interleaved running
+// sums, then a fixed order).  Hot ids neither serialise nor need atomics.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -27,7 +28,6 @@ constexpr int kSortThreads = 256;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortMaxBits = 11;
 constexpr int kSortMaxBins = 1 << kSortMaxBits;
-constexpr int kSumChunk = 32;               // sorted entries per partial sum
 
 struct SortPlan {
   int64_t N;                // entries
@@ -44,6 +44,7 @@ inline void make_sort_plan(int64_t N, int64_t V, SortPlan& s) {
   s.N = N;
   s.passes = (bits + kSortMaxBits - 1) / kSortMaxBits;
   s.bits = (bits + s.passes - 1) / s.passes;
+  if (s.bits < 2) s.bits = 2;                 // a thread of the scatter holds four digits
   // tiles of 1024 entries while a scatter block can read all histograms cheaply, then 4096, then 16384
   s.ipt = N <= 65536 ? 4 : N <= 1048576 ? 16 : 64;
   s.nblk = static_cast<int>(ceil_div(N, int64_t(kSortThreads) * s.ipt));
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_keys(const int32_t* __res
   for (int d = threadIdx.x; d < bins; d += kSortThreads) h[d] = 0;
   __syncthreads();
   const int64_t base = static_cast<int64_t>(blockIdx.x) * kSortThreads * IPT;
-#pragma unroll 4
+#pragma unroll 16
   for (int r = 0; r < IPT; ++r) {
     const int64_t i = base + r * kSortThreads + threadIdx.x;
     if (i < N) {
@@ -115,25 +116,40 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const int* __rest
   __shared__ uint16_t cnt[kSortWarps][kSortMaxBins];
   __shared__ int off[kSortMaxBins];
   __shared__ int wsum[kSortWarps];
-  if (*status != 0) return;
+  const int failed = *status;                       // looked at before anything is written
   const int bins = 1 << bits, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // offset of (digit, this tile): all smaller digits, then this digit in earlier tiles
+  // offset of (digit, this tile): all smaller digits, then this digit in earlier
+  // tiles.  A thread holds four consecutive digits (of each 1024), sixteen tiles'
+  // histograms in flight with small tiles, eight with large ones.
   int carry = 0;
-  for (int d0 = 0; d0 < bins; d0 += kSortThreads) {
-    const int d = d0 + tid;
-    int before = 0, total = 0;
-    if (d < bins && digit_total != nullptr) {
-      before = hist[static_cast<int64_t>(blockIdx.x) * bins + d];
-      total = digit_total[d];
-    } else if (d < bins) {
-#pragma unroll 8
-      for (int b = 0; b < nblk; ++b) {
-        const int v = __ldg(hist + static_cast<int64_t>(b) * bins + d);
-        if (b < static_cast<int>(blockIdx.x)) before += v;
-        total += v;
+  for (int h0 = 0; h0 < bins; h0 += 4 * kSortThreads) {
+    const int d0 = h0 + 4 * tid;
+    int before[4] = {0, 0, 0, 0}, total[4] = {0, 0, 0, 0};
+    if (d0 < bins) {
+      const int4* src = reinterpret_cast<const int4*>(hist + d0);
+      const int step = bins / 4;
+      if (digit_total != nullptr) {
+        const int4 v = src[static_cast<int64_t>(blockIdx.x) * step], t = *reinterpret_cast<const int4*>(digit_total + d0);
+        before[0] = v.x, before[1] = v.y, before[2] = v.z, before[3] = v.w;
+        total[0] = t.x, total[1] = t.y, total[2] = t.z, total[3] = t.w;
+      } else {
+        constexpr int kTiles = IPT == 4 ? 16 : 8;       // tiles in flight; the last group is guarded, not looped
+        for (int b0 = 0; b0 < nblk; b0 += kTiles) {
+          int4 v[kTiles];
+#pragma unroll
+          for (int u = 0; u < kTiles; ++u)
+            v[u] = b0 + u < nblk ? __ldg(src + static_cast<int64_t>(b0 + u) * step) : make_int4(0, 0, 0, 0);
+#pragma unroll
+          for (int u = 0; u < kTiles; ++u) {
+            const int keep = b0 + u < static_cast<int>(blockIdx.x) ? -1 : 0;
+            total[0] += v[u].x, total[1] += v[u].y, total[2] += v[u].z, total[3] += v[u].w;
+            before[0] += v[u].x & keep, before[1] += v[u].y & keep, before[2] += v[u].z & keep, before[3] += v[u].w & keep;
+          }
+        }
       }
     }
-    int inc = total;
+    const int sum = total[0] + total[1] + total[2] + total[3];
+    int inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, inc, o);
@@ -141,14 +157,19 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const int* __rest
     }
     if (lane == 31) wsum[warp] = inc;
     __syncthreads();
-    int add = carry, all = 0;
+    int run = carry + inc - sum;
 #pragma unroll
     for (int w = 0; w < kSortWarps; ++w) {
-      if (w < warp) add += wsum[w];
-      all += wsum[w];
+      if (w < warp) run += wsum[w];
+      carry += wsum[w];
     }
-    if (d < bins) off[d] = add + inc - total + before;
-    carry += all;
+    if (d0 < bins) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        off[d0 + k] = run + before[k];
+        run += total[k];
+      }
+    }
     __syncthreads();
   }
   for (int d = lane; d < bins; d += 32) cnt[warp][d] = 0;
@@ -195,6 +216,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const int* __rest
     }
   }
   __syncthreads();
+  if (failed != 0) return;
   auto put = [&](int r, int k, int rk) {
     const int64_t i = wbase + r * 32 + lane;
     if (i >= N) return;
@@ -235,125 +257,231 @@ struct SegmentParams {
   const int* status;
 };
 
+template <int VEC>
+__device__ __forceinline__ void store_floats(float* o, const float (&v)[VEC]) {
+  if constexpr (VEC % 4 == 0) {
+#pragma unroll
+    for (int k = 0; k < VEC; k += 4) *reinterpret_cast<float4*>(o + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+  } else {
+    o[0] = v[0];
+  }
+}
+
+// VEC > 1: rows of the output start on 16-byte boundaries.
 template <int VEC, typename TOut>
 __device__ __forceinline__ void write_sum(const SegmentParams& p, int id, int64_t start, int col, const float (&acc)[VEC]) {
+  float v[VEC];
   if (p.first != nullptr) {
-    float* o = static_cast<float*>(p.out) + start * p.D + col;
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) o[k] = acc[k] * p.scale;
+    for (int k = 0; k < VEC; ++k) v[k] = acc[k] * p.scale;
+    store_floats<VEC>(static_cast<float*>(p.out) + start * p.D + col, v);
     return;
   }
   TOut* o = static_cast<TOut*>(p.out) + static_cast<int64_t>(id) * p.D + col;
-  float v[VEC];
 #pragma unroll
   for (int k = 0; k < VEC; ++k) {
     v[k] = __fmul_rn(acc[k], p.scale);
     if (p.accumulate) v[k] = __fadd_rn(v[k], static_cast<float>(o[k]));
   }
+  if constexpr (sizeof(TOut) == 4) {
+    store_floats<VEC>(reinterpret_cast<float*>(o), v);
+  } else if constexpr (VEC % 4 == 0) {
 #pragma unroll
-  for (int k = 0; k < VEC; ++k) o[k] = TOut(v[k]);
+    for (int k = 0; k < VEC; k += 4)
+      *reinterpret_cast<uint2*>(o + k) = make_uint2(pack_bf16x2(v[k], v[k + 1]), pack_bf16x2(v[k + 2], v[k + 3]));
+  } else {
+    o[0] = TOut(v[0]);
+  }
 }
 
+// A piece of a row as loaded (16 bytes, or one element), and its values.
 template <int VEC, typename T>
-__device__ __forceinline__ void load_row(const T* src, float (&x)[VEC]) {
-  if constexpr (VEC == 1) {
-    x[0] = static_cast<float>(src[0]);
-  } else if constexpr (sizeof(T) == 4) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(src));
-    x[0] = v.x;
-    x[1] = v.y;
-    x[2] = v.z;
-    x[3] = v.w;
-  } else {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+struct RowPiece {
+  uint4 raw;
+  __device__ __forceinline__ void load(const T* src) { raw = __ldg(reinterpret_cast<const uint4*>(src)); }
+  __device__ __forceinline__ void values(float (&x)[VEC]) const {
+    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      x[2 * k] = __uint_as_float(u[k] << 16);
-      x[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+      if constexpr (sizeof(T) == 4) {
+        x[k] = __uint_as_float(u[k]);
+      } else {
+        x[2 * k] = __uint_as_float(u[k] << 16);
+        x[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+      }
     }
   }
+};
+template <typename T>
+struct RowPiece<1, T> {
+  T raw;
+  __device__ __forceinline__ void load(const T* src) { raw = *src; }
+  __device__ __forceinline__ void values(float (&x)[1]) const { x[0] = static_cast<float>(raw); }
+};
+
+// Geometry for rows of D elements in pieces of VEC: `lanes` threads a row (wide
+// rows in `slices`), `subs` rows side by side in a block, each sub-chunk summing
+// kSumBatch * rounds consecutive entries.
+constexpr int kSumBatch = 8;                // rows in flight per thread
+constexpr int kMinChunk = 4 * kSumBatch;    // fewest entries of a block
+struct SumGeometry {
+  int lanes, slices, subs, rounds;
+  int64_t chunk, chunks;                    // entries per block, blocks (per slice)
+};
+inline SumGeometry sum_geometry(int64_t N, int64_t D, int vec) {
+  SumGeometry g;
+  const int pieces = static_cast<int>(ceil_div(D, vec));
+  g.slices = static_cast<int>(ceil_div(pieces, 64));
+  g.lanes = static_cast<int>(ceil_div(pieces, g.slices));
+  g.subs = 256 / g.lanes;
+  if (g.subs > 64) g.subs = 64;
+  // one round while that keeps the blocks below about four an SM, then more
+  int64_t r = N / (static_cast<int64_t>(g.subs) * kSumBatch * 592);
+  g.rounds = static_cast<int>(r < 1 ? 1 : r > 16 ? 16 : r);
+  g.chunk = static_cast<int64_t>(g.subs) * kSumBatch * g.rounds;
+  g.chunks = ceil_div(N, g.chunk);
+  return g;
 }
 
-// A group of `lanes` consecutive threads per (chunk, slice of lanes * VEC columns).
+// One block per (chunk, slice).  A sub-chunk writes the segments that lie inside it
+// and leaves its first (continued) and last (continuing) ones in shared memory; the
+// lanes of sub-chunk 0 then walk the sub-chunks in order.
 template <int VEC, typename TIn, typename TOut>
-__global__ void __launch_bounds__(256) k_segment_sum(const SegmentParams p, int lanes, int slices) {
+__global__ void __launch_bounds__(256) k_segment_sum(const SegmentParams p, int lanes, int subs, int rounds) {
+  __shared__ float s_first[256 * VEC], s_last[256 * VEC];
+  __shared__ int s_kind[64], s_key[64], s_start[64];     // 1: first closes, 2: first goes through, 4: last is open
   if (*p.status != 0) return;
-  const int64_t group = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / lanes;
-  const int64_t chunk = group / slices;
-  const int col = (static_cast<int>(group % slices) * lanes + static_cast<int>(threadIdx.x) % lanes) * VEC;
-  const int64_t i0 = chunk * kSumChunk;
-  if (i0 >= p.N || col >= p.D) return;
-  const int64_t i1 = min(p.N, i0 + kSumChunk);
+  const int sub = static_cast<int>(threadIdx.x) / lanes, lane = static_cast<int>(threadIdx.x) % lanes;
+  const int col = (static_cast<int>(blockIdx.y) * lanes + lane) * VEC;
+  const int per = kSumBatch * rounds;
+  const int64_t chunk = blockIdx.x;
+  const int64_t i0 = (chunk * subs + sub) * per;
+  const int64_t i1 = min(p.N, i0 + per);
+  const bool live = col < p.D;
   const TIn* src = static_cast<const TIn*>(p.src) + col;
-  float acc[VEC];
+  if (sub < subs) {
+    int kind = 0;
+    int cur = i0 < i1 ? __ldg(p.keys + i0) : p.V;
+    bool open_left = i0 > 0 && i0 < i1 && __ldg(p.keys + i0 - 1) == cur;
+    const int after = i1 < p.N && i0 < i1 ? __ldg(p.keys + i1) : -1;
+    int start = static_cast<int>(i0);
+    float acc[VEC];
 #pragma unroll
-  for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
-  int cur = p.keys[i0];
-  bool open_left = i0 > 0 && p.keys[i0 - 1] == cur;   // the segment began in an earlier chunk
-  int64_t start = i0;
-  auto flush = [&](int id, bool open_right) {
-    if (id >= p.V) return;
-    if (!open_left && !open_right) {
-      write_sum<VEC, TOut>(p, id, start, col, acc);
-    } else {
-      float* o = p.part + (2 * chunk + (open_left ? 0 : 1)) * p.D + col;
+    for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+    // ends the running segment; `goes_on`: the next sub-chunk continues it
+    auto flush = [&](bool goes_on) {
+      if (cur >= p.V) return;
+      if (p.first != nullptr && !open_left && col == 0) p.first[cur] = start;
+      if (!open_left && !goes_on) {
+        if (live) write_sum<VEC, TOut>(p, cur, start, col, acc);
+        return;
+      }
+      float* o = (open_left ? s_first : s_last) + threadIdx.x * VEC;
 #pragma unroll
       for (int k = 0; k < VEC; ++k) o[k] = acc[k];
-    }
-    if (p.first != nullptr && !open_left && col == 0) p.first[id] = static_cast<int>(start);
-  };
-  constexpr int U = 8;                                // rows in flight
-  for (int64_t i = i0; i < i1; i += U) {
-    float x[U][VEC];
-    int id[U];
-    float w[U];
+      kind |= open_left ? (goes_on ? 2 : 1) : 4;
+    };
+    // Every load is unconditional, so that a batch's are in flight together: indices
+    // are held below N, and an entry without a row (key V) reads its row all the same
+    // and adds it to a segment that is never written.  The next batch's keys and
+    // indices are loaded before this one's rows are added.
+    int id[kSumBatch], e[kSumBatch];
+    auto load_entries = [&](int64_t i) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      id[u] = i + u < i1 ? __ldg(p.keys + i + u) : p.V;
-      w[u] = 0.f;
+      for (int u = 0; u < kSumBatch; ++u) {
+        const int64_t at = min(i + u, p.N - 1);
+        id[u] = __ldg(p.keys + at);
+        e[u] = __ldg(p.vals + at);
+      }
+    };
+    if (i0 < i1) load_entries(i0);
+    for (int64_t i = i0; i < i1; i += kSumBatch) {
+      RowPiece<VEC, TIn> x[kSumBatch];
+      float w[kSumBatch];
+      int now[kSumBatch];
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) x[u][k] = 0.f;
-      if (id[u] < p.V) {
-        const int e = __ldg(p.vals + i + u);
-        const int64_t row = p.K == 1 ? e : e / p.K;
-        w[u] = p.share != nullptr ? __ldg(p.share + e) : 1.f;
+      for (int u = 0; u < kSumBatch; ++u) {
+        const int64_t row = p.K == 1 ? e[u] : e[u] / p.K;
+        w[u] = p.share != nullptr ? __ldg(p.share + e[u]) : 1.f;
         if (p.row_coef != nullptr) w[u] *= __ldg(p.row_coef + row);
-        load_row<VEC, TIn>(src + row * p.D, x[u]);
+        x[u].load(src + (live ? row * p.D : -col));       // lanes past the row's end read its first element
+        now[u] = id[u];
+      }
+      if (i + kSumBatch < i1) load_entries(i + kSumBatch);
+#pragma unroll
+      for (int u = 0; u < kSumBatch; ++u) {
+        if (i + u >= i1) break;
+        if (now[u] != cur) {
+          flush(false);
+          cur = now[u];
+          open_left = false;
+          start = static_cast<int>(i + u);
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+        }
+        float v[VEC];
+        x[u].values(v);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) acc[k] = fmaf(w[u], v[k], acc[k]);
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (i + u >= i1) break;
-      if (id[u] != cur) {
-        flush(cur, false);
-        cur = id[u];
-        open_left = false;
-        start = i + u;
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) acc[k] = fmaf(w[u], x[u][k], acc[k]);
+    if (i0 < i1) flush(after == cur);
+    if (lane == 0) {
+      s_kind[sub] = kind;
+      s_key[sub] = cur;
+      s_start[sub] = start;
     }
   }
-  flush(cur, i1 < p.N && p.keys[i1] == cur);
+  __syncthreads();
+  if (sub != 0 || !live) return;
+  // the running segment across sub-chunks; it may have begun in an earlier block
+  float run[VEC];
+  bool open = (s_kind[0] & 3) != 0, here = false;
+  int key = 0, start = 0;
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) run[k] = 0.f;
+  auto leave = [&](int slot) {
+    store_floats<VEC>(p.part + (2 * chunk + slot) * p.D + col, run);
+  };
+  for (int s = 0; s < subs; ++s) {
+    const int kind = s_kind[s];
+    if (kind == 0) continue;
+    if (kind & 3) {
+      const float* f = s_first + (s * lanes + lane) * VEC;
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) run[k] += f[k];
+      if (kind & 1) {
+        if (here) write_sum<VEC, TOut>(p, key, start, col, run);
+        else leave(0);
+        open = false;
+      }
+    }
+    if (kind & 4) {
+      const float* f = s_last + (s * lanes + lane) * VEC;
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) run[k] = f[k];
+      key = s_key[s];
+      start = s_start[s];
+      open = here = true;
+    }
+  }
+  if (open) leave(here ? 1 : 0);
 }
 
 // One block per chunk whose last segment continues: adds that segment's partials.
 template <int VEC, typename TOut>
-__global__ void __launch_bounds__(256) k_segment_join(const SegmentParams p, int64_t chunks) {
+__global__ void __launch_bounds__(256) k_segment_join(const SegmentParams p, int64_t chunk_entries) {
   __shared__ float red[8][32 * VEC];
   if (*p.status != 0) return;
   const int64_t c0 = blockIdx.x;
-  const int64_t last = (c0 + 1) * kSumChunk - 1;
+  const int64_t last = (c0 + 1) * chunk_entries - 1;
   if (last + 1 >= p.N) return;
   const int id = p.keys[last];
   if (id >= p.V || p.keys[last + 1] != id) return;                          // nothing continues
   int64_t start = last;
   {
     // the segment's first index: in this chunk, or this chunk is a middle one
-    const int64_t b = c0 * kSumChunk;
+    const int64_t b = c0 * chunk_entries;
     if (p.keys[b] == id && b > 0 && p.keys[b - 1] == id) return;
     int64_t lo = b, hi = last;
     while (lo < hi) {
@@ -372,7 +500,7 @@ __global__ void __launch_bounds__(256) k_segment_join(const SegmentParams p, int
       if (p.keys[mid] <= id) lo = mid + 1;
       else hi = mid;
     }
-    c1 = (lo - 1) / kSumChunk;
+    c1 = (lo - 1) / chunk_entries;
   }
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   for (int col0 = 0; col0 < p.D; col0 += 32 * VEC) {
@@ -381,11 +509,22 @@ __global__ void __launch_bounds__(256) k_segment_join(const SegmentParams p, int
 #pragma unroll
     for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
     if (col < p.D) {
-#pragma unroll 4
-      for (int64_t c = c0 + w; c <= c1; c += 8) {
-        const float* q = p.part + (2 * c + (c == c0 ? 1 : 0)) * p.D + col;
+      for (int64_t cb = c0 + w; cb <= c1; cb += 32) {
+        RowPiece<VEC, float> q[4];
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) acc[k] += q[k];
+        for (int u = 0; u < 4; ++u) {
+          const int64_t c = min(cb + 8 * u, c1);
+          q[u].load(p.part + (2 * c + (c == c0 ? 1 : 0)) * p.D + col);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float v[VEC];
+          q[u].values(v);
+          if (cb + 8 * u <= c1) {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) acc[k] += v[k];
+          }
+        }
       }
     }
 #pragma unroll

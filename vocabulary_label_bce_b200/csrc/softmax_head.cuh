@@ -460,34 +460,69 @@ __global__ void __launch_bounds__(256) k_head_ref(const HeadParams p) {
 }
 
 // ------------------------------------------------------------------ lse
-// One thread per compacted row: joins the (max, sum) partials of the row's splits
+// Four threads per compacted row: join the (max, sum) partials of the row's splits
 // and slabs (or takes the lse of an earlier forward), writes lse, the exponent
 // offset of the item-owned pass and the row's share of the distillation loss,
 // which the last block adds up in block order.
 constexpr int kLseThreads = 128;
+constexpr int kLseLanes = 4;                      // lanes that share a row's partials
+constexpr int kLseRows = kLseThreads / kLseLanes;
 
 __global__ void __launch_bounds__(kLseThreads) k_head_lse(const HeadParams p) {
   __shared__ double red[kLseThreads];
   __shared__ int last;
   HeadHeader* hdr = p.hdr;
   if (hdr->w.status != 0) return;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kLseThreads + threadIdx.x;
-  double row_loss = 0.0;
+  // consecutive threads take consecutive rows, so that a slot's partials are read together
+  const int part_of = static_cast<int>(threadIdx.x) / kLseRows;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kLseRows + threadIdx.x % kLseRows;
+  __shared__ float sm[kLseLanes][kLseRows], ss[kLseLanes][kLseRows];
   const int t = c < hdr->n_rows ? p.orig[c] : -1;
-  if (t >= 0) {
+  if (p.lse_in == nullptr) {
+    // running (reference, sum) over every kLseLanes-th slot, eight loads in flight
+    float m = -3.0e38f, sum = 0.f;
+    bool bad = false;
+    if (t >= 0) {
+      for (int s0 = part_of; s0 < p.slots; s0 += 8 * kLseLanes) {
+        float2 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int s = s0 + u * kLseLanes;
+          v[u] = s < p.slots ? __ldg(p.part + s * p.Tc + c) : make_float2(-3.0e38f, 0.f);
+        }
+        float mx = m;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          mx = fmaxf(mx, v[u].x);
+          bad |= v[u].x != v[u].x;
+        }
+        sum *= exp2f(m - mx);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) sum += v[u].y * exp2f(v[u].x - mx);
+        m = mx;
+      }
+    }
+    sm[part_of][threadIdx.x % kLseRows] = bad ? NAN : m;
+    ss[part_of][threadIdx.x % kLseRows] = sum;
+    __syncthreads();
+  }
+  double row_loss = 0.0;
+  if (t >= 0 && part_of == 0) {
     float l2, ref = 0.f;
     if (p.lse_in != nullptr) {
       l2 = p.lse_in[t] * 1.4426950408889634f;
     } else {
-      float m = -3.0e38f;
-      for (int s = 0; s < p.slots; ++s) m = fmaxf(m, p.part[s * p.Tc + c].x);
-      float sum = 0.f;
-      for (int s = 0; s < p.slots; ++s) {
-        const float2 v = p.part[s * p.Tc + c];
-        sum += v.y * exp2f(v.x - m);
+      float m = sm[0][threadIdx.x], sum = 0.f;
+#pragma unroll
+      for (int q = 1; q < kLseLanes; ++q) m = fmaxf(m, sm[q][threadIdx.x]);
+      bool bad = false;
+#pragma unroll
+      for (int q = 0; q < kLseLanes; ++q) {
+        const float mq = sm[q][threadIdx.x];
+        bad |= mq != mq;
+        sum += ss[q][threadIdx.x] * exp2f(mq - m);
       }
-      l2 = m + log2f(sum);
-      if (sum != sum || m != m) l2 = NAN;
+      l2 = bad ? NAN : m + log2f(sum);
       ref = m;
     }
     p.rescale[c] = p.m2 != nullptr ? exp2f(ref - l2) : 1.f;
