@@ -209,12 +209,14 @@ cutbce_status check_head(const HeadProblem& p, bool need_data) {
 }
 
 constexpr int kMaxHeadSplits = 148;
+constexpr int kMaxHeadSlots = 2 * 3;           // partials per split: column slabs x epilogue groups
 
 struct HeadPlan {
   int DP, BN, S, tps, n_vtiles, n_blk;
+  int BN_lse, n_vtiles_lse, S_lse, tps_lse;   // the log-sum-exp pass's tiles and splits
   bool fused;                    // the dH pass takes the row sums: no log-sum-exp pass of its own
   int64_t Tc;
-  size_t o_hdr, o_blk, o_cls, o_cidx, o_orig, o_coef, o_off16, o_lse2, o_term, o_hc, o_lpart, o_part, o_wide, o_m2, o_h2, o_low2, o_rescale, o_sparse, o_dhpart,
+  size_t o_hdr, o_blk, o_cls, o_cidx, o_orig, o_coef, o_off16, o_b2, o_lse2, o_term, o_hc, o_lpart, o_part, o_wide, o_m2, o_h2, o_low2, o_rescale, o_sparse, o_dhpart,
       o_keys, o_share, o_usum, o_first, total;
   SortBuffers sort;
   size_t clear_bytes;            // header and histograms
@@ -230,6 +232,7 @@ constexpr int64_t kFusedLogits = 1000000;
 void plan_head(const HeadProblem& p, bool dH, bool dE, bool lse_pass, HeadPlan& pl) {
   pl.DP = static_cast<int>(round_up(p.D, 64));
   pl.BN = pl.DP > 128 ? 64 : 128;
+  pl.BN_lse = pl.DP == 64 ? SoftmaxCfg<64, kPassLse>::BN : pl.BN;
   pl.n_vtiles = static_cast<int>(ceil_div(p.V, pl.BN));
   pl.n_blk = static_cast<int>(ceil_div(p.T, 256));
   pl.fused = lse_pass && dH && p.T * p.V >= kFusedLogits;
@@ -240,6 +243,9 @@ void plan_head(const HeadProblem& p, bool dH, bool dE, bool lse_pass, HeadPlan& 
   s0 = std::max<int64_t>(1, std::min<int64_t>(s0, pl.n_vtiles));
   pl.tps = static_cast<int>(ceil_div(pl.n_vtiles, s0));
   pl.S = static_cast<int>(ceil_div(pl.n_vtiles, pl.tps));
+  pl.n_vtiles_lse = static_cast<int>(ceil_div(p.V, pl.BN_lse));
+  pl.tps_lse = static_cast<int>(ceil_div(pl.n_vtiles_lse, std::min<int64_t>(pl.S, pl.n_vtiles_lse)));
+  pl.S_lse = static_cast<int>(ceil_div(pl.n_vtiles_lse, pl.tps_lse));   // every split is non-empty, at most S
   const size_t T = static_cast<size_t>(p.T), Tc = static_cast<size_t>(pl.Tc), TK = T * p.K;
   Layout l;
   pl.o_hdr = l.take(256);
@@ -251,13 +257,14 @@ void plan_head(const HeadProblem& p, bool dH, bool dE, bool lse_pass, HeadPlan& 
   pl.o_cidx = l.take(4 * T);
   pl.o_orig = l.take(4 * Tc);
   pl.o_coef = l.take(4 * T);
-  pl.o_off16 = dE ? l.take(32 * Tc) : 0;
+  pl.o_off16 = dE && pl.DP <= 128 ? l.take(32 * Tc) : 0;
+  pl.o_b2 = dE && pl.DP > 128 ? l.take(4 * Tc) : 0;
   pl.o_lse2 = l.take(4 * Tc);
   pl.o_term = l.take(8 * Tc);
   pl.o_hc = l.take(2 * Tc * pl.DP);
   pl.o_lpart = l.take(8 * std::max<size_t>(static_cast<size_t>(p.P), Tc / kLseRows));
-  pl.o_part = lse_pass ? l.take(8 * static_cast<size_t>(pl.S) * 4 * Tc) : 0;
-  pl.o_wide = pl.fused ? l.take(8 * static_cast<size_t>(pl.S) * 4 * Tc) : 0;
+  pl.o_part = lse_pass ? l.take(8 * static_cast<size_t>(pl.S) * kMaxHeadSlots * Tc) : 0;
+  pl.o_wide = pl.fused ? l.take(8 * static_cast<size_t>(pl.S) * kMaxHeadSlots * Tc) : 0;
   pl.o_m2 = pl.fused ? l.take(4 * Tc) : 0;
   pl.o_h2 = pl.fused ? l.take(4 * Tc) : 0;
   pl.o_low2 = pl.fused ? l.take(4 * Tc) : 0;
@@ -287,7 +294,7 @@ cudaError_t launch_softmax(int grid, const CUtensorMap& s, const CUtensorMap& x,
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit, std::memory_order_acq_rel);
   }
-  kern<<<grid, kTileThreads, smem, st>>>(s, x, o, sp);
+  kern<<<grid, SoftmaxCfg<DP, kPass>::THREADS, smem, st>>>(s, x, o, sp);
   return cudaGetLastError();
 }
 
@@ -371,7 +378,8 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   hp.keys = dE ? at<int>(ws, pl.o_keys) : nullptr;
   hp.share = dE ? at<float>(ws, pl.o_share) : nullptr;
   hp.coef = at<float>(ws, pl.o_coef);
-  hp.off16 = dE ? at<__nv_bfloat16>(ws, pl.o_off16) : nullptr;
+  hp.off16 = dE && pl.DP <= 128 ? at<__nv_bfloat16>(ws, pl.o_off16) : nullptr;
+  hp.b2 = dE && pl.DP > 128 ? at<float>(ws, pl.o_b2) : nullptr;
   hp.lse2 = at<float>(ws, pl.o_lse2);
   hp.lse_in = lse_in;
   hp.c2 = kLog2eF / p.tau;
@@ -381,9 +389,9 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
     hp.low2 = at<float>(ws, pl.o_low2);
   }
   hp.rescale = at<float>(ws, pl.o_rescale);
-  hp.row_blocks = static_cast<int>(ceil_div(p.T + 256, 8));
   hp.part = lse_in == nullptr ? at<float2>(ws, pl.o_part) : nullptr;
-  hp.slots = 4 * pl.S;
+  const int lse_slots = 2 * pl.S_lse * SoftmaxCfg<64, kPassLse>::GROUPS;   // slabs x groups a split
+  hp.slots = pl.fused ? 2 * pl.S * SoftmaxCfg<64, kPassRows>::GROUPS : lse_slots;
   hp.Tc = pl.Tc;
   hp.loss_part = at<double>(ws, pl.o_lpart);
   hp.loss = out.loss;
@@ -395,9 +403,13 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   {
     LaunchScope ls(CUTBCE_KERNEL_HEAD_PREP, st);
     k_head_rows<<<static_cast<unsigned>(pl.n_blk), 256, 0, st>>>(hp);
-    // the table's norms, when needed: up to 8 blocks an SM beside the positions' blocks
-    const int64_t norm_blocks = pl.fused ? std::min<int64_t>(ceil_div(p.V, 128), 8 * 148) : 0;
-    k_head_gather<<<static_cast<unsigned>(hp.row_blocks + norm_blocks), 256, 0, st>>>(hp);
+    if (pl.fused)
+      k_head_norm<<<static_cast<unsigned>(std::min<int64_t>(ceil_div(p.V, 128), 8 * 148)), 256, 0, st>>>(hp.E, p.V, hp.D,
+                                                                                                       hp.hdr);
+    const unsigned gather_grid = static_cast<unsigned>(ceil_div(p.T + 256, 8));
+    if (pl.DP == 64) k_head_gather<8><<<gather_grid, 256, 0, st>>>(hp);
+    else if (pl.DP == 128) k_head_gather<16><<<gather_grid, 256, 0, st>>>(hp);
+    else k_head_gather<32><<<gather_grid, 256, 0, st>>>(hp);
     if (pl.fused) k_head_ref<<<static_cast<unsigned>(ceil_div(pl.Tc, 256)), 256, 0, st>>>(hp);
     CUTBCE_CK(cudaGetLastError());
   }
@@ -411,15 +423,15 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   sp.tiles_per_split = pl.tps;
   sp.n_item_tiles_bn = pl.n_vtiles;
   sp.timeout_ns = kDefaultTimeoutNs;
-  CUtensorMap m_rows_s, m_items_x, m_items_s, m_rows_x;   // stationary / streamed maps of H_c and E
-  if (!make_map(&m_rows_s, hp.Hc, pl.DP, pl.Tc, pl.DP, kTileM) || !make_map(&m_items_x, p.E, p.D, p.V, p.D, pl.BN) ||
-      !make_map(&m_items_s, p.E, p.D, p.V, p.D, kTileM) || !make_map(&m_rows_x, hp.Hc, pl.DP, pl.Tc, pl.DP, pl.BN))
-    return CUTBCE_ERR_CUDA;
+  CUtensorMap m_rows_s;                                      // the positions as stationary operand
+  if (!make_map(&m_rows_s, hp.Hc, pl.DP, pl.Tc, pl.DP, kTileM)) return CUTBCE_ERR_CUDA;
   const int64_t row_items = static_cast<int64_t>(pl.S) * (pl.Tc / kTileM);
   const int row_grid = static_cast<int>(std::min<int64_t>({static_cast<int64_t>(dev.sms), row_items, static_cast<int64_t>(kMaxCtas)}));
   auto row_pass = [&]() -> cudaError_t {
     LaunchScope ls(CUTBCE_KERNEL_HEAD_ROW_PASS, st);
     sp.dh_part = at<float>(ws, pl.o_dhpart);
+    CUtensorMap m_items_x;
+    if (!make_map(&m_items_x, p.E, p.D, p.V, p.D, pl.BN)) return cudaErrorInvalidValue;
     return launch_softmax_dp<kPassRows>(pl.DP, row_grid, m_rows_s, m_items_x, m_items_x, sp, st);
   };
   if (lse_in == nullptr) {
@@ -427,12 +439,19 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
       LaunchScope ls(CUTBCE_KERNEL_HEAD_LSE_PASS, st);
       sp.part = at<float2>(ws, pl.fused ? pl.o_wide : pl.o_part);
       sp.only_wide = pl.fused ? 1 : 0;
-      CUTBCE_CK(launch_softmax_dp<kPassLse>(pl.DP, row_grid, m_rows_s, m_items_x, m_items_x, sp, st));
+      CUtensorMap m_lse_x;
+      if (!make_map(&m_lse_x, p.E, p.D, p.V, p.D, pl.BN_lse)) return CUTBCE_ERR_CUDA;
+      SoftmaxParams lp = sp;
+      lp.n_item_tiles_bn = pl.n_vtiles_lse;
+      lp.tiles_per_split = pl.tps_lse;
+      lp.nsplit = pl.S_lse;
+      CUTBCE_CK(launch_softmax_dp<kPassLse>(pl.DP, row_grid, m_rows_s, m_lse_x, m_lse_x, lp, st));
     }
     if (pl.fused) {
       sp.off2 = hp.m2;
       sp.part = at<float2>(ws, pl.o_part);
       sp.wide_part = at<float2>(ws, pl.o_wide);
+      sp.wide_slots = lse_slots;
       CUTBCE_CK(row_pass());
     }
     sp.part = nullptr;
@@ -491,8 +510,12 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
     sp.dE = out.dE;
     sp.de_bf16 = out.grad_dtype == CUTBCE_GRAD_BF16;
     sp.de_acc = (out.accumulate & CUTBCE_ACCUMULATE_DE) != 0;
-    CUtensorMap m_off;
-    if (!make_map_sw32(&m_off, hp.off16, pl.Tc, pl.BN)) return CUTBCE_ERR_CUDA;
+    sp.off2 = hp.b2;
+    CUtensorMap m_items_s, m_rows_x;
+    if (!make_map(&m_items_s, p.E, p.D, p.V, p.D, kTileM) || !make_map(&m_rows_x, hp.Hc, pl.DP, pl.Tc, pl.DP, pl.BN))
+      return CUTBCE_ERR_CUDA;
+    CUtensorMap m_off = m_rows_x;
+    if (hp.off16 != nullptr && !make_map_sw32(&m_off, hp.off16, pl.Tc, pl.BN)) return CUTBCE_ERR_CUDA;
     const int grid = static_cast<int>(std::min<int64_t>({static_cast<int64_t>(dev.sms), ceil_div(p.V, kTileM), static_cast<int64_t>(kMaxCtas)}));
     LaunchScope ls(CUTBCE_KERNEL_HEAD_ITEM_PASS, st);
     CUTBCE_CK(launch_softmax_dp<kPassItems>(pl.DP, grid, m_items_s, m_rows_x, m_off, sp, st));

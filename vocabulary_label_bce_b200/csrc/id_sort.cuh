@@ -473,34 +473,32 @@ template <int VEC, typename TOut>
 __global__ void __launch_bounds__(256) k_segment_join(const SegmentParams p, int64_t chunk_entries) {
   __shared__ float red[8][32 * VEC];
   if (*p.status != 0) return;
-  const int64_t c0 = blockIdx.x;
-  const int64_t last = (c0 + 1) * chunk_entries - 1;
-  if (last + 1 >= p.N) return;
-  const int id = p.keys[last];
-  if (id >= p.V || p.keys[last + 1] != id) return;                          // nothing continues
-  int64_t start = last;
-  {
-    // the segment's first index: in this chunk, or this chunk is a middle one
-    const int64_t b = c0 * chunk_entries;
-    if (p.keys[b] == id && b > 0 && p.keys[b - 1] == id) return;
-    int64_t lo = b, hi = last;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) >> 1;
-      if (p.keys[mid] < id) lo = mid + 1;
-      else hi = mid;
-    }
-    start = lo;
+  const int64_t c0 = blockIdx.x, b0 = c0 * chunk_entries, end = b0 + chunk_entries;
+  if (end >= p.N) return;
+  const int id = __ldg(p.keys + end - 1);
+  const bool goes_on = __ldg(p.keys + end) == id;
+  const bool middle = b0 > 0 && __ldg(p.keys + b0) == id && __ldg(p.keys + b0 - 1) == id;
+  if (id >= p.V || !goes_on || middle) return;          // nothing continues, or this chunk is not the segment's first
+  // the last chunk it reaches: chunks whose first entry has the id, 256 at a time
+  int64_t c1 = c0;
+  while (true) {
+    const int64_t at = (c1 + 1 + threadIdx.x) * chunk_entries;
+    const int hit = __syncthreads_count(at < p.N && __ldg(p.keys + min(at, p.N - 1)) == id);
+    c1 += hit;
+    if (hit < 256) break;
   }
-  // last chunk the segment reaches
-  int64_t c1;
-  {
-    int64_t lo = last + 1, hi = p.N;                                          // first index with a larger id
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) >> 1;
-      if (p.keys[mid] <= id) lo = mid + 1;
-      else hi = mid;
-    }
-    c1 = (lo - 1) / chunk_entries;
+  // its first entry (needed where sums are filed by it)
+  int64_t start = b0;
+  if (p.first != nullptr) {
+    int below = 0;
+    for (int64_t i = b0 + threadIdx.x; i < end; i += 256) below += __ldg(p.keys + i) < id;
+    __shared__ int s_below;
+    if (threadIdx.x == 0) s_below = 0;
+    __syncthreads();
+    below = __reduce_add_sync(0xffffffffu, below);
+    if ((threadIdx.x & 31) == 0) atomicAdd(&s_below, below);
+    __syncthreads();
+    start = b0 + s_below;
   }
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   for (int col0 = 0; col0 < p.D; col0 += 32 * VEC) {

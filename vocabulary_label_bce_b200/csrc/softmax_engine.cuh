@@ -12,7 +12,8 @@
 //          b_t = log2 |w_t| - l_t, and dE += +-P H.  Here a logit's row offset
 //          runs along the columns of the tile; b_t / c, split into three bf16
 //          values (24 bits), enters as one more K step of the logit MMA against
-//          ones, so the epilogue loads nothing.  Rows are compacted by the sign
+//          ones, so the epilogue loads nothing (2.89 to 2.44 ms at D = 64).  Above
+//          D = 128 the pass is bound by the MMAs, and the epilogue loads b_t.  Rows are compacted by the sign
 //          of w_t (the negative ones from a tile boundary on), so the sign is
 //          the negate-A bit of the contraction's instruction descriptor.
 //
@@ -38,24 +39,28 @@ template <int DP, int kPass>
 struct SoftmaxCfg {
   static constexpr bool kGrad = kPass != kPassLse;
   static constexpr bool kItems = kPass == kPassItems;
-  static constexpr int GROUPS = 2;
-  static constexpr int GROUP_WARPS = kNumEpiWarps / GROUPS;
+  static constexpr int GROUPS = 2;                          // epilogue groups taking tiles in turn
+  // the dE pass's exponent offsets as one more K step of the logit MMA (see the top)
+  static constexpr bool OFF_MMA = kItems && DP <= 128;
+  static constexpr int GROUP_WARPS = 8;
+  static constexpr int G_WARP = 2 + GROUPS * GROUP_WARPS;   // issuer of the contractions
+  static constexpr int THREADS = 32 * (kGrad ? G_WARP + 1 : G_WARP);
   static constexpr int SLABS = GROUP_WARPS / 4;
-  static constexpr int BN = DP <= 128 ? 128 : 64;           // streamed rows per tile
+  static constexpr int BN = DP == 64 && !kGrad ? 256 : DP <= 128 ? 128 : 64;   // streamed rows per tile
   static constexpr int NKB = DP / 64;
-  static constexpr int NX = DP == 64 ? (kItems ? 9 : 12) : DP == 128 ? 5 : DP == 192 ? (kItems ? 6 : 7) : 4;
-  static constexpr int NZ = kGrad ? 3 : 4;                  // logit buffers in tensor memory
+  static constexpr int NX = DP == 64 ? (kItems ? 9 : BN == 256 ? 6 : 12) : DP == 128 ? 5 : DP == 192 ? 7 : 4;
+  static constexpr int NZ = kGrad ? 3 : BN == 256 ? 2 : 4;  // logit buffers in tensor memory
   static constexpr uint32_t S_BYTES = kTileM * DP * 2;
   static constexpr uint32_t X_BYTES = BN * DP * 2;
-  static constexpr uint32_t O_BYTES = kItems ? BN * 32 : 0;         // exponent offsets of a streamed tile (16 bf16 a row)
-  static constexpr uint32_t ONES_BYTES = kItems ? kTileM * 32 : 0;  // their other operand
+  static constexpr uint32_t O_BYTES = OFF_MMA ? BN * 32 : 0;         // exponent offsets of a streamed tile (16 bf16 a row)
+  static constexpr uint32_t ONES_BYTES = OFF_MMA ? kTileM * 32 : 0;  // their other operand
   static constexpr int ZC = BN / SLABS;                     // logit columns per epilogue warp (64 or 32)
-  static constexpr int ACC_COL = 3 * BN;
+  static constexpr int ACC_COL = kGrad ? 3 * BN : 0;
   static constexpr int S_COL = ACC_COL + DP;
   static constexpr bool S_IN_TMEM = kGrad && S_COL + DP / 2 <= 512;
-  static constexpr int NUM_BARS = 2 + 2 * NX + 3 * NZ + 2 + GROUPS;
+  static constexpr int NUM_BARS = 2 + 2 * NX + 3 * NZ + 3 + GROUPS;
   static constexpr uint32_t SMEM_BYTES = 1024 + S_BYTES + NX * (X_BYTES + O_BYTES) + ONES_BYTES + NUM_BARS * 8 + 16 + 64;
-  static_assert(ACC_COL + DP <= 512 && NZ * BN <= 512, "TMEM budget");
+  static_assert((!kGrad || ACC_COL + DP <= 512) && NZ * BN <= 512, "TMEM budget");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static_assert(SMEM_BYTES > 232448 / 2, "one CTA per SM keeps the TMEM allocation uncontended");
 };
@@ -65,9 +70,10 @@ struct SoftmaxParams {
   int64_t Tc;                  // rows of the compacted buffers
   HeadHeader* hdr;
   float c2;                    // log2(e) / tau
-  const float* off2;           // kRows: [Tc] l_t (log2 domain)
+  const float* off2;           // kRows: [Tc] l_t; kItems without OFF_MMA: [Tc] b_t (log2 domain)
   float2* part;                // kLse, and kRows where it takes the sums: [splits * groups * slabs, Tc] (reference, sum)
   const float2* wide_part;     // kRows: partials of the log-sum-exp pass, the reference where hdr->wide is set
+  int wide_slots;              // their number per row
   int only_wide;               // kLse: run only where hdr->wide is set
   float* dh_part;              // kRows: [splits, Tc, DP]
   const int* first;            // kItems: [V] row of `sparse` of each item, -1 none
@@ -79,10 +85,11 @@ struct SoftmaxParams {
 };
 
 // Pairs of every 16 whose exponential runs on the FMA pipe instead of the SFU.
-// Measured at T V = 9.0e9 logits, D = 64, for 0 / 2 / 4 / 6 / 8 pairs: log-sum-exp
-// pass 2.41 / 2.23 / 2.10 / 2.16 / 2.42 ms, dH pass 2.52 / 2.36 / 2.43 / 2.60 /
-// 2.65 ms, dE pass 2.56 / 2.44 / 2.53 ms (0 / 2 / 4).
-constexpr int kPolyLse = 4, kPolyRows = 2, kPolyItems = 2;
+// Measured at 9.0e9 logits, D = 64, for 2 / 3 / 4 pairs: dH pass 2.20 / 2.20 / 2.17
+// ms, dE pass 2.23 / 2.15 / 2.09 ms; log-sum-exp pass for 4 / 5 / 6: 2.09 / 2.02 /
+// 2.05 ms.
+constexpr int kPolyLse = 5, kPolyRows = 4, kPolyItems = 4;
+
 // 2^x of a pair on the FMA pipe, x clamped below at -125: as exp2_poly3_pair, with
 // the degree chosen by what the value feeds.  kDegree 3 (relative error 7.5e-5) for
 // values that are rounded to bf16 next, 4 (2.7e-6) for the sums of a log-sum-exp.
@@ -125,7 +132,7 @@ __device__ __forceinline__ void mask_tail(uint32_t (&r)[32], int valid) {
 }
 
 template <int DP, int kPass>
-__global__ void __launch_bounds__(kTileThreads, 1)
+__global__ void __launch_bounds__(SoftmaxCfg<DP, kPass>::THREADS, 1)
     k_softmax(const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmX,
               const __grid_constant__ CUtensorMap tmO, SoftmaxParams p) {
   constexpr bool kGrad = kPass != kPassLse;
@@ -150,7 +157,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint64_t* bar_pready = bar_zfree + NZ;          // [NZ] P written over the logits (epilogue)
   uint64_t* bar_accfull = bar_pready + NZ;        // [groups] accumulator complete, for the group that reads it (commit)
   uint64_t* bar_accempty = bar_accfull + Cfg::GROUPS;  // accumulator read out (epilogue)
-  uint64_t* bar_drain = bar_accempty + 1;
+  uint64_t* bar_drain = bar_accempty + 1;         // every logit MMA done
+  uint64_t* bar_gdrain = bar_drain + 1;           // every contraction done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::NUM_BARS);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
@@ -173,8 +181,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // no position counts: dE is zero
     if (p.de_acc) return;
     const int64_t n = static_cast<int64_t>(p.V) * p.D;
-    for (int64_t k = static_cast<int64_t>(blockIdx.x) * kTileThreads + threadIdx.x; k < n;
-         k += static_cast<int64_t>(gridDim.x) * kTileThreads) {
+    for (int64_t k = static_cast<int64_t>(blockIdx.x) * Cfg::THREADS + threadIdx.x; k < n;
+         k += static_cast<int64_t>(gridDim.x) * Cfg::THREADS) {
       if (p.de_bf16) static_cast<__nv_bfloat16*>(p.dE)[k] = __float2bfloat16_rn(0.f);
       else static_cast<float*>(p.dE)[k] = 0.f;
     }
@@ -197,15 +205,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     for (int g = 0; g < Cfg::GROUPS; ++g) mbar_init(bar_accfull + g, 1);
     mbar_init(bar_accempty, Cfg::GROUP_WARPS);
     mbar_init(bar_drain, 1);
+    mbar_init(bar_gdrain, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmS);
     tma_prefetch_desc(&tmX);
-    if (kItems) tma_prefetch_desc(&tmO);
+    if (Cfg::OFF_MMA) tma_prefetch_desc(&tmO);
   }
-  if (kItems) {
+  if (Cfg::OFF_MMA) {
     // the two 16-byte halves of a row trade places in rows 4..7 of each 8 (32-byte swizzle)
     if (threadIdx.x < kTileM) {
       const int r = threadIdx.x, sw = (r >> 2) & 1;
@@ -256,7 +265,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             break;
           }
           mbar_arrive_expect_tx(bar_xfull + st, X_BYTES + Cfg::O_BYTES);
-          if (kItems) tma_load_2d(sO + st * Cfg::O_BYTES, &tmO, 0, (x0 + j) * BN, bar_xfull + st);
+          if (Cfg::OFF_MMA) tma_load_2d(sO + st * Cfg::O_BYTES, &tmO, 0, (x0 + j) * BN, bar_xfull + st);
 #pragma unroll
           for (int kb = 0; kb < NKB; ++kb)
             tma_load_2d(sX + st * X_BYTES + kb * (BN * 128), &tmX, kb * 64, (x0 + j) * BN, bar_xfull + st);
@@ -275,150 +284,114 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else if (warp == 1) {
     // ============================================================ MMA issuer
-    // An event loop over two in-order streams, logit tiles Z(c) into buffer
-    // c mod NZ and contractions of P(c); whichever is ready is issued.  Lanes 0-4
-    // test one barrier each, a ballot gathers the answers.
+    // The logit tiles, in order, by blocking waits.  The contractions have a warp of
+    // their own: one warp polling for both took 1250 cycles a tile even with no element
+    // math at all, this form 820.
     constexpr uint32_t idesc_z = idesc_bf16_f32(kTileM, BN, false, false);
-    constexpr uint32_t idesc_acc = idesc_bf16_f32(kTileM, DP, false, true);
-    constexpr uint32_t kNegateA = 1u << 13;
     constexpr uint32_t kXStep = X_BYTES >> 4;
-    constexpr int kKsPerSlab = ZC / 16;
     const uint64_t dS = smem_desc_sw128(smem_u32(sS), 16, 1024);
     const uint64_t dXk = smem_desc_sw128(smem_u32(sX), 16, 1024);
     const uint64_t dO = smem_desc_sw32(smem_u32(sO)), dOne = smem_desc_sw32(smem_u32(sOne));
-    const uint64_t dXmn = smem_desc_sw128(smem_u32(sX), BN * 128, 1024);
-    const uint32_t tAcc = tmem_base + Cfg::ACC_COL, tS = tmem_base + Cfg::S_COL;
-    int zi = blockIdx.x, zj = 0, zn = 0, gi = zi, gj = 0, gn = 0;
-    int row0, x0, split;
-    uint32_t zic = 0, cz = 0, gic = 0, cg = 0;
-    uint32_t zst = 0, zph = 0, gst = 0, zb = 0, zbph = 0, gb = 0, gbph = 0;
-    bool s_ready = false;
-    item(zi, row0, x0, zn, split);
-    gn = zn;
-    uint64_t idle_since = 0;
+    const uint32_t tS = tmem_base + Cfg::S_COL;
+    uint32_t ic = 0, c = 0, st = 0, ph = 0, zb = 0, zph = 0;
     bool ok = true;
-    while (ok && (zi < n_items || (kGrad && gi < n_items))) {
-      bool progressed = false;
-      const bool want_z = zi < n_items;
-      const bool want_g = kGrad && gi < n_items && cg < cz;
-      bool mine = false;
-      if (lane == 0 && want_z && zj == 0 && !s_ready) mine = mbar_test_wait(bar_sfull, zic & 1);
-      if (lane == 1 && want_z) mine = mbar_test_wait(bar_xfull + zst, zph);
-      if (lane == 2 && want_z) mine = mbar_test_wait(bar_zfree + zb, zbph ^ 1);
-      if (lane == 3 && want_g) mine = mbar_test_wait(bar_pready + gb, gbph);
-      if (lane == 4 && want_g && gj == 0) mine = mbar_test_wait(bar_accempty, (gic & 1) ^ 1);
-      const uint32_t ready = __ballot_sync(0xffffffffu, mine);
-      if (want_z) {
-        if (zj == 0 && !s_ready && (ready & 1u)) {
-          tc_fence_after();
-          s_ready = true;
-          if (Cfg::S_IN_TMEM) {
-            if (elect_one()) {
-#pragma unroll
-              for (int ks = 0; ks < DP / 16; ++ks)
-                tmem_cp_128x256b(tS + 8 * ks, dS + static_cast<uint32_t>((ks >> 2) * (kTileM * 8) + (ks & 3) * 2));
-              umma_commit(bar_sempty);
-            }
-            __syncwarp();
-          }
-        }
-        if ((zj > 0 || s_ready) && (ready & 6u) == 6u) {
-          tc_fence_after();
-          const uint64_t dB = dXk + zst * kXStep;
-          const uint32_t tD = tmem_base + zb * BN;
-          if (elect_one()) {
-#pragma unroll
-            for (int ks = 0; ks < DP / 16; ++ks) {
-              const uint64_t bd = dB + static_cast<uint32_t>((ks >> 2) * (BN * 8) + (ks & 3) * 2);
-              if (Cfg::S_IN_TMEM) umma_bf16_tmem_a(tD, tS + 8 * ks, bd, idesc_z, ks > 0 ? 1u : 0u);
-              else umma_bf16(tD, dS + static_cast<uint32_t>((ks >> 2) * (kTileM * 8) + (ks & 3) * 2), bd, idesc_z,
-                             ks > 0 ? 1u : 0u);
-            }
-            if (kItems) umma_bf16(tD, dOne, dO + zst * (Cfg::O_BYTES >> 4), idesc_z, 1u);
-            umma_commit(bar_zfull + zb);
-            if (!kGrad) umma_commit(bar_xempty + zst);
-            if (!Cfg::S_IN_TMEM && zj + 1 == zn) umma_commit(bar_sempty);
-          }
-          __syncwarp();
-          progressed = true;
-          ++cz;
-          if (++zst == static_cast<uint32_t>(NX)) {
-            zst = 0;
-            zph ^= 1;
-          }
-          if (++zb == static_cast<uint32_t>(NZ)) {
-            zb = 0;
-            zbph ^= 1;
-          }
-          if (++zj == zn) {
-            zj = 0;
-            ++zic;
-            s_ready = false;
-            zi += gridDim.x;
-            if (zi < n_items) item(zi, row0, x0, zn, split);
-          }
-        }
-      }
-      if (want_g && (ready & 8u) && (gj > 0 || (ready & 16u))) {
-        tc_fence_after();
-        const uint64_t dB = dXmn + gst * kXStep;
-        const uint32_t tA = tmem_base + gb * BN;
-        const bool last = gj + 1 == gn;
-        const uint32_t idesc = kItems && gj >= neg_tile ? idesc_acc | kNegateA : idesc_acc;
+    for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x, ++ic) {
+      int row0, x0, nx, split;
+      item(i, row0, x0, nx, split);
+      if (!wait_bar_warp(bar_sfull, ic & 1, wc, wait_tag(2, 0, ic))) break;
+      tc_fence_after();
+      if (Cfg::S_IN_TMEM) {
         if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < BN / 16; ++ks) {
-            // slab k of the P tile sits in the first half of the logit columns of slab k
-            const uint32_t a_col = (ks / kKsPerSlab) * ZC + 8 * (ks % kKsPerSlab);
-            umma_bf16_tmem_a(tAcc, tA + a_col, dB + static_cast<uint32_t>(ks * 128), idesc, (gj > 0 || ks > 0) ? 1u : 0u);
-          }
-          umma_commit(bar_zfree + gb);
-          umma_commit(bar_xempty + gst);
-          if (last) umma_commit(bar_accfull + cg % Cfg::GROUPS);
+          for (int ks = 0; ks < DP / 16; ++ks)
+            tmem_cp_128x256b(tS + 8 * ks, dS + static_cast<uint32_t>((ks >> 2) * (kTileM * 8) + (ks & 3) * 2));
+          umma_commit(bar_sempty);
         }
         __syncwarp();
-        progressed = true;
-        ++cg;
-        if (++gst == static_cast<uint32_t>(NX)) gst = 0;
-        if (++gb == static_cast<uint32_t>(NZ)) {
-          gb = 0;
-          gbph ^= 1;
-        }
-        if (last) {
-          gj = 0;
-          ++gic;
-          gi += gridDim.x;
-          if (gi < n_items) item(gi, row0, x0, gn, split);
-        } else {
-          ++gj;
-        }
       }
-      if (progressed) {
-        idle_since = 0;
-      } else {
-        // bounded: give up if nothing became ready within the limit
-        const uint64_t now = global_timer_ns();
-        if (idle_since == 0) idle_since = now;
-        int give_up = 0;
-        if (lane == 0) {
-          if (*reinterpret_cast<volatile int*>(abort_flag)) {
-            give_up = 1;
-          } else if (static_cast<long long>(now - idle_since) > p.timeout_ns) {
-            *reinterpret_cast<volatile int*>(abort_flag) = 1;
-            if (atomicCAS(&hdr->status, 0, kErrTimeout) == 0) {
-              hdr->wait_tag = wait_tag(2, 15, cz);
-              hdr->wait_block = static_cast<int>(blockIdx.x);
-            }
-            give_up = 1;
-          }
+      for (int j = 0; j < nx; ++j, ++c) {
+        if (!wait_bar_warp(bar_xfull + st, ph, wc, wait_tag(2, 1, c)) ||
+            !wait_bar_warp(bar_zfree + zb, zph ^ 1, wc, wait_tag(2, 2, c))) {
+          ok = false;
+          break;
         }
-        if (__shfl_sync(0xffffffffu, give_up, 0)) ok = false;
+        tc_fence_after();
+        const uint64_t dB = dXk + st * kXStep;
+        const uint32_t tD = tmem_base + zb * BN;
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < DP / 16; ++ks) {
+            const uint64_t bd = dB + static_cast<uint32_t>((ks >> 2) * (BN * 8) + (ks & 3) * 2);
+            if (Cfg::S_IN_TMEM) umma_bf16_tmem_a(tD, tS + 8 * ks, bd, idesc_z, ks > 0 ? 1u : 0u);
+            else umma_bf16(tD, dS + static_cast<uint32_t>((ks >> 2) * (kTileM * 8) + (ks & 3) * 2), bd, idesc_z,
+                           ks > 0 ? 1u : 0u);
+          }
+          if (Cfg::OFF_MMA) umma_bf16(tD, dOne, dO + st * (Cfg::O_BYTES >> 4), idesc_z, 1u);
+          umma_commit(bar_zfull + zb);
+          if (!kGrad) umma_commit(bar_xempty + st);
+          if (!Cfg::S_IN_TMEM && j + 1 == nx) umma_commit(bar_sempty);
+        }
+        __syncwarp();
+        if (++st == static_cast<uint32_t>(NX)) {
+          st = 0;
+          ph ^= 1;
+        }
+        if (++zb == static_cast<uint32_t>(NZ)) {
+          zb = 0;
+          zph ^= 1;
+        }
       }
     }
     // every MMA this warp issued has completed once the drain barrier flips
     if (elect_one()) umma_commit(bar_drain);
     __syncwarp();
     if (lane == 0) wait_bar_drain(bar_drain, 0, p.timeout_ns);
+    __syncwarp();
+  } else if (kGrad && warp == Cfg::G_WARP) {
+    // ============================================================ contraction issuer
+    constexpr uint32_t idesc_acc = idesc_bf16_f32(kTileM, DP, false, true);
+    constexpr uint32_t kNegateA = 1u << 13;
+    constexpr uint32_t kXStep = X_BYTES >> 4;
+    constexpr int kKsPerSlab = ZC / 16;
+    const uint64_t dXmn = smem_desc_sw128(smem_u32(sX), BN * 128, 1024);
+    const uint32_t tAcc = tmem_base + Cfg::ACC_COL;
+    uint32_t ic = 0, c = 0, st = 0, gb = 0, gph = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x, ++ic) {
+      int row0, x0, nx, split;
+      item(i, row0, x0, nx, split);
+      if (!wait_bar_warp(bar_accempty, (ic & 1) ^ 1, wc, wait_tag(2, 4, ic))) break;
+      for (int j = 0; j < nx; ++j, ++c) {
+        if (!wait_bar_warp(bar_pready + gb, gph, wc, wait_tag(2, 3, c))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t dB = dXmn + st * kXStep;
+        const uint32_t tA = tmem_base + gb * BN;
+        const bool last = j + 1 == nx;
+        const uint32_t idesc = kItems && j >= neg_tile ? idesc_acc | kNegateA : idesc_acc;
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < BN / 16; ++ks) {
+            const uint32_t a_col = (ks / kKsPerSlab) * ZC + 8 * (ks % kKsPerSlab);
+            umma_bf16_tmem_a(tAcc, tA + a_col, dB + static_cast<uint32_t>(ks * 128), idesc, (j > 0 || ks > 0) ? 1u : 0u);
+          }
+          umma_commit(bar_zfree + gb);
+          umma_commit(bar_xempty + st);
+          if (last) umma_commit(bar_accfull + c % Cfg::GROUPS);
+        }
+        __syncwarp();
+        if (++st == static_cast<uint32_t>(NX)) st = 0;
+        if (++gb == static_cast<uint32_t>(NZ)) {
+          gb = 0;
+          gph ^= 1;
+        }
+      }
+    }
+    if (elect_one()) umma_commit(bar_gdrain);
+    __syncwarp();
+    if (lane == 0) wait_bar_drain(bar_gdrain, 0, p.timeout_ns);
     __syncwarp();
   } else {
     // ============================================================ epilogue
@@ -442,7 +415,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         m = __ldg(p.off2 + s_row0 + row);
         if (p.wide_part != nullptr && s_wide) {
           // the row's log-sum-exp from the partials of the pass before
-          const int slots = p.nsplit * Cfg::GROUPS * Cfg::SLABS;
+          const int slots = p.wide_slots;
           float mx = -3.0e38f, s = 0.f;
           for (int k = 0; k < slots; ++k) mx = fmaxf(mx, p.wide_part[k * p.Tc + s_row0 + row].x);
           for (int k = 0; k < slots; ++k) {
@@ -475,21 +448,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const int col = tile_col0 + ch * 32;
           if (tail) mask_tail(r, p.V - col);
           if constexpr (kPass == kPassLse) {
-            float mx = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+            float mx4[4];
 #pragma unroll
-            for (int e = 2; e < 32; e += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(r[e]), __uint_as_float(r[e + 1])));
-            mx *= p.c2;
+            for (int k = 0; k < 4; ++k) {
+              mx4[k] = fmaxf(__uint_as_float(r[8 * k]), __uint_as_float(r[8 * k + 1]));
+#pragma unroll
+              for (int e = 2; e < 8; e += 2)
+                mx4[k] = fmaxf(mx4[k], fmaxf(__uint_as_float(r[8 * k + e]), __uint_as_float(r[8 * k + e + 1])));
+            }
+            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.c2;
             // the reference moves only when the maximum has grown by 2^8: sums stay far from overflow
             const float mn = mx > m + 8.f ? mx : m;
             sum *= ex2_approx(m - mn);
             m = mn;
             const float2 nm = f2(-m, -m);
-            float2 s2 = f2(0.f, 0.f);
+            float2 s4[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               const float2 x = __ffma2_rn(f2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), c2, nm);
-              s2 = __fadd2_rn(s2, exp2_pair<kPolyLse, 4>(e >> 1, x));
+              s4[(e >> 1) & 3] = __fadd2_rn(s4[(e >> 1) & 3], exp2_pair<kPolyLse, 4>(e >> 1, x));
             }
+            const float2 s2 = __fadd2_rn(__fadd2_rn(s4[0], s4[1]), __fadd2_rn(s4[2], s4[3]));
             sum += s2.x + s2.y;
           } else {
             uint32_t pk[16];
@@ -497,7 +476,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               const float2 z = f2(__uint_as_float(r[e]), __uint_as_float(r[e + 1]));
-              const float2 x = kItems ? __fmul2_rn(z, c2) : __ffma2_rn(z, c2, f2(off, off));
+              float2 x;
+              if (Cfg::OFF_MMA) x = __fmul2_rn(z, c2);
+              else if (kItems) x = __ffma2_rn(z, c2, __ldg(reinterpret_cast<const float2*>(p.off2 + col + e)));
+              else x = __ffma2_rn(z, c2, f2(off, off));
               const float2 y = kItems ? exp2_pair<kPolyItems, 3>(e >> 1, x) : exp2_pair<kPolyRows, 4>(e >> 1, x);
               if (!kItems) s2 = __fadd2_rn(s2, y);
               pk[e >> 1] = pack_bf16x2(y.x, y.y);

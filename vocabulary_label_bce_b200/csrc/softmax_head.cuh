@@ -68,14 +68,14 @@ struct HeadParams {
   int* keys;                     // [T * K] ids of the pairs (-1 none), or null
   float* share;                  // [T * K] q of the pairs, or null
   float* coef;                   // [T] signed factor of the row's gradient
-  __nv_bfloat16* off16;          // [Tc, 16] (log2 |factor| - lse) tau in three bf16 pieces, then zeros (with dE)
+  float* b2;                     // [Tc] log2 |factor| - lse (log2 domain; with dE, wide D), or null
+  __nv_bfloat16* off16;          // [Tc, 16] (log2 |factor| - lse) tau in three bf16 pieces, then zeros (with dE), or null
   float* lse2;                   // [Tc] lse in the log2 domain
   const float* lse_in;           // [T] lse of an earlier forward, or null
   float* m2;                     // [Tc] reference of the row's exponentials in the dH pass, or null
   float* h2;                     // [Tc] |h|^2, with m2
   float* low2;                   // [Tc] a logit that the row has (log2 domain), with m2
   float c2;                      // log2(e) / tau
-  int row_blocks;                // blocks of the gather that take positions (the rest read E's norms)
   float* rescale;                // [Tc] 2^(reference - lse): factor of the dense part of dH
   const float2* part;            // [slots, Tc] (reference, sum) partials in the log2 domain
   int slots;
@@ -86,10 +86,13 @@ struct HeadParams {
   float* logp_out;               // [2P] output or null
 };
 
-// The exponent offset u of a row of the item-owned pass as three bf16 values whose
-// sum is u to 24 bits; clamped to +-1e30 (2^(c u) is 0 there, as for padding).
-__device__ __forceinline__ void write_offset(const HeadParams& p, int64_t c, float u) {
+// The exponent offset b of a row of the item-owned pass (log2 domain): as it is, or
+// u = b / c2 as three bf16 values whose sum is u to 24 bits; clamped to +-1e30 (2^b is
+// 0 there, as for padding).
+__device__ __forceinline__ void write_offset(const HeadParams& p, int64_t c, float b2) {
+  if (p.b2 != nullptr) p.b2[c] = b2;
   if (p.off16 == nullptr) return;
+  float u = b2 / p.c2;
   if (u == u) u = fminf(fmaxf(u, -1e30f), 1e30f);
   const float a = __bfloat162float(__float2bfloat16_rn(u));
   const float b = __bfloat162float(__float2bfloat16_rn(u - a));
@@ -208,61 +211,79 @@ __global__ void __launch_bounds__(256) k_head_rows(const HeadParams p) {
   }
 }
 
-// ------------------------------------------------------------------ gather
-// One warp per position, then one warp per padding row (256 of them at most).
-// Lane l holds the column pairs l, l + 32, ... of the row.  The targets' rows of
-// E are read kGatherU at a time.
-constexpr int kGatherU = 4;
-
-// Largest |e_v|^2 over the table, by the gather's blocks past the positions: eight
-// lanes a row, 16 bytes a lane.  The maximum is over float bits (all >= 0), so the
-// order of the atomics changes nothing; a NaN stays the maximum.
-__device__ void head_table_norm(const HeadParams& p) {
+// ------------------------------------------------------------------ norm
+// Largest |e_v|^2 over the table: eight lanes a row, 16 bytes a lane, four rows in
+// flight.  The maximum is over float bits (all >= 0), so the order of the atomics
+// changes nothing; a NaN stays the maximum.
+__global__ void __launch_bounds__(256) k_head_norm(const __nv_bfloat16* __restrict__ E, int64_t V, int D, HeadHeader* hdr) {
+  constexpr int U = 4;
   const int sub = threadIdx.x & 7;
-  const int64_t step = (static_cast<int64_t>(gridDim.x) - p.row_blocks) * 32;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 32;
   unsigned best = 0u;
   // every lane of a warp runs the same trips, so that the sums below are whole
-  for (int64_t v0 = (static_cast<int64_t>(blockIdx.x) - p.row_blocks) * 32; v0 < p.V; v0 += step) {
-    const int64_t v = v0 + (threadIdx.x >> 3);
-    float s = 0.f;
-    if (v < p.V) {
-      const uint4* src = reinterpret_cast<const uint4*>(p.E + v * p.D);
-      for (int i = sub; i < p.D / 8; i += 8) {
-        const uint4 x = __ldg(src + i);
-        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+  for (int64_t v0 = static_cast<int64_t>(blockIdx.x) * 32; v0 < V; v0 += U * step) {
+    float s[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) s[u] = 0.f;
+    for (int i = sub; i < D / 8; i += 8) {
+      uint4 x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t v = min(v0 + u * step + (threadIdx.x >> 3), V - 1);     // a row read twice changes nothing
+        x[u] = __ldg(reinterpret_cast<const uint4*>(E + v * D) + i);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float a = __uint_as_float(u[k] << 16), b = __uint_as_float(u[k] & 0xFFFF0000u);
-          s = fmaf(a, a, fmaf(b, b, s));
+          const float a = __uint_as_float(w[k] << 16), b = __uint_as_float(w[k] & 0xFFFF0000u);
+          s[u] = fmaf(a, a, fmaf(b, b, s[u]));
         }
       }
     }
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    best = max(best, __float_as_uint(s) & 0x7FFFFFFFu);
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+      best = max(best, __float_as_uint(s[u]) & 0x7FFFFFFFu);
+    }
   }
   best = __reduce_max_sync(0xffffffffu, best);
-  if ((threadIdx.x & 31) == 0) atomicMax(&p.hdr->emax2, best);
+  if ((threadIdx.x & 31) == 0 && best > *reinterpret_cast<volatile unsigned*>(&hdr->emax2)) atomicMax(&hdr->emax2, best);
 }
 
+// ------------------------------------------------------------------ gather
+// One warp per position, then one warp per padding row (256 of them at most).
+// `L` lanes hold a row in 16-byte pieces (8, 16 or 32 for DP = 64, 128 and above),
+// so a warp reads the rows of 32 / L targets at once, kGatherU of those in flight.
+constexpr int kGatherU = 4;
+
+__device__ __forceinline__ void unpack8(uint4 r, float (&x)[8]) {
+  const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x[2 * k] = __uint_as_float(u[k] << 16);
+    x[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+  }
+}
+
+template <int L>
 __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
+  constexpr int G = 32 / L;                     // targets side by side
   const HeadHeader* hdr = p.hdr;
   if (hdr->w.status != 0) return;
-  if (static_cast<int>(blockIdx.x) >= p.row_blocks) {
-    head_table_norm(p);
-    return;
-  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane % L, grp = lane / L;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + warp;
-  const int pairs = p.DP / 64;                  // column pairs per lane (1 .. 4)
+  const bool piece = 8 * sub < p.DP, real = 8 * sub < p.D;       // this lane's piece of a padded row, and of a row
   if (t >= p.T) {
     // padding rows: [n_pos, neg0) and [neg0 + n_neg, n_rows)
     const int j = static_cast<int>(t - p.T);
     const int gap = hdr->neg0 - hdr->n_pos;
     const int64_t c = j < gap ? hdr->n_pos + j : hdr->neg0 + hdr->n_neg + (j - gap);
     if (c >= hdr->n_rows) return;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.Hc + c * p.DP);
-    for (int i = 0; i < pairs; ++i) dst[lane + 32 * i] = 0u;
+    if (grp == 0 && piece) reinterpret_cast<uint4*>(p.Hc + c * p.DP)[sub] = make_uint4(0u, 0u, 0u, 0u);
     if (lane == 0) {
       p.orig[c] = -1;
       write_offset(p, c, -1e30f);
@@ -286,39 +307,41 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
     }
     return;
   }
+  // the row, and the ids and logits of its slots (slot k = lane + 32 j), all in flight
+  const uint4 hraw = real ? __ldg(reinterpret_cast<const uint4*>(p.H + t * p.D) + sub) : make_uint4(0u, 0u, 0u, 0u);
+  float q[4], lq[4];
+  int id[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int k = lane + 32 * j;
+    id[j] = k < p.K ? __ldg(p.ids + r + k) : -1;
+    lq[j] = p.kind == kHeadDistill && k < p.K ? __ldg(p.logits + r + k) : 0.f;
+  }
   // compacted row: this block's prefix plus the rows of the class before t in its 256
   int64_t c;
   {
     const int b = static_cast<int>(t >> 8);
+    const int n = static_cast<int>(t & 255);
     int before = 0;
-    for (int i = lane; i < static_cast<int>(t & 255); i += 32) before += p.cls[(static_cast<int64_t>(b) << 8) + i] == cls;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = lane + 32 * i;
+      if (k < n) before += p.cls[(static_cast<int64_t>(b) << 8) + k] == cls;
+    }
     before = __reduce_add_sync(0xffffffffu, before);
     c = p.blk[2 * b + cls - 1] + before + (cls == 2 ? hdr->neg0 : 0);
   }
-  float2 h[4], sp[4];
-  {
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(p.H + t * p.D);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.Hc + c * p.DP);
+  if (grp == 0 && piece) reinterpret_cast<uint4*>(p.Hc + c * p.DP)[sub] = hraw;
+  float h[8], sp[8];
+  unpack8(hraw, h);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      h[i] = sp[i] = make_float2(0.f, 0.f);
-      if (i >= pairs) continue;
-      const int j = lane + 32 * i;
-      const uint32_t u = 2 * j < p.D ? __ldg(src + j) : 0u;
-      dst[j] = u;
-      h[i] = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
-    }
-  }
-  // the teacher's weights: slot k = lane + 32 j
-  float q[4], lq[4];
-  int id[4];
+  for (int k = 0; k < 8; ++k) sp[k] = 0.f;
+  // the targets' weights
   if (p.kind == kHeadDistill) {
     float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int k = lane + 32 * j;
-      id[j] = k < p.K ? __ldg(p.ids + r + k) : -1;
-      lq[j] = id[j] >= 0 ? __ldg(p.logits + r + k) * p.inv_tau : -INFINITY;
+      lq[j] = id[j] >= 0 ? lq[j] * p.inv_tau : -INFINITY;
       m = fmaxf(m, lq[j]);
     }
 #pragma unroll
@@ -343,9 +366,7 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
     for (int j = 0; j < 4; ++j) {
       q[j] = j == 0 && lane == 0 ? 1.f : 0.f;
       lq[j] = 0.f;
-      id[j] = -1;
     }
-    if (lane == 0) id[0] = __ldg(p.ids + t);
   }
   double term = 0.0;
   float zmax = -INFINITY;
@@ -357,37 +378,32 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
       p.keys[r + 32 * j + lane] = q[j] == 0.f ? -1 : id[j];
       p.share[r + 32 * j + lane] = q[j];
     }
-    for (int k = 0; k < n; k += kGatherU) {
-      float z[kGatherU], w[kGatherU], lw[kGatherU];
-      float2 e[kGatherU][4];
+    for (int k = 0; k < n; k += G * kGatherU) {
+      uint4 e[kGatherU];
+      float w[kGatherU], lw[kGatherU], z[kGatherU];
 #pragma unroll
       for (int u = 0; u < kGatherU; ++u) {
-        const int from = min(k + u, 31);
+        const int slot = k + u * G + grp, from = min(slot, 31);
         const int v = __shfl_sync(0xffffffffu, id[j], from);
         w[u] = __shfl_sync(0xffffffffu, q[j], from);
         lw[u] = __shfl_sync(0xffffffffu, lq[j], from);
-        z[u] = 0.f;
-        if (k + u >= n || v < 0 || v >= p.V) w[u] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          e[u][i] = make_float2(0.f, 0.f);
-          if (i >= pairs || w[u] == 0.f) continue;
-          const int col = lane + 32 * i;
-          const uint32_t x = 2 * col < p.D ? __ldg(reinterpret_cast<const uint32_t*>(p.E + static_cast<int64_t>(v) * p.D) + col) : 0u;
-          e[u][i] = make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
-        }
+        if (slot >= n || v < 0 || v >= p.V) w[u] = 0.f;
+        e[u] = w[u] != 0.f && real ? __ldg(reinterpret_cast<const uint4*>(p.E + static_cast<int64_t>(v) * p.D) + sub)
+                                   : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
       for (int u = 0; u < kGatherU; ++u) {
+        float x[8];
+        unpack8(e[u], x);
+        z[u] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          z[u] = fmaf(h[i].x, e[u][i].x, fmaf(h[i].y, e[u][i].y, z[u]));
-          sp[i].x = fmaf(w[u], e[u][i].x, sp[i].x);
-          sp[i].y = fmaf(w[u], e[u][i].y, sp[i].y);
+        for (int i = 0; i < 8; ++i) {
+          z[u] = fmaf(h[i], x[i], z[u]);
+          sp[i] = fmaf(w[u], x[i], sp[i]);
         }
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
+      for (int o = L / 2; o > 0; o >>= 1)
 #pragma unroll
         for (int u = 0; u < kGatherU; ++u) z[u] += __shfl_xor_sync(0xffffffffu, z[u], o);
 #pragma unroll
@@ -400,18 +416,21 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
       }
     }
   }
-  if (p.sparse != nullptr) {
-    float2* o = reinterpret_cast<float2*>(p.sparse + c * p.DP);
+  // the groups' parts, in a fixed order
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < pairs) o[lane + 32 * i] = sp[i];
+  for (int o = L; o < 32; o <<= 1) {
+    term += __shfl_xor_sync(0xffffffffu, term, o);
+    zmax = fmaxf(zmax, __shfl_xor_sync(0xffffffffu, zmax, o));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sp[i] += __shfl_xor_sync(0xffffffffu, sp[i], o);
   }
+  if (p.sparse != nullptr && grp == 0 && piece) store_floats<8>(p.sparse + c * p.DP + 8 * sub, sp);
   if (p.m2 != nullptr) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s = fmaf(h[i].x, h[i].x, fmaf(h[i].y, h[i].y, s));
+    for (int i = 0; i < 8; ++i) s = fmaf(h[i], h[i], s);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) {
       p.h2[c] = s;
       p.low2[c] = zmax * p.c2;
@@ -531,7 +550,7 @@ __global__ void __launch_bounds__(kLseThreads) k_head_lse(const HeadParams p) {
     if (p.lse_out != nullptr) p.lse_out[t] = static_cast<float>(lse);
     if (p.kind == kHeadDistill) {
       const float w = p.weights != nullptr ? p.weights[t] : 1.f;
-      write_offset(p, c, ((p.weights != nullptr ? log2f(fabsf(w)) : 0.f) - l2) / p.c2);
+      write_offset(p, c, (p.weights != nullptr ? log2f(fabsf(w)) : 0.f) - l2);
       row_loss = static_cast<double>(w) * p.tau * p.tau * (p.rowterm[c] + lse);
     }
   }
@@ -587,7 +606,7 @@ __global__ void __launch_bounds__(kPairThreads) k_head_pairs(const HeadParams p)
       const int c = p.cidx[t];
       if (c < 0) continue;
       p.coef[t] = q == 0 ? f : -f;
-      write_offset(p, c, (lf - p.lse2[c]) / p.c2);
+      write_offset(p, c, lf - p.lse2[c]);
     }
   }
   if (threadIdx.x == 0) {
