@@ -5,7 +5,7 @@ libcutbce's kernels (see include/cutbce.h).
 """
 from __future__ import annotations
 
-import contextlib
+import functools
 from typing import Optional
 
 import torch
@@ -129,13 +129,23 @@ def cut_bce(H, E, targets, mask=None, reduction: str = "mean") -> torch.Tensor:
 # stream, and take their workspace from torch's caching allocator per call, so
 # calls on several streams, and captured graphs, never share one.
 
-_HERE = contextlib.nullcontext()
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _on(t: torch.Tensor):
+def _on_cuda(t: torch.Tensor) -> None:
     if not t.is_cuda:
         raise ValueError(f"tensors must be on a CUDA device, not {t.device}")
-    return _HERE if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def _there(call):
+    """The call, made on the device of its first tensor."""
+    @functools.wraps(call)
+    def wrapped(first, *args, **kw):
+        if first.is_cuda and first.get_device() != _current_device():
+            with torch.cuda.device(first.device):
+                return call(first, *args, **kw)
+        return call(first, *args, **kw)
+    return wrapped
 
 
 def _plain(t: torch.Tensor) -> torch.Tensor:
@@ -161,17 +171,19 @@ def _workspace(nbytes: int, device: torch.device, given: Optional[torch.Tensor])
     return given if given is not None else torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
+@_there
 def embed_forward(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, status: Optional[torch.Tensor] = None):
     """scale * E[ids] (any shape of ids; -1 gives a zero row), in E's dtype (bf16 or fp32)."""
     if E.dim() != 2:
         raise ValueError("E must be [V, D]")
-    with _on(E):
-        X = torch.empty(ids.shape + E.shape[1:], dtype=E.dtype, device=E.device)
-        if ids.numel() > 0:
-            B.cutbce_embed_forward(_plain(E), _ids32(ids), X, scale, status)
+    _on_cuda(E)
+    X = torch.empty(ids.shape + E.shape[1:], dtype=E.dtype, device=E.device)
+    if ids.numel() > 0:
+        B.cutbce_embed_forward(_plain(E), _ids32(ids), X, scale, status)
     return X
 
 
+@_there
 def embed_backward(dX: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 1.0,
                    grad_dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None,
                    accumulate: bool = False, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -186,15 +198,14 @@ def embed_backward(dX: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 1
         raise ValueError("accumulate needs out")
     if out is not None and tuple(out.shape) != (V, D):
         raise ValueError(f"out must be [{V}, {D}]")
-    with _on(dX):
-        if ids.numel() == 0:
-            if out is None:
-                return torch.zeros((V, D), dtype=grad_dtype, device=dX.device)
-            return out if accumulate else out.zero_()
-        dE = out if out is not None else torch.empty((V, D), dtype=grad_dtype, device=dX.device)
-        ws = _workspace(B.cutbce_embed_workspace_size(ids.numel(), V, D), dX.device, workspace)
-        B.cutbce_embed_backward(_plain(dX).view(-1, D), _ids32(ids), dE, ws, scale,
-                                accumulate)
+    _on_cuda(dX)
+    if ids.numel() == 0:
+        if out is None:
+            return torch.zeros((V, D), dtype=grad_dtype, device=dX.device)
+        return out if accumulate else out.zero_()
+    dE = out if out is not None else torch.empty((V, D), dtype=grad_dtype, device=dX.device)
+    ws = _workspace(B.cutbce_embed_workspace_size(ids.numel(), V, D), dX.device, workspace)
+    B.cutbce_embed_backward(_plain(dX).view(-1, D), _ids32(ids), dE, ws, scale, accumulate)
     return dE
 
 
@@ -254,6 +265,7 @@ def _rows(H: torch.Tensor, *rest: Optional[torch.Tensor]):
 
 def _distill_problem(H, E, ids, logits, mask, weights, temperature, reduction):
     """The problem and the tensors it points to (to be kept until the launch)."""
+    _on_cuda(H)
     if logits.shape != ids.shape:
         raise ValueError("teacher ids and logits must have one shape")
     H2, ids2, lg, m, w = _rows(H, _ids32(ids), logits.to(torch.float32), mask,
@@ -264,6 +276,7 @@ def _distill_problem(H, E, ids, logits, mask, weights, temperature, reduction):
 
 
 def _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction):
+    _on_cuda(H)
     H2, ids2, m = _rows(H, _ids32(ids), mask)
     if offsets is None:
         if H.dim() != 3:
@@ -301,35 +314,36 @@ def _lse_rows(lse: torch.Tensor, H: torch.Tensor) -> torch.Tensor:
     return lse.contiguous()
 
 
+@_there
 def distill_forward(H, E, teacher_ids, teacher_logits, mask=None, weights=None, temperature: float = 1.0,
                     reduction: str = "mean", workspace: Optional[torch.Tensor] = None):
     """Distillation loss (0-d float64) and the rows' log-sum-exps of z / temperature (float32, H.shape[:-1]).
 
     H [T, D] or [B, N, D] and E [V, D] bf16; teacher_ids [.., K] (-1 empty) and teacher_logits [.., K]
     the teacher's top items and logits of each position; mask 1 = counts; weights a factor per position."""
-    with _on(H):
-        prob, keep = _distill_problem(H, E, teacher_ids, teacher_logits, mask, weights, temperature, reduction)
-        ws = _workspace(B.cutbce_distill_workspace_size(prob, B.OUT_LOSS), H.device, workspace)
-        loss = torch.empty((), dtype=torch.float64, device=H.device)
-        lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
-        B.cutbce_distill_forward(prob, loss, lse, ws)
+    prob, keep = _distill_problem(H, E, teacher_ids, teacher_logits, mask, weights, temperature, reduction)
+    ws = _workspace(B.cutbce_distill_workspace_size(prob, B.OUT_LOSS), H.device, workspace)
+    loss = torch.empty((), dtype=torch.float64, device=H.device)
+    lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
+    B.cutbce_distill_forward(prob, loss, lse, ws)
     return loss, lse
 
 
+@_there
 def distill_backward(H, E, teacher_ids, teacher_logits, lse, mask=None, weights=None, temperature: float = 1.0,
                      reduction: str = "mean", grad_loss=None, want_dH: bool = True, want_dE: bool = True,
                      grad_dtype: torch.dtype = torch.float32, dE_out=None, accumulate_dE: bool = False,
                      workspace: Optional[torch.Tensor] = None):
     """(dH, dE) given the lse of distill_forward on the same inputs."""
-    with _on(H):
-        prob, keep = _distill_problem(H, E, teacher_ids, teacher_logits, mask, weights, temperature, reduction)
-        dH, dE, opts = _grad_outputs(H, E, want_dH, want_dE, grad_dtype, dE_out, accumulate_dE)
-        ws = _workspace(B.cutbce_distill_workspace_size(prob, _bits(dH, dE)), H.device, workspace)
-        g = _scalar_grad(grad_loss)
-        B.cutbce_distill_backward(prob, opts, _lse_rows(lse, H), g, dH, dE, ws)
+    prob, keep = _distill_problem(H, E, teacher_ids, teacher_logits, mask, weights, temperature, reduction)
+    dH, dE, opts = _grad_outputs(H, E, want_dH, want_dE, grad_dtype, dE_out, accumulate_dE)
+    ws = _workspace(B.cutbce_distill_workspace_size(prob, _bits(dH, dE)), H.device, workspace)
+    g = _scalar_grad(grad_loss)
+    B.cutbce_distill_backward(prob, opts, _lse_rows(lse, H), g, dH, dE, ws)
     return dH, dE
 
 
+@_there
 def distill_forward_backward(H, E, teacher_ids, teacher_logits, mask=None, weights=None, temperature: float = 1.0,
                              reduction: str = "mean", grad_loss=None, want_dH: bool = True, want_dE: bool = True,
                              grad_dtype: torch.dtype = torch.float32, dE_out=None, accumulate_dE: bool = False,
@@ -337,17 +351,17 @@ def distill_forward_backward(H, E, teacher_ids, teacher_logits, mask=None, weigh
     """(loss, lse, dH, dE) in one call; None for a gradient that is not wanted.
 
     dE_out ([V, D], contiguous) is written instead of a new tensor, or added to with accumulate_dE."""
-    with _on(H):
-        prob, keep = _distill_problem(H, E, teacher_ids, teacher_logits, mask, weights, temperature, reduction)
-        dH, dE, opts = _grad_outputs(H, E, want_dH, want_dE, grad_dtype, dE_out, accumulate_dE)
-        ws = _workspace(B.cutbce_distill_workspace_size(prob, B.OUT_LOSS | _bits(dH, dE)), H.device, workspace)
-        loss = torch.empty((), dtype=torch.float64, device=H.device)
-        lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
-        g = _scalar_grad(grad_loss)
-        B.cutbce_distill_forward_backward(prob, opts, g, loss, lse, dH, dE, ws)
+    prob, keep = _distill_problem(H, E, teacher_ids, teacher_logits, mask, weights, temperature, reduction)
+    dH, dE, opts = _grad_outputs(H, E, want_dH, want_dE, grad_dtype, dE_out, accumulate_dE)
+    ws = _workspace(B.cutbce_distill_workspace_size(prob, B.OUT_LOSS | _bits(dH, dE)), H.device, workspace)
+    loss = torch.empty((), dtype=torch.float64, device=H.device)
+    lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
+    g = _scalar_grad(grad_loss)
+    B.cutbce_distill_forward_backward(prob, opts, g, loss, lse, dH, dE, ws)
     return loss, lse, dH, dE
 
 
+@_there
 def preference_forward(H, E, ids, offsets=None, ref_logp=None, mask=None, beta: float = 0.1, reduction: str = "mean",
                        workspace: Optional[torch.Tensor] = None):
     """Preference loss (0-d float64), the sequences' log-probabilities (float32 [2P]) and the rows'
@@ -357,44 +371,43 @@ def preference_forward(H, E, ids, offsets=None, ref_logp=None, mask=None, beta: 
     without; ids: the item that followed each position (-1: does not count); ref_logp [2P]: the
     sequences' log-probabilities under the reference model (the second output of this call with
     that model's H and E), or None for 0."""
-    with _on(H):
-        prob, keep = _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction)
-        ws = _workspace(B.cutbce_preference_workspace_size(prob, B.OUT_LOSS), H.device, workspace)
-        loss = torch.empty((), dtype=torch.float64, device=H.device)
-        logp = torch.empty(2 * prob.P, dtype=torch.float32, device=H.device)
-        lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
-        B.cutbce_preference_forward(prob, loss, logp, lse, ws)
+    prob, keep = _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction)
+    ws = _workspace(B.cutbce_preference_workspace_size(prob, B.OUT_LOSS), H.device, workspace)
+    loss = torch.empty((), dtype=torch.float64, device=H.device)
+    logp = torch.empty(2 * prob.P, dtype=torch.float32, device=H.device)
+    lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
+    B.cutbce_preference_forward(prob, loss, logp, lse, ws)
     return loss, logp, lse
 
 
+@_there
 def preference_backward(H, E, ids, lse, offsets=None, ref_logp=None, mask=None, beta: float = 0.1,
                         reduction: str = "mean", grad_loss=None, want_dH: bool = True, want_dE: bool = True,
                         grad_dtype: torch.dtype = torch.float32, dE_out=None, accumulate_dE: bool = False,
                         workspace: Optional[torch.Tensor] = None):
     """(dH, dE) given the lse of preference_forward on the same inputs."""
-    with _on(H):
-        prob, keep = _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction)
-        dH, dE, opts = _grad_outputs(H, E, want_dH, want_dE, grad_dtype, dE_out, accumulate_dE)
-        ws = _workspace(B.cutbce_preference_workspace_size(prob, _bits(dH, dE)), H.device, workspace)
-        g = _scalar_grad(grad_loss)
-        B.cutbce_preference_backward(prob, opts, _lse_rows(lse, H), g, dH, dE, ws)
+    prob, keep = _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction)
+    dH, dE, opts = _grad_outputs(H, E, want_dH, want_dE, grad_dtype, dE_out, accumulate_dE)
+    ws = _workspace(B.cutbce_preference_workspace_size(prob, _bits(dH, dE)), H.device, workspace)
+    g = _scalar_grad(grad_loss)
+    B.cutbce_preference_backward(prob, opts, _lse_rows(lse, H), g, dH, dE, ws)
     return dH, dE
 
 
+@_there
 def preference_forward_backward(H, E, ids, offsets=None, ref_logp=None, mask=None, beta: float = 0.1,
                                 reduction: str = "mean", grad_loss=None, want_dH: bool = True, want_dE: bool = True,
                                 grad_dtype: torch.dtype = torch.float32, dE_out=None, accumulate_dE: bool = False,
                                 workspace: Optional[torch.Tensor] = None):
     """(loss, logp, lse, dH, dE) in one call; None for a gradient that is not wanted."""
-    with _on(H):
-        prob, keep = _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction)
-        dH, dE, opts = _grad_outputs(H, E, want_dH, want_dE, grad_dtype, dE_out, accumulate_dE)
-        ws = _workspace(B.cutbce_preference_workspace_size(prob, B.OUT_LOSS | _bits(dH, dE)), H.device, workspace)
-        loss = torch.empty((), dtype=torch.float64, device=H.device)
-        logp = torch.empty(2 * prob.P, dtype=torch.float32, device=H.device)
-        lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
-        g = _scalar_grad(grad_loss)
-        B.cutbce_preference_forward_backward(prob, opts, g, loss, logp, lse, dH, dE, ws)
+    prob, keep = _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction)
+    dH, dE, opts = _grad_outputs(H, E, want_dH, want_dE, grad_dtype, dE_out, accumulate_dE)
+    ws = _workspace(B.cutbce_preference_workspace_size(prob, B.OUT_LOSS | _bits(dH, dE)), H.device, workspace)
+    loss = torch.empty((), dtype=torch.float64, device=H.device)
+    logp = torch.empty(2 * prob.P, dtype=torch.float32, device=H.device)
+    lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
+    g = _scalar_grad(grad_loss)
+    B.cutbce_preference_forward_backward(prob, opts, g, loss, logp, lse, dH, dE, ws)
     return loss, logp, lse, dH, dE
 
 

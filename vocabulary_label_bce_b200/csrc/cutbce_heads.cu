@@ -45,60 +45,85 @@ cutbce_status check_device() {
   return dev.major == 10 && dev.minor == 0 ? CUTBCE_OK : CUTBCE_ERR_UNSUPPORTED;
 }
 
+// Sets a kernel's dynamic shared memory limit once per device (the attribute belongs
+// to the current device).
+template <int kTag, typename Kernel>
+cudaError_t set_smem_once(Kernel kern, size_t bytes) {
+  static std::atomic<uint64_t> configured{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  const uint64_t bit = uint64_t(1) << dev;
+  if ((configured.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) configured.fetch_or(bit, std::memory_order_acq_rel);
+  return e;
+}
+
 // ---------------------------------------------------------------- sort and segment sums
-constexpr size_t kSideFillBytes = size_t(16) << 20;
 constexpr int64_t kMaxSortEntries = int64_t(1) << 28;
 
 // Buffers of the sort and of the sums over N entries.
 struct SortBuffers {
   SortPlan sp;
-  size_t o_hist, o_total, o_k[2], o_v[2], o_part;
+  bool cluster;
+  size_t o_hist, o_total, o_pairs[2], o_part;
 };
 
 void plan_sort(int64_t N, int64_t V, int64_t D, SortBuffers& b, Layout& l) {
   make_sort_plan(N, V, b.sp);
+  b.cluster = N <= kClusterEntries;
+  if (b.cluster) b.sp.hist_bytes = 0;
   b.o_hist = l.take(b.sp.hist_bytes);                 // right after the header: one memset clears both
-  b.o_total = l.take(sizeof(int) * (size_t(1) << b.sp.bits));
-  for (int i = 0; i < 2; ++i) {
-    b.o_k[i] = l.take(4 * static_cast<size_t>(N));
-    b.o_v[i] = l.take(4 * static_cast<size_t>(N));
-  }
+  b.o_total = l.take(b.cluster ? 0 : sizeof(int) * (size_t(1) << b.sp.bits));
+  for (int i = 0; i < 2; ++i) b.o_pairs[i] = l.take(8 * static_cast<size_t>(N));
   b.o_part = l.take(4 * 2 * static_cast<size_t>(ceil_div(N, kMinChunk)) * D);   // the most blocks of any geometry
 }
 
-// Sorts the entries by id; the sorted keys and entry indices end in *keys, *vals.
+// Sorts the entries by id into *pairs.
 template <int IPT>
-cutbce_status run_sort_ipt(const SortBuffers& b, const int32_t* ids, int V, void* ws, int* status, cudaStream_t st,
-                           const int** keys, const int** vals) {
+cutbce_status run_sort_ipt(const SortBuffers& b, const int32_t* ids, int V, void* ws, int* status, FillJob fill,
+                           cudaStream_t st, const int2** pairs) {
   const SortPlan& sp = b.sp;
   const size_t pass_hist = static_cast<size_t>(sp.nblk) << sp.bits;
   int* hist = at<int>(ws, b.o_hist);
   int* total = at<int>(ws, b.o_total);
-  k_sort_keys<IPT><<<sp.nblk, kSortThreads, 0, st>>>(ids, sp.N, V, sp.bits, hist, status);
-  const int* kin = ids;
-  const int* vin = nullptr;
+  const int fill_blocks = static_cast<int>(std::min<int64_t>(ceil_div(fill.n, 4 * kSortThreads), 8 * 148));
+  k_sort_keys<IPT><<<sp.nblk + fill_blocks, kSortThreads, 0, st>>>(ids, sp.N, V, sp.bits, hist, status, sp.nblk, fill);
+  const int2* in = nullptr;
   for (int p = 0; p < sp.passes; ++p) {
     int* h = hist + p * pass_hist;
     int* next = p + 1 < sp.passes ? h + pass_hist : nullptr;
     if (sp.scan) k_sort_scan<<<static_cast<unsigned>(ceil_div(1 << sp.bits, 128)), 128, 0, st>>>(h, total, 1 << sp.bits, sp.nblk);
-    int* ko = at<int>(ws, b.o_k[p & 1]);
-    int* vo = at<int>(ws, b.o_v[p & 1]);
-    k_sort_scatter<IPT><<<sp.nblk, kSortThreads, 0, st>>>(kin, vin, sp.N, V, p * sp.bits, sp.bits, sp.nblk, h,
-                                                          sp.scan ? total : nullptr, ko, vo, next, status);
-    kin = ko;
-    vin = vo;
+    int2* out = at<int2>(ws, b.o_pairs[p & 1]);
+    k_sort_scatter<IPT><<<sp.nblk, kSortThreads, 0, st>>>(p == 0 ? ids : nullptr, in, sp.N, V, p * sp.bits, sp.bits, sp.nblk,
+                                                          h, sp.scan ? total : nullptr, out, next, status);
+    in = out;
   }
-  *keys = kin;
-  *vals = vin;
+  *pairs = in;
   return cudaGetLastError() == cudaSuccess ? CUTBCE_OK : CUTBCE_ERR_CUDA;
 }
 
-cutbce_status run_sort(const SortBuffers& b, const int32_t* ids, int V, void* ws, int* status, cudaStream_t st,
-                       const int** keys, const int** vals) {
+// clear_status: the status word is not yet cleared (one-kernel sort only: the others
+// follow a memset of the header and the histograms).
+cutbce_status run_sort(const SortBuffers& b, const int32_t* ids, int V, void* ws, int* status, bool clear_status,
+                       FillJob fill, cudaStream_t st, const int2** pairs) {
   LaunchScope ls(CUTBCE_KERNEL_ID_SORT, st);
-  if (b.sp.ipt == 4) return run_sort_ipt<4>(b, ids, V, ws, status, st, keys, vals);
-  if (b.sp.ipt == 16) return run_sort_ipt<16>(b, ids, V, ws, status, st, keys, vals);
-  return run_sort_ipt<64>(b, ids, V, ws, status, st, keys, vals);
+  if (b.cluster) {
+    const size_t smem = size_t(64) << b.sp.bits;           // a 16-bit counter per warp and digit
+    const cudaError_t e = set_smem_once<0>(k_sort_cluster, size_t(64) << kSortMaxBits);
+    if (e != cudaSuccess) return CUTBCE_ERR_CUDA;
+    const int fill_clusters = static_cast<int>(std::min<int64_t>(ceil_div(fill.n, 2 * kClusterCtas * kClusterThreads), 18));
+    k_sort_cluster<<<kClusterCtas * (1 + fill_clusters), kClusterThreads, smem, st>>>(ids, static_cast<int>(b.sp.N), V, b.sp.bits, b.sp.passes,
+                                                                at<int2>(ws, b.o_pairs[0]), at<int2>(ws, b.o_pairs[1]),
+                                                                status, clear_status ? 1 : 0, fill);
+    *pairs = at<int2>(ws, b.o_pairs[(b.sp.passes - 1) & 1]);
+    return cudaGetLastError() == cudaSuccess ? CUTBCE_OK : CUTBCE_ERR_CUDA;
+  }
+  if (b.sp.ipt == 4) return run_sort_ipt<4>(b, ids, V, ws, status, fill, st, pairs);
+  if (b.sp.ipt == 16) return run_sort_ipt<16>(b, ids, V, ws, status, fill, st, pairs);
+  return run_sort_ipt<64>(b, ids, V, ws, status, fill, st, pairs);
 }
 
 template <int VEC, typename TIn, typename TOut>
@@ -283,17 +308,8 @@ cudaError_t launch_softmax(int grid, const CUtensorMap& s, const CUtensorMap& x,
                            const SoftmaxParams& sp, cudaStream_t st) {
   auto kern = k_softmax<DP, kPass>;
   constexpr uint32_t smem = SoftmaxCfg<DP, kPass>::SMEM_BYTES;
-  static std::atomic<uint64_t> configured{0};   // the attribute belongs to the current device
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = set_smem_once<DP + kPass>(kern, smem);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  const uint64_t bit = uint64_t(1) << dev;
-  if ((configured.load(std::memory_order_acquire) & bit) == 0) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    configured.fetch_or(bit, std::memory_order_acq_rel);
-  }
   kern<<<grid, SoftmaxCfg<DP, kPass>::THREADS, smem, st>>>(s, x, o, sp);
   return cudaGetLastError();
 }
@@ -341,9 +357,9 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   HeadPlan pl;
   plan_head(p, dH, dE, lse_in == nullptr, pl);
   if (ws_bytes < pl.total) return CUTBCE_ERR_WORKSPACE;
-  if ((s = check_device()) != CUTBCE_OK) return s;
   DeviceFacts dev;
   if ((s = device_facts(dev)) != CUTBCE_OK) return s;
+  if (!(dev.major == 10 && dev.minor == 0)) return CUTBCE_ERR_UNSUPPORTED;
 
   HeadParams hp{};
   hp.kind = p.kind;
@@ -399,10 +415,12 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   hp.logp_out = out.logp;
   int* status = &hp.hdr->w.status;
 
-  CUTBCE_CK(cudaMemsetAsync(hp.hdr, 0, pl.clear_bytes, st));
+  const bool one_block = p.T <= kOneBlockRows && pl.clear_bytes <= 256;
+  if (!one_block) CUTBCE_CK(cudaMemsetAsync(hp.hdr, 0, pl.clear_bytes, st));
   {
     LaunchScope ls(CUTBCE_KERNEL_HEAD_PREP, st);
-    k_head_rows<<<static_cast<unsigned>(pl.n_blk), 256, 0, st>>>(hp);
+    if (one_block) k_head_rows_one<<<1, kOneBlockRows, 0, st>>>(hp);
+    else k_head_rows<<<static_cast<unsigned>(pl.n_blk), 256, 0, st>>>(hp);
     if (pl.fused)
       k_head_norm<<<static_cast<unsigned>(std::min<int64_t>(ceil_div(p.V, 128), 8 * 148)), 256, 0, st>>>(hp.E, p.V, hp.D,
                                                                                                        hp.hdr);
@@ -490,7 +508,7 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   if (dE) {
     // the sparse part of dE: sum of coef q h over the pairs of each item, in fp32
     SegmentParams gp{};
-    if ((s = run_sort(pl.sort, hp.keys, hp.V, ws, status, st, &gp.keys, &gp.vals)) != CUTBCE_OK) return s;
+    if ((s = run_sort(pl.sort, hp.keys, hp.V, ws, status, false, FillJob{}, st, &gp.pairs)) != CUTBCE_OK) return s;
     gp.N = p.T * p.K;
     gp.V = hp.V;
     gp.D = hp.D;
@@ -583,25 +601,14 @@ cutbce_status cutbce_embed_backward(const void* dX, int32_t dtype, const int32_t
   if ((s = check_device()) != CUTBCE_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int* status = at<int>(ws, pl.o_hdr);
-  CUTBCE_CK(cudaMemsetAsync(status, 0, pl.sort.o_hist + pl.sort.sp.hist_bytes, st));
-  // a large dE is cleared on a second stream while the entries are sorted
+  if (!pl.sort.cluster) CUTBCE_CK(cudaMemsetAsync(status, 0, pl.sort.o_hist + pl.sort.sp.hist_bytes, st));
+  // dE starts at zero: by blocks beside the sort, or ahead of it where its ends are not 16-byte aligned
   const size_t de_bytes = eo * static_cast<size_t>(V) * D;
-  SideStreamLease side;
-  if (!accumulate) {
-    cudaStream_t fill = st;
-    if (de_bytes >= kSideFillBytes) {
-      if ((s = take_side_stream(side.s)) != CUTBCE_OK) return s;
-      side.held = true;
-      CUTBCE_CK(cudaEventRecord(side.s.ev, st));
-      CUTBCE_CK(cudaStreamWaitEvent(side.s.s, side.s.ev, 0));
-      fill = side.s.s;
-    }
-    CUTBCE_CK(cudaMemsetAsync(dE, 0, de_bytes, fill));
-    if (side.held) CUTBCE_CK(cudaEventRecord(side.s.ev2, side.s.s));
-  }
+  FillJob fill{};
+  if (!accumulate && aligned(dE, 16) && de_bytes % 16 == 0) fill = FillJob{static_cast<uint4*>(dE), static_cast<int64_t>(de_bytes / 16)};
+  else if (!accumulate) CUTBCE_CK(cudaMemsetAsync(dE, 0, de_bytes, st));
   SegmentParams p{};
-  s = run_sort(pl.sort, ids, static_cast<int>(V), ws, status, st, &p.keys, &p.vals);
-  if (side.held) CUTBCE_CK(cudaStreamWaitEvent(st, side.s.ev2, 0));   // joined on every path
+  s = run_sort(pl.sort, ids, static_cast<int>(V), ws, status, true, fill, st, &p.pairs);
   if (s != CUTBCE_OK) return s;
   p.N = N;
   p.V = static_cast<int>(V);

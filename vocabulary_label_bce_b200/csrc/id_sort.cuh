@@ -2,8 +2,8 @@
 // by id: the table's gradient from its sparse side (lookup gradient, and the
 // target part of the softmax losses).
 //
-// Sort: LSD over at most 11 bits a pass, so V up to 2048 takes one pass and V up
-// to 4 M two.  A block owns a tile of consecutive entries; each warp ranks a
+// Sort: LSD over at most 11 bits a pass, so V up to 2047 takes one pass and V up
+// to 4 M two.  Up to 16,384 entries it is one kernel (k_sort_cluster); beyond, a block owns a tile of consecutive entries; each warp ranks a
 // contiguous part of it with match_any and 16-bit counters in shared memory, so
 // equal ids keep entry order.  Every scatter block forms its own offsets from the
 // tile histograms (they sit in L2), and the scatter of one pass counts the
@@ -52,12 +52,27 @@ inline void make_sort_plan(int64_t N, int64_t V, SortPlan& s) {
   s.hist_bytes = sizeof(int) * static_cast<size_t>(s.passes) * s.nblk * (size_t(1) << s.bits);
 }
 
+// Zeros for a dense gradient's rows, written by blocks of their own beside a sort
+// kernel that leaves most SMs idle: `n` pieces of 16 bytes.
+struct FillJob {
+  uint4* dst;
+  int64_t n;                // 0: nothing to fill
+};
+__device__ __forceinline__ void fill_zeros(const FillJob& f, int64_t block, int64_t blocks) {
+  for (int64_t i = block * blockDim.x + threadIdx.x; i < f.n; i += blocks * blockDim.x) f.dst[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 // Keys from plain ids (lookup gradient): -1 is an empty entry, any other id outside
-// [0, V) sets the status.  Counts the first pass's histogram.
+// [0, V) sets the status.  Counts the first pass's histogram.  Blocks from nblk on fill.
 template <int IPT>
 __global__ void __launch_bounds__(kSortThreads) k_sort_keys(const int32_t* __restrict__ ids, int64_t N, int V,
-                                                            int bits, int* __restrict__ hist, int* status) {
+                                                            int bits, int* __restrict__ hist, int* status, int nblk,
+                                                            FillJob fill) {
   __shared__ int h[kSortMaxBins];
+  if (static_cast<int>(blockIdx.x) >= nblk) {
+    fill_zeros(fill, static_cast<int>(blockIdx.x) - nblk, static_cast<int>(gridDim.x) - nblk);
+    return;
+  }
   const int bins = 1 << bits;
   for (int d = threadIdx.x; d < bins; d += kSortThreads) h[d] = 0;
   __syncthreads();
@@ -101,17 +116,17 @@ __global__ void __launch_bounds__(128) k_sort_scan(int* __restrict__ hist, int* 
   total[d] = run;
 }
 
-// One pass.  keys_in: ids (empty and out-of-range ones count as V); vals_in null
-// means the entry's own index.  hist_next (null in the last pass): the next
+// One pass over (id, entry index) pairs.  ids (first pass, else null): the plain ids,
+// empty and out-of-range ones counting as V, the index being the entry's own.
+// hist_next (null in the last pass): the next
 // pass's histogram, cleared before the call.
 template <int IPT>
-__global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const int* __restrict__ keys_in,
-                                                               const int* __restrict__ vals_in, int64_t N, int V,
+__global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const int* __restrict__ ids,
+                                                               const int2* __restrict__ in, int64_t N, int V,
                                                                int shift, int bits, int nblk,
                                                                const int* __restrict__ hist,
                                                                const int* __restrict__ digit_total,
-                                                               int* __restrict__ keys_out,
-                                                               int* __restrict__ vals_out, int* __restrict__ hist_next,
+                                                               int2* __restrict__ out, int* __restrict__ hist_next,
                                                                const int* __restrict__ status) {
   __shared__ uint16_t cnt[kSortWarps][kSortMaxBins];
   __shared__ int off[kSortMaxBins];
@@ -178,30 +193,40 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const int* __rest
   const int64_t wbase = static_cast<int64_t>(blockIdx.x) * kSortThreads * IPT + static_cast<int64_t>(warp) * 32 * IPT;
   const unsigned lt = (1u << lane) - 1u;
   constexpr int KEEP = IPT <= 16 ? IPT : 1;       // ranks kept in registers, or formed again below
-  int key[KEEP], rank[KEEP];
-  auto load_key = [&](int64_t i) {
-    const int k = keys_in[i];
-    return (k < 0 || k > V) ? V : k;
+  int2 key[KEEP];
+  int rank[KEEP];
+  auto load_pair = [&](int64_t i) {
+    if (ids == nullptr) return in[i];
+    const int k = ids[i];
+    return make_int2((k < 0 || k > V) ? V : k, static_cast<int>(i));
   };
-  auto count_round = [&](int r, int& k, int& rk) {
+  if constexpr (KEEP == IPT) {
+#pragma unroll
+    for (int r = 0; r < IPT; ++r) {
+      const int64_t i = wbase + r * 32 + lane;
+      key[r] = i < N ? load_pair(i) : make_int2(0, 0);
+    }
+  }
+  auto count_round = [&](int r, int2& k, int& rk) {
     const int64_t i = wbase + r * 32 + lane;
-    const bool in = i < N;
-    k = in ? load_key(i) : 0;
-    const int d = in ? (k >> shift) & (bins - 1) : bins;
+    const bool live = i < N;
+    if constexpr (KEEP != IPT) k = live ? load_pair(i) : make_int2(0, 0);
+    const int d = live ? (k.x >> shift) & (bins - 1) : bins;
     const unsigned peers = __match_any_sync(0xffffffffu, d);
-    const int old = in ? cnt[warp][d] : 0;
+    const int old = live ? cnt[warp][d] : 0;
     rk = old + __popc(peers & lt);
     __syncwarp();
-    if (in && (peers & lt) == 0) cnt[warp][d] = static_cast<uint16_t>(old + __popc(peers));
+    if (live && (peers & lt) == 0) cnt[warp][d] = static_cast<uint16_t>(old + __popc(peers));
     __syncwarp();
   };
 #pragma unroll
   for (int r = 0; r < IPT; ++r) {
-    int k, rk;
-    count_round(r, k, rk);
     if constexpr (KEEP == IPT) {
-      key[r] = k;
-      rank[r] = rk;
+      count_round(r, key[r], rank[r]);
+    } else {
+      int2 k;
+      int rk;
+      count_round(r, k, rk);
     }
   }
   __syncthreads();
@@ -217,32 +242,165 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const int* __rest
   }
   __syncthreads();
   if (failed != 0) return;
-  auto put = [&](int r, int k, int rk) {
+  auto put = [&](int r, int2 k, int rk) {
     const int64_t i = wbase + r * 32 + lane;
     if (i >= N) return;
-    const int pos = off[(k >> shift) & (bins - 1)] + rk;
-    keys_out[pos] = k;
-    vals_out[pos] = vals_in != nullptr ? vals_in[i] : static_cast<int>(i);
+    const int pos = off[(k.x >> shift) & (bins - 1)] + rk;
+    out[pos] = k;
     if (hist_next != nullptr)
-      atomicAdd(hist_next + static_cast<int64_t>(pos / (kSortThreads * IPT)) * bins + ((k >> (shift + bits)) & (bins - 1)), 1);
+      atomicAdd(hist_next + static_cast<int64_t>(pos / (kSortThreads * IPT)) * bins + ((k.x >> (shift + bits)) & (bins - 1)), 1);
   };
 #pragma unroll
   for (int r = 0; r < IPT; ++r) {
     if constexpr (KEEP == IPT) {
-      put(r, key[r], rank[r] + cnt[warp][(key[r] >> shift) & (bins - 1)]);
+      put(r, key[r], rank[r] + cnt[warp][(key[r].x >> shift) & (bins - 1)]);
     } else {
       // the counters now hold each warp's start: counting again gives start + rank
-      int k, rk;
+      int2 k;
+      int rk;
       count_round(r, k, rk);
       put(r, k, rk);
     }
   }
 }
 
+// The whole sort in one kernel, for up to 16,384 entries: a cluster of
+// eight CTAs, whose warps own consecutive entries (held in registers over a pass).
+// The CTAs read each other's digit totals from shared memory; the pairs of a pass go
+// through L2.  No launch, histogram or clearing between the passes: 12,800 entries
+// of 20-bit ids take 9 us against 20 us for the kernels above.  ids as there;
+// `clear_status`: the status starts here, and bad ids set it.  Clusters past the
+// first fill.
+constexpr int kClusterCtas = 8;
+constexpr int kClusterThreads = 1024;
+constexpr int kClusterRounds = 2;                       // entries per thread: 16,384 in all
+constexpr int64_t kClusterEntries = 16384;
+
+__device__ __forceinline__ int ld_cluster_shared(const int* local, uint32_t rank) {
+  uint32_t addr;
+  int v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterThreads)
+    k_sort_cluster(const int* __restrict__ ids, int N, int V, int bits, int passes, int2* buf0, int2* buf1, int* status,
+                   int clear_status, FillJob fill) {
+  if (blockIdx.x >= kClusterCtas) {                         // clusters past the first
+    fill_zeros(fill, static_cast<int>(blockIdx.x) - kClusterCtas, static_cast<int>(gridDim.x) - kClusterCtas);
+    return;
+  }
+  extern __shared__ uint16_t s_cnt[];                       // [32 warps][bins]
+  __shared__ int tot[kSortMaxBins], off[kSortMaxBins];
+  __shared__ int wsum[32];
+  const int bins = 1 << bits, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = cluster_ctarank();
+  uint16_t* cnt = s_cnt + warp * bins;
+  const unsigned lt = (1u << lane) - 1u;
+  const int per = (N + kClusterCtas * 1024 - 1) / (kClusterCtas * 1024);   // rounds of 32 entries a warp
+  const int base = (static_cast<int>(rank) * 32 + warp) * per * 32;
+  if (clear_status) {
+    if (rank == 0 && tid == 0) *status = 0;
+    cluster_sync_all();
+  }
+  for (int p = 0; p < passes; ++p) {
+    const int shift = p * bits;
+    const int2* in = (p & 1) ? buf0 : buf1;                 // pass p writes buf0 for even p
+    int2* out = (p & 1) ? buf1 : buf0;
+    int2 key[kClusterRounds];
+    int rk[kClusterRounds];
+    for (int i = tid; i < 4 * bins; i += kClusterThreads) reinterpret_cast<uint4*>(s_cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int r = 0; r < kClusterRounds; ++r) {
+      const int i = base + r * 32 + lane;
+      key[r] = make_int2(V, 0);
+      if (r < per && i < N) {
+        if (p == 0) {
+          const int id = __ldg(ids + i);
+          const bool real = id >= 0 && id < V;
+          if (!real && id != -1) atomicCAS(status, 0, kErrTargetRange);
+          key[r] = make_int2(real ? id : V, i);
+        } else {
+          key[r] = __ldcg(in + i);
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kClusterRounds; ++r) {
+      if (r >= per) break;
+      const bool live = base + r * 32 + lane < N;
+      const int d = live ? (key[r].x >> shift) & (bins - 1) : bins;
+      const unsigned peers = __match_any_sync(0xffffffffu, d);
+      const int old = live ? cnt[d] : 0;
+      rk[r] = old + __popc(peers & lt);
+      __syncwarp();
+      if (live && (peers & lt) == 0) cnt[d] = static_cast<uint16_t>(old + __popc(peers));
+      __syncwarp();
+    }
+    __syncthreads();
+    // this CTA's totals, and each warp's start within them
+    for (int d = tid; d < bins; d += kClusterThreads) {
+      int run = 0;
+#pragma unroll
+      for (int w = 0; w < 32; ++w) {
+        const int c = s_cnt[w * bins + d];
+        s_cnt[w * bins + d] = static_cast<uint16_t>(run);
+        run += c;
+      }
+      tot[d] = run;
+    }
+    cluster_sync_all();
+    // offsets: smaller digits in the whole cluster, then this digit in earlier CTAs
+    int carry = 0;
+    for (int d0 = 0; d0 < bins; d0 += kClusterThreads) {
+      const int d = d0 + tid;
+      int before = 0, total = 0;
+      if (d < bins) {
+#pragma unroll
+        for (uint32_t c = 0; c < kClusterCtas; ++c) {
+          const int v = ld_cluster_shared(tot + d, c);
+          total += v;
+          if (c < rank) before += v;
+        }
+      }
+      int inc = total;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (lane == 31) wsum[warp] = inc;
+      __syncthreads();
+      if (warp == 0) {
+        int s = wsum[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, s, o);
+          if (lane >= o) s += v;
+        }
+        wsum[lane] = s;
+      }
+      __syncthreads();
+      if (d < bins) off[d] = carry + (warp > 0 ? wsum[warp - 1] : 0) + inc - total + before;
+      carry += wsum[31];
+      __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < kClusterRounds; ++r) {
+      if (r >= per || base + r * 32 + lane >= N) break;
+      const int d = (key[r].x >> shift) & (bins - 1);
+      out[off[d] + cnt[d] + rk[r]] = key[r];
+    }
+    // the pairs are visible to the cluster, and no CTA still reads another's totals
+    cluster_sync_all();
+  }
+}
+
 // ------------------------------------------------------------------ segment sums
 struct SegmentParams {
-  const int* keys;            // sorted ids (V: no row)
-  const int* vals;            // entry indices, ascending within an id
+  const int2* pairs;          // sorted (id, entry index): id V has no row; indices ascend within an id
   int64_t N;
   int V, D;
   const void* src;            // [rows, D] rows to add; entry p reads row p / K
@@ -322,7 +480,7 @@ struct RowPiece<1, T> {
 // Geometry for rows of D elements in pieces of VEC: `lanes` threads a row (wide
 // rows in `slices`), `subs` rows side by side in a block, each sub-chunk summing
 // kSumBatch * rounds consecutive entries.
-constexpr int kSumBatch = 8;                // rows in flight per thread
+constexpr int kSumBatch = 4;                // rows in flight per thread
 constexpr int kMinChunk = 4 * kSumBatch;    // fewest entries of a block
 struct SumGeometry {
   int lanes, slices, subs, rounds;
@@ -335,8 +493,9 @@ inline SumGeometry sum_geometry(int64_t N, int64_t D, int vec) {
   g.lanes = static_cast<int>(ceil_div(pieces, g.slices));
   g.subs = 256 / g.lanes;
   if (g.subs > 64) g.subs = 64;
-  // one round while that keeps the blocks below about four an SM, then more
-  int64_t r = N / (static_cast<int64_t>(g.subs) * kSumBatch * 592);
+  // rounds so that about eight blocks an SM remain: fewer leave SMs idle at the end (626
+  // blocks in waves of 592: a third lost), more leave more partials to join
+  int64_t r = N / (static_cast<int64_t>(g.subs) * kSumBatch * 1184);
   g.rounds = static_cast<int>(r < 1 ? 1 : r > 16 ? 16 : r);
   g.chunk = static_cast<int64_t>(g.subs) * kSumBatch * g.rounds;
   g.chunks = ceil_div(N, g.chunk);
@@ -347,7 +506,7 @@ inline SumGeometry sum_geometry(int64_t N, int64_t D, int vec) {
 // and leaves its first (continued) and last (continuing) ones in shared memory; the
 // lanes of sub-chunk 0 then walk the sub-chunks in order.
 template <int VEC, typename TIn, typename TOut>
-__global__ void __launch_bounds__(256) k_segment_sum(const SegmentParams p, int lanes, int subs, int rounds) {
+__global__ void __launch_bounds__(256, VEC == 8 ? 3 : 4) k_segment_sum(const SegmentParams p, int lanes, int subs, int rounds) {
   __shared__ float s_first[256 * VEC], s_last[256 * VEC];
   __shared__ int s_kind[64], s_key[64], s_start[64];     // 1: first closes, 2: first goes through, 4: last is open
   if (*p.status != 0) return;
@@ -361,9 +520,9 @@ __global__ void __launch_bounds__(256) k_segment_sum(const SegmentParams p, int 
   const TIn* src = static_cast<const TIn*>(p.src) + col;
   if (sub < subs) {
     int kind = 0;
-    int cur = i0 < i1 ? __ldg(p.keys + i0) : p.V;
-    bool open_left = i0 > 0 && i0 < i1 && __ldg(p.keys + i0 - 1) == cur;
-    const int after = i1 < p.N && i0 < i1 ? __ldg(p.keys + i1) : -1;
+    int cur = i0 < i1 ? __ldg(&p.pairs[i0].x) : p.V;
+    bool open_left = i0 > 0 && i0 < i1 && __ldg(&p.pairs[i0 - 1].x) == cur;
+    const int after = i1 < p.N && i0 < i1 ? __ldg(&p.pairs[i1].x) : -1;
     int start = static_cast<int>(i0);
     float acc[VEC];
 #pragma unroll
@@ -390,8 +549,9 @@ __global__ void __launch_bounds__(256) k_segment_sum(const SegmentParams p, int 
 #pragma unroll
       for (int u = 0; u < kSumBatch; ++u) {
         const int64_t at = min(i + u, p.N - 1);
-        id[u] = __ldg(p.keys + at);
-        e[u] = __ldg(p.vals + at);
+        const int2 pair = __ldg(p.pairs + at);
+        id[u] = pair.x;
+        e[u] = pair.y;
       }
     };
     if (i0 < i1) load_entries(i0);
@@ -475,15 +635,15 @@ __global__ void __launch_bounds__(256) k_segment_join(const SegmentParams p, int
   if (*p.status != 0) return;
   const int64_t c0 = blockIdx.x, b0 = c0 * chunk_entries, end = b0 + chunk_entries;
   if (end >= p.N) return;
-  const int id = __ldg(p.keys + end - 1);
-  const bool goes_on = __ldg(p.keys + end) == id;
-  const bool middle = b0 > 0 && __ldg(p.keys + b0) == id && __ldg(p.keys + b0 - 1) == id;
+  const int id = __ldg(&p.pairs[end - 1].x);
+  const bool goes_on = __ldg(&p.pairs[end].x) == id;
+  const bool middle = b0 > 0 && __ldg(&p.pairs[b0].x) == id && __ldg(&p.pairs[b0 - 1].x) == id;
   if (id >= p.V || !goes_on || middle) return;          // nothing continues, or this chunk is not the segment's first
   // the last chunk it reaches: chunks whose first entry has the id, 256 at a time
   int64_t c1 = c0;
   while (true) {
     const int64_t at = (c1 + 1 + threadIdx.x) * chunk_entries;
-    const int hit = __syncthreads_count(at < p.N && __ldg(p.keys + min(at, p.N - 1)) == id);
+    const int hit = __syncthreads_count(at < p.N && __ldg(&p.pairs[min(at, p.N - 1)].x) == id);
     c1 += hit;
     if (hit < 256) break;
   }
@@ -491,7 +651,7 @@ __global__ void __launch_bounds__(256) k_segment_join(const SegmentParams p, int
   int64_t start = b0;
   if (p.first != nullptr) {
     int below = 0;
-    for (int64_t i = b0 + threadIdx.x; i < end; i += 256) below += __ldg(p.keys + i) < id;
+    for (int64_t i = b0 + threadIdx.x; i < end; i += 256) below += __ldg(&p.pairs[i].x) < id;
     __shared__ int s_below;
     if (threadIdx.x == 0) s_below = 0;
     __syncthreads();

@@ -103,28 +103,22 @@ __device__ __forceinline__ void write_offset(const HeadParams& p, int64_t c, flo
 }
 
 // ------------------------------------------------------------------ rows
-__global__ void __launch_bounds__(256) k_head_rows(const HeadParams p) {
-  __shared__ int cnt[2];
-  __shared__ int last;
-  __shared__ int tot[2][256];
-  HeadHeader* hdr = p.hdr;
-  const int tid = threadIdx.x;
-  const int t = blockIdx.x * 256 + tid;
-  if (tid < 2) cnt[tid] = 0;
-  __syncthreads();
+// The class of position t (0: it does not count); `bad` if its ids are out of range.
+__device__ __forceinline__ int row_class(const HeadParams& p, int t, bool& bad) {
   int cls = 0;
-  bool bad = false;
   if (t < p.T && (p.mask == nullptr || p.mask[t] != 0)) {
     if (p.kind == kHeadDistill) {
       const float w = p.weights != nullptr ? p.weights[t] : 1.f;
       if (w != 0.f) {
         const int64_t r = static_cast<int64_t>(t) * p.K;
         bool any = false;
+#pragma unroll 4
         for (int k = 0; k < p.K; ++k) {
           const int id = __ldg(p.ids + r + k);
+          const float l = __ldg(p.logits + r + k);
           if (id == -1) continue;
           if (id < 0 || id >= p.V) bad = true;
-          any |= !(__ldg(p.logits + r + k) == -INFINITY);
+          any |= !(l == -INFINITY);
         }
         if (any) cls = w < 0.f ? 2 : 1;
       }
@@ -143,12 +137,51 @@ __global__ void __launch_bounds__(256) k_head_rows(const HeadParams p) {
       }
     }
   }
-  if (p.kind == kHeadPreference) {
-    for (int64_t i = t; i <= 2 * static_cast<int64_t>(p.P); i += static_cast<int64_t>(gridDim.x) * 256) {
-      const int o = p.offsets[i];
-      if (o < 0 || o > p.T || (i > 0 && p.offsets[i - 1] > o)) bad = true;
-    }
+  return cls;
+}
+
+// The header from the rows of each class.
+__device__ __forceinline__ void write_counts(const HeadParams& p, int np, int nn) {
+  HeadHeader* hdr = p.hdr;
+  const int neg0 = (np + kTileM - 1) / kTileM * kTileM;
+  hdr->n_pos = np;
+  hdr->n_neg = nn;
+  hdr->neg0 = neg0;
+  hdr->n_rows = neg0 + (nn + kTileM - 1) / kTileM * kTileM;
+  hdr->w.n_valid = np + nn;
+  double s = 1.0;
+  if (p.reduction == kMeanValidPositions) {
+    const int n = p.kind == kHeadDistill ? np + nn : p.P;
+    s = n > 0 ? 1.0 / n : 0.0;
   }
+  const double g = p.grad_loss != nullptr ? static_cast<double>(*p.grad_loss) : 1.0;
+  hdr->w.loss_scale = s;
+  hdr->w.grad_scale = static_cast<float>(g * s * (p.kind == kHeadDistill ? p.tau : p.beta));
+}
+
+
+// Preference offsets ascend within [0, T]; thread i of n looks at every n-th from i on.
+__device__ __forceinline__ bool bad_offsets(const HeadParams& p, int i0, int n) {
+  bool bad = false;
+  if (p.kind != kHeadPreference) return bad;
+  for (int64_t i = i0; i <= 2 * static_cast<int64_t>(p.P); i += n) {
+    const int o = p.offsets[i];
+    if (o < 0 || o > p.T || (i > 0 && p.offsets[i - 1] > o)) bad = true;
+  }
+  return bad;
+}
+
+__global__ void __launch_bounds__(256) k_head_rows(const HeadParams p) {
+  __shared__ int cnt[2];
+  __shared__ int last;
+  __shared__ int tot[2][256];
+  HeadHeader* hdr = p.hdr;
+  const int tid = threadIdx.x;
+  const int t = blockIdx.x * 256 + tid;
+  if (tid < 2) cnt[tid] = 0;
+  __syncthreads();
+  bool bad = bad_offsets(p, t, gridDim.x * 256);
+  const int cls = row_class(p, t, bad);
   if (bad) atomicCAS(&hdr->w.status, 0, kErrTargetRange);
   if (t < p.T) p.cls[t] = static_cast<uint8_t>(cls);
   const unsigned b1 = __ballot_sync(0xffffffffu, cls == 1), b2 = __ballot_sync(0xffffffffu, cls == 2);
@@ -192,22 +225,38 @@ __global__ void __launch_bounds__(256) k_head_rows(const HeadParams p) {
     r0 += c0;
     r1 += c1;
   }
-  if (tid == 0) {
-    const int np = tot[0][255], nn = tot[1][255];
-    const int neg0 = (np + kTileM - 1) / kTileM * kTileM;
-    hdr->n_pos = np;
-    hdr->n_neg = nn;
-    hdr->neg0 = neg0;
-    hdr->n_rows = neg0 + (nn + kTileM - 1) / kTileM * kTileM;
-    hdr->w.n_valid = np + nn;
-    double s = 1.0;
-    if (p.reduction == kMeanValidPositions) {
-      const int n = p.kind == kHeadDistill ? np + nn : p.P;
-      s = n > 0 ? 1.0 / n : 0.0;
+  if (tid == 0) write_counts(p, tot[0][255], tot[1][255]);
+}
+
+// The same for up to kOneBlockRows positions in one block, which also clears the
+// header: a short call needs no memset.
+constexpr int kOneBlockRows = 1024;
+
+__global__ void __launch_bounds__(kOneBlockRows) k_head_rows_one(const HeadParams p) {
+  __shared__ int cnt[8];                          // [256-row block][class]
+  const int t = threadIdx.x;
+  if (t < static_cast<int>(sizeof(HeadHeader) / 4)) reinterpret_cast<int*>(p.hdr)[t] = 0;
+  if (t < 8) cnt[t] = 0;
+  __syncthreads();
+  bool bad = bad_offsets(p, t, kOneBlockRows);
+  const int cls = row_class(p, t, bad);
+  if (bad) atomicCAS(&p.hdr->w.status, 0, kErrTargetRange);
+  if (t < p.T) p.cls[t] = static_cast<uint8_t>(cls);
+  const unsigned pos = __ballot_sync(0xffffffffu, cls == 1), neg = __ballot_sync(0xffffffffu, cls == 2);
+  if ((t & 31) == 0) {
+    atomicAdd(&cnt[2 * (t >> 8)], __popc(pos));
+    atomicAdd(&cnt[2 * (t >> 8) + 1], __popc(neg));
+  }
+  __syncthreads();
+  if (t == 0) {
+    int np = 0, nn = 0;
+    for (int b = 0; b < p.n_blk; ++b) {
+      p.blk[2 * b] = np;
+      p.blk[2 * b + 1] = nn;
+      np += cnt[2 * b];
+      nn += cnt[2 * b + 1];
     }
-    const double g = p.grad_loss != nullptr ? static_cast<double>(*p.grad_loss) : 1.0;
-    hdr->w.loss_scale = s;
-    hdr->w.grad_scale = static_cast<float>(g * s * (p.kind == kHeadDistill ? p.tau : p.beta));
+    write_counts(p, np, nn);
   }
 }
 
