@@ -161,6 +161,19 @@ def test_distill_large_problem_takes_the_row_sums():
     assert torch.allclose(a[2], b[2], rtol=0, atol=4e-5)
 
 
+# from 8e6 logits on the dH pass takes the row sums itself, with a bound as reference
+FUSED = [dict(T=520, V=16001, D=64, K=8), dict(T=520, V=16001, D=64, K=8, mask="random", weights="mixed"),
+         dict(T=700, V=15003, D=72, K=5, mask="random"), dict(T=640, V=15000, D=200, K=3, weights="negative"),
+         dict(T=600, V=16100, D=256, K=4, mask="random", weights="mixed")]
+
+
+@pytest.mark.parametrize("h", [1.0, 30.0])
+@pytest.mark.parametrize("case", FUSED, ids=lambda c: "_".join(f"{k}{v}" for k, v in c.items()))
+def test_distill_with_row_sums_in_the_dh_pass(case, h):
+    # h = 30: the bound lies more than 70 (log2) above the logits, so the log-sum-exp pass runs first
+    check_distill(draw_distill(seed=33, h=h, **case), tau=1.2)
+
+
 @pytest.mark.parametrize("how", ["masked", "zero weight", "empty slots", "infinite logits"])
 def test_distill_nothing_counts(how):
     c = list(draw_distill(T=70, V=300, D=64, K=3, seed=9, holes=False))
@@ -281,6 +294,18 @@ def test_preference_options(beta, reduction, g, bits, with_ref):
 def test_preference_large_logits():
     check_preference(draw_preference([70, 60], V=9000, D=64, seed=14, h=30.0), beta=0.01)
     check_preference(draw_preference([70, 60], V=9000, D=256, seed=15, h=12.0), beta=0.01, entry="split")
+
+
+@pytest.mark.parametrize("D,h", [(64, 1.0), (64, 30.0), (136, 1.0), (256, 12.0)])
+def test_preference_with_row_sums_in_the_dh_pass(D, h):
+    check_preference(draw_preference([150, 130, 0, 100, 120, 97], V=16001, D=D, seed=34, h=h, mask=True), beta=0.02)
+
+
+def test_nothing_counts_in_a_large_problem():
+    c = list(draw_distill(T=530, V=16000, D=64, K=2, seed=35, holes=False))
+    c[6] = np.zeros(530, np.uint8)
+    ref, loss, lse, dH, dE = check_distill(tuple(c))
+    assert float(loss) == 0 and not dE.any() and not dH.any()
 
 
 def test_preference_far_apart_pairs():

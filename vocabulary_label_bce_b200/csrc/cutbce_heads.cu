@@ -241,16 +241,18 @@ struct HeadPlan {
   int BN_lse, n_vtiles_lse, S_lse, tps_lse;   // the log-sum-exp pass's tiles and splits
   bool fused;                    // the dH pass takes the row sums: no log-sum-exp pass of its own
   int64_t Tc;
-  size_t o_hdr, o_blk, o_cls, o_cidx, o_orig, o_coef, o_off16, o_b2, o_lse2, o_term, o_hc, o_lpart, o_part, o_wide, o_m2, o_h2, o_low2, o_rescale, o_sparse, o_dhpart,
+  size_t o_hdr, o_blk, o_cls, o_cidx, o_orig, o_coef, o_off16, o_b2, o_lse2, o_term, o_hc, o_lpart, o_part, o_wide, o_m2, o_rescale, o_sparse, o_dhpart,
       o_keys, o_share, o_usum, o_first, total;
   SortBuffers sort;
   size_t clear_bytes;            // header and histograms
 };
 
 // A call that needs both the log-sum-exps and dH can take the row sums in the dH
-// pass, with a bound as the exponentials' reference (k_head_ref): it saves the
-// log-sum-exp pass and costs a read of E's norms and two small launches.
-constexpr int64_t kFusedLogits = 1000000;
+// pass, with a bound as the exponentials' reference (see the gather): it saves the
+// log-sum-exp pass and costs a read of E's norms.
+// Measured for the whole gradient call, D = 64, with / without: 67.6 / 65.6 us at
+// T V = 2.6e6 logits, 79.5 / 81.3 at 1.0e7, 125 / 142 at 6.4e7.
+constexpr int64_t kFusedLogits = 8000000;
 
 // dH partials per position: about 16 work items per SM, at most kMaxSplits splits;
 // with few position tiles enough splits for one work item per SM.
@@ -291,15 +293,13 @@ void plan_head(const HeadProblem& p, bool dH, bool dE, bool lse_pass, HeadPlan& 
   pl.o_part = lse_pass ? l.take(8 * static_cast<size_t>(pl.S) * kMaxHeadSlots * Tc) : 0;
   pl.o_wide = pl.fused ? l.take(8 * static_cast<size_t>(pl.S) * kMaxHeadSlots * Tc) : 0;
   pl.o_m2 = pl.fused ? l.take(4 * Tc) : 0;
-  pl.o_h2 = pl.fused ? l.take(4 * Tc) : 0;
-  pl.o_low2 = pl.fused ? l.take(4 * Tc) : 0;
   pl.o_rescale = l.take(4 * Tc);
   pl.o_sparse = dH ? l.take(4 * Tc * pl.DP) : 0;
   pl.o_dhpart = dH ? l.take(4 * static_cast<size_t>(pl.S) * Tc * pl.DP) : 0;
   pl.o_keys = dE ? l.take(4 * TK) : 0;
   pl.o_share = dE ? l.take(4 * TK) : 0;
   pl.o_usum = dE ? l.take(4 * TK * p.D) : 0;
-  pl.o_first = dE ? l.take(4 * static_cast<size_t>(p.V)) : 0;
+  pl.o_first = dE ? l.take(16 * static_cast<size_t>(ceil_div(p.V, 4))) : 0;
   pl.total = l.total;
 }
 
@@ -399,11 +399,7 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   hp.lse2 = at<float>(ws, pl.o_lse2);
   hp.lse_in = lse_in;
   hp.c2 = kLog2eF / p.tau;
-  if (pl.fused) {
-    hp.m2 = at<float>(ws, pl.o_m2);
-    hp.h2 = at<float>(ws, pl.o_h2);
-    hp.low2 = at<float>(ws, pl.o_low2);
-  }
+  hp.m2 = pl.fused ? at<float>(ws, pl.o_m2) : nullptr;
   hp.rescale = at<float>(ws, pl.o_rescale);
   hp.part = lse_in == nullptr ? at<float2>(ws, pl.o_part) : nullptr;
   const int lse_slots = 2 * pl.S_lse * SoftmaxCfg<64, kPassLse>::GROUPS;   // slabs x groups a split
@@ -415,20 +411,17 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   hp.logp_out = out.logp;
   int* status = &hp.hdr->w.status;
 
-  const bool one_block = p.T <= kOneBlockRows && pl.clear_bytes <= 256;
+  const bool one_block = p.T <= kOneBlockRows && pl.clear_bytes <= 256 && !pl.fused;
   if (!one_block) CUTBCE_CK(cudaMemsetAsync(hp.hdr, 0, pl.clear_bytes, st));
   {
     LaunchScope ls(CUTBCE_KERNEL_HEAD_PREP, st);
     if (one_block) k_head_rows_one<<<1, kOneBlockRows, 0, st>>>(hp);
-    else k_head_rows<<<static_cast<unsigned>(pl.n_blk), 256, 0, st>>>(hp);
-    if (pl.fused)
-      k_head_norm<<<static_cast<unsigned>(std::min<int64_t>(ceil_div(p.V, 128), 8 * 148)), 256, 0, st>>>(hp.E, p.V, hp.D,
-                                                                                                       hp.hdr);
+    else k_head_rows<<<static_cast<unsigned>(pl.n_blk + (pl.fused ? std::min<int64_t>(ceil_div(p.V, 128), 8 * 148) : 0)), 256,
+                       0, st>>>(hp);
     const unsigned gather_grid = static_cast<unsigned>(ceil_div(p.T + 256, 8));
     if (pl.DP == 64) k_head_gather<8><<<gather_grid, 256, 0, st>>>(hp);
     else if (pl.DP == 128) k_head_gather<16><<<gather_grid, 256, 0, st>>>(hp);
     else k_head_gather<32><<<gather_grid, 256, 0, st>>>(hp);
-    if (pl.fused) k_head_ref<<<static_cast<unsigned>(ceil_div(pl.Tc, 256)), 256, 0, st>>>(hp);
     CUTBCE_CK(cudaGetLastError());
   }
   SoftmaxParams sp{};
@@ -508,7 +501,8 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   if (dE) {
     // the sparse part of dE: sum of coef q h over the pairs of each item, in fp32
     SegmentParams gp{};
-    if ((s = run_sort(pl.sort, hp.keys, hp.V, ws, status, false, FillJob{}, st, &gp.pairs)) != CUTBCE_OK) return s;
+    const FillJob none{at<uint4>(ws, pl.o_first), ceil_div(p.V, 4), 0xFFFFFFFFu};
+    if ((s = run_sort(pl.sort, hp.keys, hp.V, ws, status, false, none, st, &gp.pairs)) != CUTBCE_OK) return s;
     gp.N = p.T * p.K;
     gp.V = hp.V;
     gp.D = hp.D;
@@ -521,7 +515,6 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
     gp.out = at<float>(ws, pl.o_usum);
     gp.first = at<int>(ws, pl.o_first);
     gp.status = status;
-    CUTBCE_CK(cudaMemsetAsync(gp.first, 0xFF, 4 * static_cast<size_t>(p.V), st));
     if ((s = run_sums(gp, true, st)) != CUTBCE_OK) return s;
     sp.first = gp.first;
     sp.sparse = at<float>(ws, pl.o_usum);
@@ -605,7 +598,7 @@ cutbce_status cutbce_embed_backward(const void* dX, int32_t dtype, const int32_t
   // dE starts at zero: by blocks beside the sort, or ahead of it where its ends are not 16-byte aligned
   const size_t de_bytes = eo * static_cast<size_t>(V) * D;
   FillJob fill{};
-  if (!accumulate && aligned(dE, 16) && de_bytes % 16 == 0) fill = FillJob{static_cast<uint4*>(dE), static_cast<int64_t>(de_bytes / 16)};
+  if (!accumulate && aligned(dE, 16) && de_bytes % 16 == 0) fill = FillJob{static_cast<uint4*>(dE), static_cast<int64_t>(de_bytes / 16), 0u};
   else if (!accumulate) CUTBCE_CK(cudaMemsetAsync(dE, 0, de_bytes, st));
   SegmentParams p{};
   s = run_sort(pl.sort, ids, static_cast<int>(V), ws, status, true, fill, st, &p.pairs);

@@ -52,14 +52,17 @@ inline void make_sort_plan(int64_t N, int64_t V, SortPlan& s) {
   s.hist_bytes = sizeof(int) * static_cast<size_t>(s.passes) * s.nblk * (size_t(1) << s.bits);
 }
 
-// Zeros for a dense gradient's rows, written by blocks of their own beside a sort
-// kernel that leaves most SMs idle: `n` pieces of 16 bytes.
+// Memory to set (zeros for a dense gradient's rows, -1 for an index), written by
+// blocks of their own beside a sort kernel that leaves most SMs idle: `n` pieces of 16
+// bytes, every 32-bit word `value`.
 struct FillJob {
   uint4* dst;
   int64_t n;                // 0: nothing to fill
+  uint32_t value;
 };
-__device__ __forceinline__ void fill_zeros(const FillJob& f, int64_t block, int64_t blocks) {
-  for (int64_t i = block * blockDim.x + threadIdx.x; i < f.n; i += blocks * blockDim.x) f.dst[i] = make_uint4(0u, 0u, 0u, 0u);
+__device__ __forceinline__ void fill_words(const FillJob& f, int64_t block, int64_t blocks) {
+  for (int64_t i = block * blockDim.x + threadIdx.x; i < f.n; i += blocks * blockDim.x)
+    f.dst[i] = make_uint4(f.value, f.value, f.value, f.value);
 }
 
 // Keys from plain ids (lookup gradient): -1 is an empty entry, any other id outside
@@ -70,7 +73,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_keys(const int32_t* __res
                                                             FillJob fill) {
   __shared__ int h[kSortMaxBins];
   if (static_cast<int>(blockIdx.x) >= nblk) {
-    fill_zeros(fill, static_cast<int>(blockIdx.x) - nblk, static_cast<int>(gridDim.x) - nblk);
+    fill_words(fill, static_cast<int>(blockIdx.x) - nblk, static_cast<int>(gridDim.x) - nblk);
     return;
   }
   const int bins = 1 << bits;
@@ -288,7 +291,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
     k_sort_cluster(const int* __restrict__ ids, int N, int V, int bits, int passes, int2* buf0, int2* buf1, int* status,
                    int clear_status, FillJob fill) {
   if (blockIdx.x >= kClusterCtas) {                         // clusters past the first
-    fill_zeros(fill, static_cast<int>(blockIdx.x) - kClusterCtas, static_cast<int>(gridDim.x) - kClusterCtas);
+    fill_words(fill, static_cast<int>(blockIdx.x) - kClusterCtas, static_cast<int>(gridDim.x) - kClusterCtas);
     return;
   }
   extern __shared__ uint16_t s_cnt[];                       // [32 warps][bins]

@@ -85,10 +85,10 @@ struct SoftmaxParams {
 };
 
 // Pairs of every 16 whose exponential runs on the FMA pipe instead of the SFU.
-// Measured at 9.0e9 logits, D = 64, for 2 / 3 / 4 pairs: dH pass 2.20 / 2.20 / 2.17
-// ms, dE pass 2.23 / 2.15 / 2.09 ms; log-sum-exp pass for 4 / 5 / 6: 2.09 / 2.02 /
-// 2.05 ms.
-constexpr int kPolyLse = 5, kPolyRows = 4, kPolyItems = 4;
+// Measured at 9.0e9 logits, D = 64, for 2 / 4 / 5 / 6 / 7 pairs: dH pass 2.20 / 2.17 /
+// 2.15 / 2.15 / 2.26 ms, dE pass 2.23 / 2.09 / 2.11 / 2.10 / 2.16 ms; log-sum-exp
+// pass for 4 / 5 / 6 / 7: 2.09 / 2.01 / 2.05 / 2.14 ms.
+constexpr int kPolyLse = 5, kPolyRows = 5, kPolyItems = 5;
 
 // 2^x of a pair on the FMA pipe, x clamped below at -125: as exp2_poly3_pair, with
 // the degree chosen by what the value feeds.  kDegree 3 (relative error 7.5e-5) for

@@ -37,7 +37,7 @@ struct HeadHeader {
   int lse_ticket;
   int pairs_ticket;
   unsigned emax2;           // bits of max |e_v|^2 (with a dH pass that takes the row sums too)
-  int wide;                 // 1: some row's logits may lie too far below its bound (see k_head_ref)
+  int wide;                 // 1: some row's logits may lie too far below its bound (see the gather)
 };
 static_assert(sizeof(HeadHeader) <= 256, "the workspace header is 256 bytes");
 
@@ -73,8 +73,6 @@ struct HeadParams {
   float* lse2;                   // [Tc] lse in the log2 domain
   const float* lse_in;           // [T] lse of an earlier forward, or null
   float* m2;                     // [Tc] reference of the row's exponentials in the dH pass, or null
-  float* h2;                     // [Tc] |h|^2, with m2
-  float* low2;                   // [Tc] a logit that the row has (log2 domain), with m2
   float c2;                      // log2(e) / tau
   float* rescale;                // [Tc] 2^(reference - lse): factor of the dense part of dH
   const float2* part;            // [slots, Tc] (reference, sum) partials in the log2 domain
@@ -171,7 +169,54 @@ __device__ __forceinline__ bool bad_offsets(const HeadParams& p, int i0, int n) 
   return bad;
 }
 
+// Largest |e_v|^2 over the table: eight lanes a row, 16 bytes a lane, four rows in
+// flight.  The maximum is over float bits (all >= 0), so the order of the atomics
+// changes nothing; a NaN stays the maximum.
+__device__ __forceinline__ void table_norm(const __nv_bfloat16* __restrict__ E, int64_t V, int D, HeadHeader* hdr,
+                                           int block, int blocks) {
+  constexpr int U = 4;
+  const int sub = threadIdx.x & 7;
+  const int64_t step = static_cast<int64_t>(blocks) * 32;
+  unsigned best = 0u;
+  // every lane of a warp runs the same trips, so that the sums below are whole
+  for (int64_t v0 = static_cast<int64_t>(block) * 32; v0 < V; v0 += U * step) {
+    float s[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) s[u] = 0.f;
+    for (int i = sub; i < D / 8; i += 8) {
+      uint4 x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t v = min(v0 + u * step + (threadIdx.x >> 3), V - 1);     // a row read twice changes nothing
+        x[u] = __ldg(reinterpret_cast<const uint4*>(E + v * D) + i);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float a = __uint_as_float(w[k] << 16), b = __uint_as_float(w[k] & 0xFFFF0000u);
+          s[u] = fmaf(a, a, fmaf(b, b, s[u]));
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+      best = max(best, __float_as_uint(s[u]) & 0x7FFFFFFFu);
+    }
+  }
+  best = __reduce_max_sync(0xffffffffu, best);
+  if ((threadIdx.x & 31) == 0 && best > *reinterpret_cast<volatile unsigned*>(&hdr->emax2)) atomicMax(&hdr->emax2, best);
+}
+
+// Blocks from n_blk on read the table's norms (with m2).
 __global__ void __launch_bounds__(256) k_head_rows(const HeadParams p) {
+  if (static_cast<int>(blockIdx.x) >= p.n_blk) {
+    table_norm(p.E, p.V, p.D, p.hdr, static_cast<int>(blockIdx.x) - p.n_blk, static_cast<int>(gridDim.x) - p.n_blk);
+    return;
+  }
   __shared__ int cnt[2];
   __shared__ int last;
   __shared__ int tot[2][256];
@@ -180,7 +225,7 @@ __global__ void __launch_bounds__(256) k_head_rows(const HeadParams p) {
   const int t = blockIdx.x * 256 + tid;
   if (tid < 2) cnt[tid] = 0;
   __syncthreads();
-  bool bad = bad_offsets(p, t, gridDim.x * 256);
+  bool bad = bad_offsets(p, t, p.n_blk * 256);
   const int cls = row_class(p, t, bad);
   if (bad) atomicCAS(&hdr->w.status, 0, kErrTargetRange);
   if (t < p.T) p.cls[t] = static_cast<uint8_t>(cls);
@@ -194,7 +239,7 @@ __global__ void __launch_bounds__(256) k_head_rows(const HeadParams p) {
     p.blk[2 * blockIdx.x] = cnt[0];
     p.blk[2 * blockIdx.x + 1] = cnt[1];
     __threadfence();
-    last = atomicAdd(&hdr->rows_ticket, 1) == static_cast<int>(gridDim.x) - 1;
+    last = atomicAdd(&hdr->rows_ticket, 1) == p.n_blk - 1;
   }
   __syncthreads();
   if (!last) return;
@@ -260,53 +305,21 @@ __global__ void __launch_bounds__(kOneBlockRows) k_head_rows_one(const HeadParam
   }
 }
 
-// ------------------------------------------------------------------ norm
-// Largest |e_v|^2 over the table: eight lanes a row, 16 bytes a lane, four rows in
-// flight.  The maximum is over float bits (all >= 0), so the order of the atomics
-// changes nothing; a NaN stays the maximum.
-__global__ void __launch_bounds__(256) k_head_norm(const __nv_bfloat16* __restrict__ E, int64_t V, int D, HeadHeader* hdr) {
-  constexpr int U = 4;
-  const int sub = threadIdx.x & 7;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * 32;
-  unsigned best = 0u;
-  // every lane of a warp runs the same trips, so that the sums below are whole
-  for (int64_t v0 = static_cast<int64_t>(blockIdx.x) * 32; v0 < V; v0 += U * step) {
-    float s[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) s[u] = 0.f;
-    for (int i = sub; i < D / 8; i += 8) {
-      uint4 x[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t v = min(v0 + u * step + (threadIdx.x >> 3), V - 1);     // a row read twice changes nothing
-        x[u] = __ldg(reinterpret_cast<const uint4*>(E + v * D) + i);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float a = __uint_as_float(w[k] << 16), b = __uint_as_float(w[k] & 0xFFFF0000u);
-          s[u] = fmaf(a, a, fmaf(b, b, s[u]));
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
-      best = max(best, __float_as_uint(s[u]) & 0x7FFFFFFFu);
-    }
-  }
-  best = __reduce_max_sync(0xffffffffu, best);
-  if ((threadIdx.x & 31) == 0 && best > *reinterpret_cast<volatile unsigned*>(&hdr->emax2)) atomicMax(&hdr->emax2, best);
-}
-
 // ------------------------------------------------------------------ gather
 // One warp per position, then one warp per padding row (256 of them at most).
 // `L` lanes hold a row in 16-byte pieces (8, 16 or 32 for DP = 64, 128 and above),
 // so a warp reads the rows of 32 / L targets at once, kGatherU of those in flight.
+//
+// With m2 it also sets the reference of the row's exponentials in a dH pass that
+// takes the row's sum on the way: m = |h| max|e| c, a bound of every logit
+// (Cauchy-Schwarz), so 2^(x - m) never overflows.  It must not lie too far above
+// the row's largest logit either: terms below 2^-126 are lost, and with a gap of at
+// most 70 (log2) the V < 2^31 lost terms are below 2^-25 of the sum.  The gap is
+// bounded by a logit that the row is known to have, its largest sparse target.
+// Rows beyond it set `wide`, and then the log-sum-exp pass runs first and its
+// result is the reference.
 constexpr int kGatherU = 4;
+constexpr float kMaxRefGap = 70.f;
 
 __device__ __forceinline__ void unpack8(uint4 r, float (&x)[8]) {
   const uint32_t u[4] = {r.x, r.y, r.z, r.w};
@@ -337,7 +350,7 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
       p.orig[c] = -1;
       write_offset(p, c, -1e30f);
       p.lse2[c] = 0.f;
-      if (p.m2 != nullptr) p.h2[c] = p.low2[c] = 0.f;
+      if (p.m2 != nullptr) p.m2[c] = 0.f;
     }
     return;
   }
@@ -481,8 +494,10 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) {
-      p.h2[c] = s;
-      p.low2[c] = zmax * p.c2;
+      const float bound = sqrtf(s) * sqrtf(__uint_as_float(hdr->emax2)) * p.c2;
+      const float m = bound * 1.0001f + 0.01f;               // above the rounding of the norms
+      p.m2[c] = m;
+      if (!(m - zmax * p.c2 <= kMaxRefGap)) p.hdr->wide = 1; // NaN counts as wide
     }
   }
   if (lane == 0) {
@@ -504,27 +519,6 @@ __device__ __forceinline__ double head_block_sum(double v, double* red) {
   const double r = red[0];
   __syncthreads();
   return r;
-}
-
-// ------------------------------------------------------------------ ref
-// The reference of a row's exponentials when the dH pass takes the row's sum on
-// the way: m = |h| max|e| c, a bound of every logit (Cauchy-Schwarz), so 2^(x - m)
-// never overflows.  It must not lie too far above the row's largest logit either:
-// terms below 2^-126 are lost, and with a gap of at most 70 (log2) the V < 2^31
-// lost terms are below 2^-25 of the sum.  The gap is bounded by a logit that the
-// row is known to have, its largest sparse target.  Rows beyond it set `wide`, and
-// then the log-sum-exp pass runs first and its result is the reference.
-constexpr float kMaxRefGap = 70.f;
-
-__global__ void __launch_bounds__(256) k_head_ref(const HeadParams p) {
-  HeadHeader* hdr = p.hdr;
-  if (hdr->w.status != 0) return;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (c >= hdr->n_rows) return;
-  const float bound = sqrtf(p.h2[c]) * sqrtf(__uint_as_float(hdr->emax2)) * p.c2;
-  const float m = bound * 1.0001f + 0.01f;                  // above the rounding of the norms
-  p.m2[c] = m;
-  if (!(m - p.low2[c] <= kMaxRefGap)) hdr->wide = 1;       // NaN counts as wide
 }
 
 // ------------------------------------------------------------------ lse
@@ -705,13 +699,18 @@ __global__ void __launch_bounds__(256) k_head_dh(const HeadDhParams p) {
     const float* src = p.part + static_cast<int64_t>(c) * p.DP + col;
     const int64_t stride = p.Tc * p.DP;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int s = 0; s < p.S; ++s) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(src + s * stride));
-      a.x += v.x;
-      a.y += v.y;
-      a.z += v.z;
-      a.w += v.w;
+    for (int s0 = 0; s0 < p.S; s0 += 8) {                     // eight loads in flight, added in split order
+      float4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        v[u] = s0 + u < p.S ? __ldg(reinterpret_cast<const float4*>(src + (s0 + u) * stride)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        a.x += v[u].x;
+        a.y += v[u].y;
+        a.z += v[u].z;
+        a.w += v[u].w;
+      }
     }
     const float4 q = __ldg(reinterpret_cast<const float4*>(p.sparse + static_cast<int64_t>(c) * p.DP + col));
     const float f = p.hdr->w.grad_scale * p.coef[t];
