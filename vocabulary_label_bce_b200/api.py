@@ -253,14 +253,17 @@ def embed(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0) -> torch.Tenso
 def _rows(H: torch.Tensor, *rest: Optional[torch.Tensor]):
     """H [.., D] and per-position tensors flattened to T rows."""
     lead = H.dim() - 1
-    out = [_plain(H) if lead == 1 else _plain(H).view(-1, H.shape[-1])]
+    size = H.shape[:lead]
     for t in rest:
-        if t is not None:
-            if t.shape[:lead] != H.shape[:lead]:
-                raise ValueError(f"leading sizes {tuple(t.shape[:lead])} and {tuple(H.shape[:lead])} do not fit")
-            t = _plain(t) if lead == 1 else _plain(t).view((-1,) + t.shape[lead:])
-        out.append(t)
-    return out
+        if t is not None and t.shape[:lead] != size:
+            raise ValueError(f"leading sizes {tuple(t.shape[:lead])} and {tuple(size)} do not fit")
+    if lead == 1:
+        return [_plain(H)] + [None if t is None else _plain(t) for t in rest]
+    return [_plain(H).view(-1, H.shape[-1])] + [None if t is None else _plain(t).view((-1,) + t.shape[lead:]) for t in rest]
+
+
+def _as(t: Optional[torch.Tensor], dtype: torch.dtype) -> Optional[torch.Tensor]:
+    return t if t is None or t.dtype == dtype else t.to(dtype)
 
 
 def _distill_problem(H, E, ids, logits, mask, weights, temperature, reduction):
@@ -268,8 +271,7 @@ def _distill_problem(H, E, ids, logits, mask, weights, temperature, reduction):
     _on_cuda(H)
     if logits.shape != ids.shape:
         raise ValueError("teacher ids and logits must have one shape")
-    H2, ids2, lg, m, w = _rows(H, _ids32(ids), logits.to(torch.float32), mask,
-                               None if weights is None else weights.to(torch.float32))
+    H2, ids2, lg, m, w = _rows(H, _ids32(ids), _as(logits, torch.float32), mask, _as(weights, torch.float32))
     E2 = _plain(E)
     keep = (H2, E2, ids2, lg, m, w)
     return B.make_distill_problem(H2, E2, ids2, lg, m, w, temperature, reduction), keep
@@ -283,8 +285,8 @@ def _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction):
             raise ValueError("without offsets H must be [2P, N, D]")
         offsets = torch.arange(0, H2.shape[0] + 1, H.shape[1], dtype=torch.int32, device=H.device)
     E2 = _plain(E)
-    off = offsets.to(torch.int32).contiguous()
-    ref = None if ref_logp is None else _plain(ref_logp).to(torch.float32).view(-1)
+    off = _as(offsets, torch.int32).contiguous()
+    ref = None if ref_logp is None else _as(_plain(ref_logp), torch.float32).view(-1)
     keep = (H2, E2, ids2, off, ref, m)
     return B.make_preference_problem(H2, E2, ids2, off, ref, m, beta, reduction), keep
 

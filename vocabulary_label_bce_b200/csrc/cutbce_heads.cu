@@ -234,7 +234,7 @@ cutbce_status check_head(const HeadProblem& p, bool need_data) {
 }
 
 constexpr int kMaxHeadSplits = 148;
-constexpr int kMaxHeadSlots = 2 * 3;           // partials per split: column slabs x epilogue groups
+constexpr int kHeadSlots = 4;                  // partials per split: column slabs x epilogue groups
 
 struct HeadPlan {
   int DP, BN, S, tps, n_vtiles, n_blk;
@@ -254,8 +254,35 @@ struct HeadPlan {
 // T V = 2.6e6 logits, 79.5 / 81.3 at 1.0e7, 125 / 142 at 6.4e7.
 constexpr int64_t kFusedLogits = 8000000;
 
-// dH partials per position: about 16 work items per SM, at most kMaxSplits splits;
-// with few position tiles enough splits for one work item per SM.
+// Vocabulary splits of a pass that owns position tiles (nT of them) and streams
+// `tiles` item tiles: the count with the least estimated time, in units of a streamed
+// tile.  A work item costs its tiles and about kItemColumns streamed rows more (stationary
+// tile, accumulator, pipeline fill); the persistent grid runs ceil(items / 148) of them one
+// after the other; a split of dH costs `split_cost` to add up.  Masked positions leave
+// fewer position tiles than the host knows, so the estimate is taken at three counts.
+// The splits depend on sizes alone (148 is a constant, not the device's SM count).
+// At T = 4,900, V = 100,000: 15 splits, 4 rounds of 56, where "16 items an SM" took 61
+// splits, 17 rounds of 16.
+constexpr double kItemColumns = 3.0 * 128;
+
+int choose_splits(int64_t nT, int64_t tiles, int BN, double split_cost) {
+  const double item_tiles = kItemColumns / BN;
+  int best = 1;
+  double best_cost = 1e300;
+  for (int64_t want = 1; want <= std::min<int64_t>(kMaxHeadSplits, tiles); ++want) {
+    const int64_t tps = ceil_div(tiles, want), S = ceil_div(tiles, tps);
+    if (S != want) continue;                       // the same cut as a smaller count
+    double cost = split_cost * static_cast<double>(S);
+    for (const int64_t n : {nT, nT, ceil_div(9 * nT, 10), ceil_div(8 * nT, 10)})
+      cost += 0.25 * static_cast<double>(ceil_div(S * n, 148)) * (static_cast<double>(tps) + item_tiles);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = static_cast<int>(S);
+    }
+  }
+  return best;
+}
+
 void plan_head(const HeadProblem& p, bool dH, bool dE, bool lse_pass, HeadPlan& pl) {
   pl.DP = static_cast<int>(round_up(p.D, 64));
   pl.BN = pl.DP > 128 ? 64 : 128;
@@ -265,14 +292,13 @@ void plan_head(const HeadProblem& p, bool dH, bool dE, bool lse_pass, HeadPlan& 
   pl.fused = lse_pass && dH && p.T * p.V >= kFusedLogits;
   pl.Tc = round_up(p.T, kTileM) + kTileM;
   const int64_t nT = ceil_div(p.T, kTileM);
-  int64_t s0 = std::max<int64_t>(std::min<int64_t>(ceil_div(16 * 148, nT), kMaxSplits),
-                                 std::min<int64_t>(ceil_div(148, nT), kMaxHeadSplits));
-  s0 = std::max<int64_t>(1, std::min<int64_t>(s0, pl.n_vtiles));
-  pl.tps = static_cast<int>(ceil_div(pl.n_vtiles, s0));
-  pl.S = static_cast<int>(ceil_div(pl.n_vtiles, pl.tps));
+  // dH partials are read at about 5 MB a microsecond, a streamed tile takes about 0.6
+  const double split_cost = 4.0 * static_cast<double>(pl.Tc) * pl.DP / 5e6 / 0.6;
+  pl.S = choose_splits(nT, pl.n_vtiles, pl.BN, split_cost);
+  pl.tps = static_cast<int>(ceil_div(pl.n_vtiles, pl.S));
   pl.n_vtiles_lse = static_cast<int>(ceil_div(p.V, pl.BN_lse));
-  pl.tps_lse = static_cast<int>(ceil_div(pl.n_vtiles_lse, std::min<int64_t>(pl.S, pl.n_vtiles_lse)));
-  pl.S_lse = static_cast<int>(ceil_div(pl.n_vtiles_lse, pl.tps_lse));   // every split is non-empty, at most S
+  pl.S_lse = choose_splits(nT, pl.n_vtiles_lse, pl.BN_lse, 0.1);
+  pl.tps_lse = static_cast<int>(ceil_div(pl.n_vtiles_lse, pl.S_lse));
   const size_t T = static_cast<size_t>(p.T), Tc = static_cast<size_t>(pl.Tc), TK = T * p.K;
   Layout l;
   pl.o_hdr = l.take(256);
@@ -290,8 +316,8 @@ void plan_head(const HeadProblem& p, bool dH, bool dE, bool lse_pass, HeadPlan& 
   pl.o_term = l.take(8 * Tc);
   pl.o_hc = l.take(2 * Tc * pl.DP);
   pl.o_lpart = l.take(8 * std::max<size_t>(static_cast<size_t>(p.P), Tc / kLseRows));
-  pl.o_part = lse_pass ? l.take(8 * static_cast<size_t>(pl.S) * kMaxHeadSlots * Tc) : 0;
-  pl.o_wide = pl.fused ? l.take(8 * static_cast<size_t>(pl.S) * kMaxHeadSlots * Tc) : 0;
+  pl.o_part = lse_pass ? l.take(8 * static_cast<size_t>(pl.fused ? pl.S : pl.S_lse) * kHeadSlots * Tc) : 0;
+  pl.o_wide = pl.fused ? l.take(8 * static_cast<size_t>(pl.S_lse) * kHeadSlots * Tc) : 0;
   pl.o_m2 = pl.fused ? l.take(4 * Tc) : 0;
   pl.o_rescale = l.take(4 * Tc);
   pl.o_sparse = dH ? l.take(4 * Tc * pl.DP) : 0;
@@ -402,8 +428,7 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   hp.m2 = pl.fused ? at<float>(ws, pl.o_m2) : nullptr;
   hp.rescale = at<float>(ws, pl.o_rescale);
   hp.part = lse_in == nullptr ? at<float2>(ws, pl.o_part) : nullptr;
-  const int lse_slots = 2 * pl.S_lse * SoftmaxCfg<64, kPassLse>::GROUPS;   // slabs x groups a split
-  hp.slots = pl.fused ? 2 * pl.S * SoftmaxCfg<64, kPassRows>::GROUPS : lse_slots;
+  hp.slots = kHeadSlots * (pl.fused ? pl.S : pl.S_lse);
   hp.Tc = pl.Tc;
   hp.loss_part = at<double>(ws, pl.o_lpart);
   hp.loss = out.loss;
@@ -436,14 +461,16 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   sp.timeout_ns = kDefaultTimeoutNs;
   CUtensorMap m_rows_s;                                      // the positions as stationary operand
   if (!make_map(&m_rows_s, hp.Hc, pl.DP, pl.Tc, pl.DP, kTileM)) return CUTBCE_ERR_CUDA;
-  const int64_t row_items = static_cast<int64_t>(pl.S) * (pl.Tc / kTileM);
-  const int row_grid = static_cast<int>(std::min<int64_t>({static_cast<int64_t>(dev.sms), row_items, static_cast<int64_t>(kMaxCtas)}));
+  auto row_grid = [&](int splits) {                          // persistent: at most one CTA per SM
+    const int64_t items = static_cast<int64_t>(splits) * (pl.Tc / kTileM);
+    return static_cast<int>(std::min<int64_t>({static_cast<int64_t>(dev.sms), items, static_cast<int64_t>(kMaxCtas)}));
+  };
   auto row_pass = [&]() -> cudaError_t {
     LaunchScope ls(CUTBCE_KERNEL_HEAD_ROW_PASS, st);
     sp.dh_part = at<float>(ws, pl.o_dhpart);
     CUtensorMap m_items_x;
     if (!make_map(&m_items_x, p.E, p.D, p.V, p.D, pl.BN)) return cudaErrorInvalidValue;
-    return launch_softmax_dp<kPassRows>(pl.DP, row_grid, m_rows_s, m_items_x, m_items_x, sp, st);
+    return launch_softmax_dp<kPassRows>(pl.DP, row_grid(pl.S), m_rows_s, m_items_x, m_items_x, sp, st);
   };
   if (lse_in == nullptr) {
     {
@@ -456,13 +483,13 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
       lp.n_item_tiles_bn = pl.n_vtiles_lse;
       lp.tiles_per_split = pl.tps_lse;
       lp.nsplit = pl.S_lse;
-      CUTBCE_CK(launch_softmax_dp<kPassLse>(pl.DP, row_grid, m_rows_s, m_lse_x, m_lse_x, lp, st));
+      CUTBCE_CK(launch_softmax_dp<kPassLse>(pl.DP, row_grid(pl.S_lse), m_rows_s, m_lse_x, m_lse_x, lp, st));
     }
     if (pl.fused) {
       sp.off2 = hp.m2;
       sp.part = at<float2>(ws, pl.o_part);
       sp.wide_part = at<float2>(ws, pl.o_wide);
-      sp.wide_slots = lse_slots;
+      sp.wide_slots = kHeadSlots * pl.S_lse;
       CUTBCE_CK(row_pass());
     }
     sp.part = nullptr;

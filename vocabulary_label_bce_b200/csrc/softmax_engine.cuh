@@ -62,6 +62,7 @@ struct SoftmaxCfg {
   static constexpr uint32_t SMEM_BYTES = 1024 + S_BYTES + NX * (X_BYTES + O_BYTES) + ONES_BYTES + NUM_BARS * 8 + 16 + 64;
   static_assert((!kGrad || ACC_COL + DP <= 512) && NZ * BN <= 512, "TMEM budget");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static_assert(GROUPS * SLABS == 4, "partials per split");
   static_assert(SMEM_BYTES > 232448 / 2, "one CTA per SM keeps the TMEM allocation uncontended");
 };
 
