@@ -114,7 +114,7 @@ cutbce_status run_sort(const SortBuffers& b, const int32_t* ids, int V, void* ws
     const size_t smem = size_t(64) << b.sp.bits;           // a 16-bit counter per warp and digit
     const cudaError_t e = set_smem_once<0>(k_sort_cluster, size_t(64) << kSortMaxBits);
     if (e != cudaSuccess) return CUTBCE_ERR_CUDA;
-    const int fill_clusters = static_cast<int>(std::min<int64_t>(ceil_div(fill.n, 2 * kClusterCtas * kClusterThreads), 18));
+    const int fill_clusters = static_cast<int>(std::min<int64_t>(ceil_div(fill.n, 2 * kClusterCtas * kClusterThreads), 36));
     k_sort_cluster<<<kClusterCtas * (1 + fill_clusters), kClusterThreads, smem, st>>>(ids, static_cast<int>(b.sp.N), V, b.sp.bits, b.sp.passes,
                                                                 at<int2>(ws, b.o_pairs[0]), at<int2>(ws, b.o_pairs[1]),
                                                                 status, clear_status ? 1 : 0, fill);
@@ -132,8 +132,10 @@ cutbce_status run_sums_t(const SegmentParams& p, cudaStream_t st) {
   LaunchScope ls(CUTBCE_KERNEL_SEGMENT_SUM, st);
   k_segment_sum<VEC, TIn, TOut><<<dim3(static_cast<unsigned>(g.chunks), static_cast<unsigned>(g.slices)),
                                   g.lanes * g.subs, 0, st>>>(p, g.lanes, g.subs, g.rounds);
+  constexpr int kJoinVec = VEC == 8 ? 4 : VEC;
   if (g.chunks > 1)
-    k_segment_join<VEC == 8 ? 4 : VEC, TOut><<<static_cast<unsigned>(g.chunks - 1), 256, 0, st>>>(p, g.chunk);
+    k_segment_join<kJoinVec, TOut><<<dim3(static_cast<unsigned>(g.chunks - 1), static_cast<unsigned>(ceil_div(p.D, 32 * kJoinVec))),
+                                     256, 0, st>>>(p, g.chunk);
   return cudaGetLastError() == cudaSuccess ? CUTBCE_OK : CUTBCE_ERR_CUDA;
 }
 

@@ -61,8 +61,14 @@ struct FillJob {
   uint32_t value;
 };
 __device__ __forceinline__ void fill_words(const FillJob& f, int64_t block, int64_t blocks) {
-  for (int64_t i = block * blockDim.x + threadIdx.x; i < f.n; i += blocks * blockDim.x)
-    f.dst[i] = make_uint4(f.value, f.value, f.value, f.value);
+  const uint4 v = make_uint4(f.value, f.value, f.value, f.value);
+  const int64_t step = blocks * blockDim.x;
+  int64_t i = block * blockDim.x + threadIdx.x;
+  for (; i + 3 * step < f.n; i += 4 * step) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) f.dst[i + u * step] = v;
+  }
+  for (; i < f.n; i += step) f.dst[i] = v;
 }
 
 // Keys from plain ids (lookup gradient): -1 is an empty entry, any other id outside
@@ -138,7 +144,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const int* __rest
   const int bins = 1 << bits, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // offset of (digit, this tile): all smaller digits, then this digit in earlier
   // tiles.  A thread holds four consecutive digits (of each 1024), sixteen tiles'
-  // histograms in flight with small tiles, eight with large ones.
+  // histograms in flight.
   int carry = 0;
   for (int h0 = 0; h0 < bins; h0 += 4 * kSortThreads) {
     const int d0 = h0 + 4 * tid;
@@ -151,7 +157,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const int* __rest
         before[0] = v.x, before[1] = v.y, before[2] = v.z, before[3] = v.w;
         total[0] = t.x, total[1] = t.y, total[2] = t.z, total[3] = t.w;
       } else {
-        constexpr int kTiles = IPT == 4 ? 16 : 8;       // tiles in flight; the last group is guarded, not looped
+        constexpr int kTiles = 16;                      // tiles in flight; the last group is guarded, not looped
         for (int b0 = 0; b0 < nblk; b0 += kTiles) {
           int4 v[kTiles];
 #pragma unroll
@@ -246,12 +252,15 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const int* __rest
   __syncthreads();
   if (failed != 0) return;
   auto put = [&](int r, int2 k, int rk) {
-    const int64_t i = wbase + r * 32 + lane;
-    if (i >= N) return;
-    const int pos = off[(k.x >> shift) & (bins - 1)] + rk;
-    out[pos] = k;
-    if (hist_next != nullptr)
-      atomicAdd(hist_next + static_cast<int64_t>(pos / (kSortThreads * IPT)) * bins + ((k.x >> (shift + bits)) & (bins - 1)), 1);
+    const bool live = wbase + r * 32 + lane < N;
+    const int pos = live ? off[(k.x >> shift) & (bins - 1)] + rk : 0;
+    if (live) out[pos] = k;
+    if (hist_next != nullptr) {
+      // one atomic per distinct counter of the warp: entries of a hot id share theirs
+      const int bin = live ? (pos / (kSortThreads * IPT)) * bins + ((k.x >> (shift + bits)) & (bins - 1)) : -1;
+      const unsigned peers = __match_any_sync(0xffffffffu, bin);
+      if (live && (peers & lt) == 0) atomicAdd(hist_next + bin, __popc(peers));
+    }
   };
 #pragma unroll
   for (int r = 0; r < IPT; ++r) {
@@ -664,41 +673,38 @@ __global__ void __launch_bounds__(256) k_segment_join(const SegmentParams p, int
     start = b0 + s_below;
   }
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  for (int col0 = 0; col0 < p.D; col0 += 32 * VEC) {
-    const int col = col0 + lane * VEC;
-    float acc[VEC];
+  const int col = (static_cast<int>(blockIdx.y) * 32 + lane) * VEC;
+  float acc[VEC];
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
-    if (col < p.D) {
-      for (int64_t cb = c0 + w; cb <= c1; cb += 32) {
-        RowPiece<VEC, float> q[4];
+  for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+  if (col < p.D) {
+    for (int64_t cb = c0 + w; cb <= c1; cb += 32) {
+      RowPiece<VEC, float> q[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int64_t c = min(cb + 8 * u, c1);
-          q[u].load(p.part + (2 * c + (c == c0 ? 1 : 0)) * p.D + col);
-        }
+      for (int u = 0; u < 4; ++u) {
+        const int64_t c = min(cb + 8 * u, c1);
+        q[u].load(p.part + (2 * c + (c == c0 ? 1 : 0)) * p.D + col);
+      }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          float v[VEC];
-          q[u].values(v);
-          if (cb + 8 * u <= c1) {
+      for (int u = 0; u < 4; ++u) {
+        float v[VEC];
+        q[u].values(v);
+        if (cb + 8 * u <= c1) {
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) acc[k] += v[k];
-          }
+          for (int k = 0; k < VEC; ++k) acc[k] += v[k];
         }
       }
     }
+  }
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) red[w][lane * VEC + k] = acc[k];
-    __syncthreads();
-    if (w == 0 && col < p.D) {
+  for (int k = 0; k < VEC; ++k) red[w][lane * VEC + k] = acc[k];
+  __syncthreads();
+  if (w == 0 && col < p.D) {
 #pragma unroll
-      for (int q = 1; q < 8; ++q)
+    for (int q = 1; q < 8; ++q)
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) acc[k] += red[q][lane * VEC + k];
-      write_sum<VEC, TOut>(p, id, start, col, acc);
-    }
-    __syncthreads();
+      for (int k = 0; k < VEC; ++k) acc[k] += red[q][lane * VEC + k];
+    write_sum<VEC, TOut>(p, id, start, col, acc);
   }
 }
 
