@@ -432,13 +432,25 @@ def cutbce_embed_backward(dX: torch.Tensor, ids: torch.Tensor, dE: torch.Tensor,
 _HEAD_REDUCTIONS = {"mean": 0, "sum": 1}
 
 
+def _head_ok(H, E, ids, mask, i: int) -> bool:
+    """Whether H, E, ids and mask are what the softmax losses take (one pass over the common case)."""
+    bf = torch.bfloat16
+    return (H.dtype is bf and E.dtype is bf and ids.dtype is torch.int32 and H.dim() == 2 and E.dim() == 2
+            and H.shape[1] == E.shape[1] and H.is_contiguous() and E.is_contiguous() and ids.is_contiguous()
+            and E.get_device() == i and ids.get_device() == i
+            and (mask is None or ((mask.dtype is torch.uint8 or mask.dtype is torch.bool) and mask.is_contiguous()
+                                  and mask.shape == H.shape[:1] and mask.get_device() == i)))
+
+
 def _head_tensors(H, E, ids, mask):
+    """Raises for what _head_ok refuses."""
     if H.dim() != 2 or E.dim() != 2 or H.shape[1] != E.shape[1]:
         raise ValueError("H [T, D] and E [V, D] do not fit")
     _dense(H, "H", (torch.bfloat16,))
     _dense(E, "E", (torch.bfloat16,))
     _dense(ids, "ids", (torch.int32,))
     _dense(mask, "mask", (torch.uint8, torch.bool), (H.shape[0],))
+    _same_device(H, E, ids, mask)
 
 
 def _head_reduction(reduction) -> int:
@@ -451,12 +463,15 @@ def make_distill_problem(H: torch.Tensor, E: torch.Tensor, ids: torch.Tensor, lo
                          mask: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None,
                          temperature: float = 1.0, reduction: str = "mean") -> cutbce_distill_problem:
     """H [T, D], E [V, D] bf16; teacher ids int32 [T, K] and logits float32 [T, K]; mask [T]; weights float32 [T]."""
-    _head_tensors(H, E, ids, mask)
+    i = H.get_device()
+    if not _head_ok(H, E, ids, mask, i):
+        _head_tensors(H, E, ids, mask)
     if ids.dim() != 2 or ids.shape[0] != H.shape[0]:
         raise ValueError("ids must be [T, K]")
     _dense(logits, "logits", (torch.float32,), ids.shape)
-    _dense(weights, "weights", (torch.float32,), (H.shape[0],))
-    _same_device(H, E, ids, logits, mask, weights)
+    _dense(weights, "weights", (torch.float32,), H.shape[:1])
+    if logits.get_device() != i or (weights is not None and weights.get_device() != i):
+        _same_device(H, logits, weights)
     return cutbce_distill_problem(H.shape[0], E.shape[0], H.shape[1], ids.shape[1], BF16, _head_reduction(reduction),
                                   H.data_ptr(), E.data_ptr(), ids.data_ptr(), logits.data_ptr(), _ptr(mask),
                                   _ptr(weights), float(temperature))
@@ -466,7 +481,9 @@ def make_preference_problem(H: torch.Tensor, E: torch.Tensor, ids: torch.Tensor,
                             ref_logp: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
                             beta: float = 0.1, reduction: str = "mean") -> cutbce_preference_problem:
     """H [T, D], E [V, D] bf16; ids int32 [T]; offsets int32 [2P + 1]; ref_logp float32 [2P]; mask [T]."""
-    _head_tensors(H, E, ids, mask)
+    i = H.get_device()
+    if not _head_ok(H, E, ids, mask, i):
+        _head_tensors(H, E, ids, mask)
     if ids.numel() != H.shape[0]:
         raise ValueError("ids must be [T]")
     _dense(offsets, "offsets", (torch.int32,))
@@ -474,7 +491,8 @@ def make_preference_problem(H: torch.Tensor, E: torch.Tensor, ids: torch.Tensor,
         raise ValueError("offsets must be [2P + 1] with P >= 1")
     P = (offsets.numel() - 1) // 2
     _dense(ref_logp, "ref_logp", (torch.float32,), (2 * P,))
-    _same_device(H, E, ids, offsets, ref_logp, mask)
+    if offsets.get_device() != i or (ref_logp is not None and ref_logp.get_device() != i):
+        _same_device(H, offsets, ref_logp)
     return cutbce_preference_problem(H.shape[0], E.shape[0], H.shape[1], P, BF16, _head_reduction(reduction),
                                      H.data_ptr(), E.data_ptr(), ids.data_ptr(), offsets.data_ptr(), _ptr(ref_logp),
                                      _ptr(mask), float(beta))

@@ -438,17 +438,22 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   hp.logp_out = out.logp;
   int* status = &hp.hdr->w.status;
 
-  const bool one_block = p.T <= kOneBlockRows && pl.clear_bytes <= 256 && !pl.fused;
-  if (!one_block) CUTBCE_CK(cudaMemsetAsync(hp.hdr, 0, pl.clear_bytes, st));
+  const bool small = p.T <= kSmallRows && pl.clear_bytes <= 256 && !pl.fused;
+  if (!small) CUTBCE_CK(cudaMemsetAsync(hp.hdr, 0, pl.clear_bytes, st));
   {
     LaunchScope ls(CUTBCE_KERNEL_HEAD_PREP, st);
-    if (one_block) k_head_rows_one<<<1, kOneBlockRows, 0, st>>>(hp);
-    else k_head_rows<<<static_cast<unsigned>(pl.n_blk + (pl.fused ? std::min<int64_t>(ceil_div(p.V, 128), 8 * 148) : 0)), 256,
-                       0, st>>>(hp);
-    const unsigned gather_grid = static_cast<unsigned>(ceil_div(p.T + 256, 8));
-    if (pl.DP == 64) k_head_gather<8><<<gather_grid, 256, 0, st>>>(hp);
-    else if (pl.DP == 128) k_head_gather<16><<<gather_grid, 256, 0, st>>>(hp);
-    else k_head_gather<32><<<gather_grid, 256, 0, st>>>(hp);
+    const unsigned grid = static_cast<unsigned>(ceil_div(p.T + 256, 8));
+    if (small) {
+      if (pl.DP == 64) k_head_gather<8, true><<<grid, 256, 0, st>>>(hp);
+      else if (pl.DP == 128) k_head_gather<16, true><<<grid, 256, 0, st>>>(hp);
+      else k_head_gather<32, true><<<grid, 256, 0, st>>>(hp);
+    } else {
+      const int64_t norm_blocks = pl.fused ? std::min<int64_t>(ceil_div(p.V, 128), 8 * 148) : 0;
+      k_head_rows<<<static_cast<unsigned>(pl.n_blk + norm_blocks), 256, 0, st>>>(hp);
+      if (pl.DP == 64) k_head_gather<8, false><<<grid, 256, 0, st>>>(hp);
+      else if (pl.DP == 128) k_head_gather<16, false><<<grid, 256, 0, st>>>(hp);
+      else k_head_gather<32, false><<<grid, 256, 0, st>>>(hp);
+    }
     CUTBCE_CK(cudaGetLastError());
   }
   SoftmaxParams sp{};

@@ -273,38 +273,6 @@ __global__ void __launch_bounds__(256) k_head_rows(const HeadParams p) {
   if (tid == 0) write_counts(p, tot[0][255], tot[1][255]);
 }
 
-// The same for up to kOneBlockRows positions in one block, which also clears the
-// header: a short call needs no memset.
-constexpr int kOneBlockRows = 1024;
-
-__global__ void __launch_bounds__(kOneBlockRows) k_head_rows_one(const HeadParams p) {
-  __shared__ int cnt[8];                          // [256-row block][class]
-  const int t = threadIdx.x;
-  if (t < static_cast<int>(sizeof(HeadHeader) / 4)) reinterpret_cast<int*>(p.hdr)[t] = 0;
-  if (t < 8) cnt[t] = 0;
-  __syncthreads();
-  bool bad = bad_offsets(p, t, kOneBlockRows);
-  const int cls = row_class(p, t, bad);
-  if (bad) atomicCAS(&p.hdr->w.status, 0, kErrTargetRange);
-  if (t < p.T) p.cls[t] = static_cast<uint8_t>(cls);
-  const unsigned pos = __ballot_sync(0xffffffffu, cls == 1), neg = __ballot_sync(0xffffffffu, cls == 2);
-  if ((t & 31) == 0) {
-    atomicAdd(&cnt[2 * (t >> 8)], __popc(pos));
-    atomicAdd(&cnt[2 * (t >> 8) + 1], __popc(neg));
-  }
-  __syncthreads();
-  if (t == 0) {
-    int np = 0, nn = 0;
-    for (int b = 0; b < p.n_blk; ++b) {
-      p.blk[2 * b] = np;
-      p.blk[2 * b + 1] = nn;
-      np += cnt[2 * b];
-      nn += cnt[2 * b + 1];
-    }
-    write_counts(p, np, nn);
-  }
-}
-
 // ------------------------------------------------------------------ gather
 // One warp per position, then one warp per padding row (256 of them at most).
 // `L` lanes hold a row in 16-byte pieces (8, 16 or 32 for DP = 64, 128 and above),
@@ -318,8 +286,13 @@ __global__ void __launch_bounds__(kOneBlockRows) k_head_rows_one(const HeadParam
 // bounded by a logit that the row is known to have, its largest sparse target.
 // Rows beyond it set `wide`, and then the log-sum-exp pass runs first and its
 // result is the reference.
+//
+// kSmall (up to kSmallRows positions): every block works out the classes of all
+// positions itself, and block 0 writes the header, so a short call has neither the
+// row kernel nor a memset before this one (one launch of 4 us less for the host).
 constexpr int kGatherU = 4;
 constexpr float kMaxRefGap = 70.f;
+constexpr int kSmallRows = 1024;
 
 __device__ __forceinline__ void unpack8(uint4 r, float (&x)[8]) {
   const uint32_t u[4] = {r.x, r.y, r.z, r.w};
@@ -330,11 +303,51 @@ __device__ __forceinline__ void unpack8(uint4 r, float (&x)[8]) {
   }
 }
 
-template <int L>
+template <int L, bool kSmall>
 __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
   constexpr int G = 32 / L;                     // targets side by side
   const HeadHeader* hdr = p.hdr;
-  if (hdr->w.status != 0) return;
+  __shared__ uint8_t s_cls[kSmall ? kSmallRows : 1];
+  __shared__ int s_cnt[kSmallRows / 256][2];    // rows per class of each 256 positions
+  __shared__ int s_bad;
+  int n_pos, n_neg, neg0;
+  if (kSmall) {
+    const int tid = threadIdx.x;
+    if (tid < kSmallRows / 128) (&s_cnt[0][0])[tid] = 0;
+    if (tid == 0) s_bad = 0;
+    if (blockIdx.x == 0 && tid < static_cast<int>(sizeof(HeadHeader) / 4)) reinterpret_cast<int*>(p.hdr)[tid] = 0;
+    __syncthreads();
+    bool bad = bad_offsets(p, tid, 256);
+#pragma unroll 1
+    for (int g = 0; g * 256 < p.T; ++g) {
+      const int cl = row_class(p, g * 256 + tid, bad);
+      s_cls[g * 256 + tid] = static_cast<uint8_t>(cl);
+      const unsigned pos = __ballot_sync(0xffffffffu, cl == 1), neg = __ballot_sync(0xffffffffu, cl == 2);
+      if ((tid & 31) == 0) {
+        atomicAdd(&s_cnt[g][0], __popc(pos));
+        atomicAdd(&s_cnt[g][1], __popc(neg));
+      }
+    }
+    if (bad) s_bad = 1;
+    __syncthreads();
+    n_pos = n_neg = 0;
+#pragma unroll
+    for (int g = 0; g < kSmallRows / 256; ++g) {
+      n_pos += s_cnt[g][0];
+      n_neg += s_cnt[g][1];
+    }
+    neg0 = (n_pos + kTileM - 1) / kTileM * kTileM;
+    if (blockIdx.x == 0 && tid == 0) {
+      write_counts(p, n_pos, n_neg);
+      if (s_bad != 0) p.hdr->w.status = kErrTargetRange;
+    }
+    if (s_bad != 0) return;
+  } else {
+    if (hdr->w.status != 0) return;
+    n_pos = hdr->n_pos;
+    n_neg = hdr->n_neg;
+    neg0 = hdr->neg0;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane % L, grp = lane / L;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + warp;
@@ -342,9 +355,9 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
   if (t >= p.T) {
     // padding rows: [n_pos, neg0) and [neg0 + n_neg, n_rows)
     const int j = static_cast<int>(t - p.T);
-    const int gap = hdr->neg0 - hdr->n_pos;
-    const int64_t c = j < gap ? hdr->n_pos + j : hdr->neg0 + hdr->n_neg + (j - gap);
-    if (c >= hdr->n_rows) return;
+    const int gap = neg0 - n_pos;
+    const int64_t c = j < gap ? n_pos + j : neg0 + n_neg + (j - gap);
+    if (c >= neg0 + (n_neg + kTileM - 1) / kTileM * kTileM) return;
     if (grp == 0 && piece) reinterpret_cast<uint4*>(p.Hc + c * p.DP)[sub] = make_uint4(0u, 0u, 0u, 0u);
     if (lane == 0) {
       p.orig[c] = -1;
@@ -354,7 +367,7 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
     }
     return;
   }
-  const int cls = p.cls[t];
+  const int cls = kSmall ? s_cls[t] : p.cls[t];
   const int64_t r = t * p.K;
   if (cls == 0) {
     if (p.keys != nullptr)
@@ -388,10 +401,15 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int k = lane + 32 * i;
-      if (k < n) before += p.cls[(static_cast<int64_t>(b) << 8) + k] == cls;
+      if (k < n) before += (kSmall ? s_cls[(b << 8) + k] : p.cls[(static_cast<int64_t>(b) << 8) + k]) == cls;
     }
     before = __reduce_add_sync(0xffffffffu, before);
-    c = p.blk[2 * b + cls - 1] + before + (cls == 2 ? hdr->neg0 : 0);
+    c = before + (cls == 2 ? neg0 : 0);
+    if (kSmall) {
+      for (int g = 0; g < b; ++g) c += s_cnt[g][cls - 1];
+    } else {
+      c += p.blk[2 * b + cls - 1];
+    }
   }
   if (grp == 0 && piece) reinterpret_cast<uint4*>(p.Hc + c * p.DP)[sub] = hraw;
   float h[8], sp[8];
