@@ -319,7 +319,7 @@ cutbce_status cutbce_embed_forward(const void* E, int64_t V, int64_t D, int32_t 
  * and that is rounded).  accumulate = 1 with the dE of a loss gives the gradient
  * of a table that is both the model's input and its output.  A bad id sets the
  * workspace status word (cutbce_read_status); dE is then unspecified.
- * ws: cutbce_embed_workspace_size bytes (about 16 N + N D / 4), 256-byte aligned. */
+ * ws: cutbce_embed_workspace_size bytes (about 16 N + N D / 2), 256-byte aligned. */
 cutbce_status cutbce_embed_workspace_size(int64_t N, int64_t V, int64_t D, size_t* bytes);
 cutbce_status cutbce_embed_backward(const void* dX, int32_t dtype, const int32_t* ids, int64_t N, int64_t V, int64_t D,
                                     float scale, void* dE, int32_t grad_dtype, int32_t accumulate, void* ws,
@@ -333,7 +333,9 @@ cutbce_status cutbce_embed_backward(const void* dX, int32_t dtype, const int32_t
  * With p_t = softmax(z_t / tau), every gradient has the form
  *   dz_tv = w_t (p_tv - q_tv),   dH = dz E,   dE = dz^T H.
  * The dense part w p is rounded to bf16 once, as the operand of the second tensor
- * contraction; the sparse part w q stays in fp32.  Deterministic.
+ * contraction; the sparse part w q stays in fp32.  Deterministic.  All sizes are at
+ * least 1.  On a data error (workspace status, cutbce_read_status) the loss is NaN and
+ * the other outputs are unspecified.
  *
  * Gradient options (NULL: fp32, overwrite). */
 typedef struct {

@@ -604,6 +604,49 @@ def test_captured_backward_beside_an_eager_graph():
     assert torch.equal(loss, eager) and all(torch.equal(a, b) for a, b in zip(grads, ge))
 
 
+def test_bad_ids_give_a_nan_loss():
+    Hf, H, Ef, E, ids, lg, m, w = draw_distill(T=30, V=100, D=64, K=3, seed=36, holes=False)
+    ids[11, 1] = 100
+    assert torch.isnan(api.distill_forward(H, E, dev(ids), dev(lg))[0])
+    y, off = dev(ids[:, 1]), torch.tensor([0, 15, 30], dtype=torch.int32, device="cuda")
+    assert torch.isnan(api.preference_forward(H, E, y, off)[0])
+    # more positions than the short form takes
+    big = H.repeat(50, 1)
+    assert torch.isnan(api.distill_forward(big, E, dev(ids).repeat(50, 1), dev(lg).repeat(50, 1))[0])
+
+
+def test_calls_by_keyword_and_refusals_on_the_device():
+    Hf, H, Ef, E, ids, lg, m, w = draw_distill(T=30, V=100, D=64, K=3, seed=37, holes=False)
+    i, l = dev(ids), dev(lg)
+    a = api.distill_forward_backward(H, E, i, l)
+    b = api.distill_forward_backward(E=E, H=H, teacher_logits=l, teacher_ids=i)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert torch.equal(api.embed_forward(ids=i, E=E), api.embed_forward(E, i))
+    g = torch.tensor(2.0)
+    for bad in (dict(grad_loss=g), dict(grad_loss=g.cuda().repeat(2)), dict(workspace=torch.empty(1 << 20, dtype=torch.uint8)),
+                dict(workspace=torch.empty(1 << 20, device="cuda")), dict(want_dH=False, want_dE=False),
+                dict(accumulate_dE=True), dict(dE_out=torch.empty(99, 64, device="cuda")),
+                dict(dE_out=torch.empty(100, 64)), dict(dE_out=torch.empty(100, 64, device="cuda"), grad_dtype=torch.bfloat16),
+                dict(grad_dtype=torch.float16)):
+        with pytest.raises(ValueError):
+            api.distill_forward_backward(H, E, i, l, **bad)
+    with pytest.raises(ValueError):
+        api.distill_forward(H, E, i, l.cpu())
+    with pytest.raises(ValueError):
+        api.distill_backward(H, E, i, l, torch.zeros(29, device="cuda"))
+    with pytest.raises(B.CutBCEError) as e:
+        api.distill_forward(H, E, i, l, workspace=torch.empty(1024, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == B.ERR_WORKSPACE
+    p = B.make_distill_problem(H, E, i, l)
+    ws = torch.empty(B.cutbce_distill_workspace_size(p, 7), dtype=torch.uint8, device="cuda")
+    loss, lse = torch.empty((), dtype=torch.float64, device="cuda"), torch.empty(30, device="cuda")
+    for args in ((loss.float(), lse), (loss, lse.double()), (loss, lse[:29])):
+        with pytest.raises(ValueError):
+            B.cutbce_distill_forward(p, *args, ws)
+    with pytest.raises(ValueError):
+        B.cutbce_distill_backward(p, None, lse, None, torch.empty(29, 64, device="cuda"), None, ws)
+
+
 def test_workspace_guards():
     """Nothing outside the requested workspace is written."""
     Hf, H, Ef, E, ids, lg, m, w = draw_distill(T=131, V=1333, D=72, K=5, seed=31, mask="random")

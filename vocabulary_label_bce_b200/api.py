@@ -6,6 +6,7 @@ libcutbce's kernels (see include/cutbce.h).
 from __future__ import annotations
 
 import functools
+import inspect
 from typing import Optional
 
 import torch
@@ -139,12 +140,15 @@ def _on_cuda(t: torch.Tensor) -> None:
 
 def _there(call):
     """The call, made on the device of its first tensor."""
+    name = next(iter(inspect.signature(call).parameters))
+
     @functools.wraps(call)
-    def wrapped(first, *args, **kw):
-        if first.is_cuda and first.get_device() != _current_device():
+    def wrapped(*args, **kw):
+        first = args[0] if args else kw.get(name)
+        if first is not None and first.is_cuda and first.get_device() != _current_device():
             with torch.cuda.device(first.device):
-                return call(first, *args, **kw)
-        return call(first, *args, **kw)
+                return call(*args, **kw)
+        return call(*args, **kw)
     return wrapped
 
 
@@ -163,12 +167,24 @@ def _ids32(ids: torch.Tensor) -> torch.Tensor:
     return ids.to(torch.int32).contiguous()
 
 
-def _scalar_grad(g: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
-    return None if g is None else g.detach().to(torch.float32).reshape(())
+def _scalar_grad(g: Optional[torch.Tensor], like: torch.Tensor) -> Optional[torch.Tensor]:
+    if g is None:
+        return None
+    if g.device != like.device or g.numel() != 1:
+        raise ValueError("grad_loss must be one value on the device of H")
+    return _as(g.detach(), torch.float32).reshape(())
 
 
-def _workspace(nbytes: int, device: torch.device, given: Optional[torch.Tensor]) -> torch.Tensor:
-    return given if given is not None else torch.empty(nbytes, dtype=torch.uint8, device=device)
+def _as(t: Optional[torch.Tensor], dtype: torch.dtype) -> Optional[torch.Tensor]:
+    return t if t is None or t.dtype == dtype else t.to(dtype)
+
+
+def _workspace(nbytes: int, like: torch.Tensor, given: Optional[torch.Tensor]) -> torch.Tensor:
+    if given is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if given.dtype != torch.uint8 or given.device != like.device or not given.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the device of the inputs")
+    return given
 
 
 @_there
@@ -204,7 +220,7 @@ def embed_backward(dX: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 1
             return torch.zeros((V, D), dtype=grad_dtype, device=dX.device)
         return out if accumulate else out.zero_()
     dE = out if out is not None else torch.empty((V, D), dtype=grad_dtype, device=dX.device)
-    ws = _workspace(B.cutbce_embed_workspace_size(ids.numel(), V, D), dX.device, workspace)
+    ws = _workspace(B.cutbce_embed_workspace_size(ids.numel(), V, D), dX, workspace)
     B.cutbce_embed_backward(_plain(dX).view(-1, D), _ids32(ids), dE, ws, scale, accumulate)
     return dE
 
@@ -260,10 +276,6 @@ def _rows(H: torch.Tensor, *rest: Optional[torch.Tensor]):
     if lead == 1:
         return [_plain(H)] + [None if t is None else _plain(t) for t in rest]
     return [_plain(H).view(-1, H.shape[-1])] + [None if t is None else _plain(t).view((-1,) + t.shape[lead:]) for t in rest]
-
-
-def _as(t: Optional[torch.Tensor], dtype: torch.dtype) -> Optional[torch.Tensor]:
-    return t if t is None or t.dtype == dtype else t.to(dtype)
 
 
 def _distill_problem(H, E, ids, logits, mask, weights, temperature, reduction):
@@ -324,7 +336,7 @@ def distill_forward(H, E, teacher_ids, teacher_logits, mask=None, weights=None, 
     H [T, D] or [B, N, D] and E [V, D] bf16; teacher_ids [.., K] (-1 empty) and teacher_logits [.., K]
     the teacher's top items and logits of each position; mask 1 = counts; weights a factor per position."""
     prob, keep = _distill_problem(H, E, teacher_ids, teacher_logits, mask, weights, temperature, reduction)
-    ws = _workspace(B.cutbce_distill_workspace_size(prob, B.OUT_LOSS), H.device, workspace)
+    ws = _workspace(B.cutbce_distill_workspace_size(prob, B.OUT_LOSS), H, workspace)
     loss = torch.empty((), dtype=torch.float64, device=H.device)
     lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
     B.cutbce_distill_forward(prob, loss, lse, ws)
@@ -339,8 +351,8 @@ def distill_backward(H, E, teacher_ids, teacher_logits, lse, mask=None, weights=
     """(dH, dE) given the lse of distill_forward on the same inputs."""
     prob, keep = _distill_problem(H, E, teacher_ids, teacher_logits, mask, weights, temperature, reduction)
     dH, dE, opts = _grad_outputs(H, E, want_dH, want_dE, grad_dtype, dE_out, accumulate_dE)
-    ws = _workspace(B.cutbce_distill_workspace_size(prob, _bits(dH, dE)), H.device, workspace)
-    g = _scalar_grad(grad_loss)
+    ws = _workspace(B.cutbce_distill_workspace_size(prob, _bits(dH, dE)), H, workspace)
+    g = _scalar_grad(grad_loss, H)
     B.cutbce_distill_backward(prob, opts, _lse_rows(lse, H), g, dH, dE, ws)
     return dH, dE
 
@@ -355,10 +367,10 @@ def distill_forward_backward(H, E, teacher_ids, teacher_logits, mask=None, weigh
     dE_out ([V, D], contiguous) is written instead of a new tensor, or added to with accumulate_dE."""
     prob, keep = _distill_problem(H, E, teacher_ids, teacher_logits, mask, weights, temperature, reduction)
     dH, dE, opts = _grad_outputs(H, E, want_dH, want_dE, grad_dtype, dE_out, accumulate_dE)
-    ws = _workspace(B.cutbce_distill_workspace_size(prob, B.OUT_LOSS | _bits(dH, dE)), H.device, workspace)
+    ws = _workspace(B.cutbce_distill_workspace_size(prob, B.OUT_LOSS | _bits(dH, dE)), H, workspace)
     loss = torch.empty((), dtype=torch.float64, device=H.device)
     lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
-    g = _scalar_grad(grad_loss)
+    g = _scalar_grad(grad_loss, H)
     B.cutbce_distill_forward_backward(prob, opts, g, loss, lse, dH, dE, ws)
     return loss, lse, dH, dE
 
@@ -374,7 +386,7 @@ def preference_forward(H, E, ids, offsets=None, ref_logp=None, mask=None, beta: 
     sequences' log-probabilities under the reference model (the second output of this call with
     that model's H and E), or None for 0."""
     prob, keep = _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction)
-    ws = _workspace(B.cutbce_preference_workspace_size(prob, B.OUT_LOSS), H.device, workspace)
+    ws = _workspace(B.cutbce_preference_workspace_size(prob, B.OUT_LOSS), H, workspace)
     loss = torch.empty((), dtype=torch.float64, device=H.device)
     logp = torch.empty(2 * prob.P, dtype=torch.float32, device=H.device)
     lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
@@ -390,8 +402,8 @@ def preference_backward(H, E, ids, lse, offsets=None, ref_logp=None, mask=None, 
     """(dH, dE) given the lse of preference_forward on the same inputs."""
     prob, keep = _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction)
     dH, dE, opts = _grad_outputs(H, E, want_dH, want_dE, grad_dtype, dE_out, accumulate_dE)
-    ws = _workspace(B.cutbce_preference_workspace_size(prob, _bits(dH, dE)), H.device, workspace)
-    g = _scalar_grad(grad_loss)
+    ws = _workspace(B.cutbce_preference_workspace_size(prob, _bits(dH, dE)), H, workspace)
+    g = _scalar_grad(grad_loss, H)
     B.cutbce_preference_backward(prob, opts, _lse_rows(lse, H), g, dH, dE, ws)
     return dH, dE
 
@@ -404,11 +416,11 @@ def preference_forward_backward(H, E, ids, offsets=None, ref_logp=None, mask=Non
     """(loss, logp, lse, dH, dE) in one call; None for a gradient that is not wanted."""
     prob, keep = _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction)
     dH, dE, opts = _grad_outputs(H, E, want_dH, want_dE, grad_dtype, dE_out, accumulate_dE)
-    ws = _workspace(B.cutbce_preference_workspace_size(prob, B.OUT_LOSS | _bits(dH, dE)), H.device, workspace)
+    ws = _workspace(B.cutbce_preference_workspace_size(prob, B.OUT_LOSS | _bits(dH, dE)), H, workspace)
     loss = torch.empty((), dtype=torch.float64, device=H.device)
     logp = torch.empty(2 * prob.P, dtype=torch.float32, device=H.device)
     lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
-    g = _scalar_grad(grad_loss)
+    g = _scalar_grad(grad_loss, H)
     B.cutbce_preference_forward_backward(prob, opts, g, loss, logp, lse, dH, dE, ws)
     return loss, logp, lse, dH, dE
 

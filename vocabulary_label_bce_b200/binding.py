@@ -509,6 +509,16 @@ def make_grad_options(dH: Optional[torch.Tensor], dE: Optional[torch.Tensor], ac
     return cutbce_grad_options(_GRADS[kinds.pop()], int(accumulate))
 
 
+def _head_outputs(prob, loss=None, lse=None, logp=None, dH=None, dE=None) -> None:
+    """Raises unless the outputs that are given hold what a call on `prob` writes."""
+    for t, dtype, n, name in ((loss, torch.float64, 1, "loss"), (lse, torch.float32, prob.T, "lse"),
+                              (logp, torch.float32, 2 * getattr(prob, "P", 0), "logp")):
+        if t is not None and (t.dtype is not dtype or t.numel() != n or not t.is_contiguous()):
+            raise ValueError(f"{name} must be {n} contiguous {dtype} values")
+    if dH is not None and dH.numel() != prob.T * prob.D or dE is not None and dE.numel() != prob.V * prob.D:
+        raise ValueError("dH must be [T, D] and dE [V, D]")
+
+
 def _head_size(fn: str, prob, outputs: int) -> int:
     n = _sz(0)
     _check(getattr(load_library(), fn)(ctypes.byref(prob), int(outputs), ctypes.byref(n)), fn)
@@ -525,6 +535,7 @@ def cutbce_preference_workspace_size(prob: cutbce_preference_problem, outputs: i
 
 def cutbce_distill_forward(prob, loss: Optional[torch.Tensor], lse: Optional[torch.Tensor], ws: torch.Tensor,
                            stream=None) -> None:
+    _head_outputs(prob, loss, lse)
     _check(load_library().cutbce_distill_forward(ctypes.byref(prob), _ptr(loss), _ptr(lse), ws.data_ptr(), ws.numel(),
                                                  _stream(stream)), "cutbce_distill_forward")
 
@@ -532,6 +543,7 @@ def cutbce_distill_forward(prob, loss: Optional[torch.Tensor], lse: Optional[tor
 def cutbce_distill_backward(prob, opts: Optional[cutbce_grad_options], lse: torch.Tensor,
                             grad_loss: Optional[torch.Tensor], dH: Optional[torch.Tensor],
                             dE: Optional[torch.Tensor], ws: torch.Tensor, stream=None) -> None:
+    _head_outputs(prob, None, lse, None, dH, dE)
     _check(load_library().cutbce_distill_backward(
         ctypes.byref(prob), ctypes.byref(opts) if opts is not None else None, _ptr(lse), _ptr(grad_loss), _ptr(dH),
         _ptr(dE), ws.data_ptr(), ws.numel(), _stream(stream)), "cutbce_distill_backward")
@@ -541,6 +553,7 @@ def cutbce_distill_forward_backward(prob, opts: Optional[cutbce_grad_options], g
                                     loss: Optional[torch.Tensor], lse: Optional[torch.Tensor],
                                     dH: Optional[torch.Tensor], dE: Optional[torch.Tensor], ws: torch.Tensor,
                                     stream=None) -> None:
+    _head_outputs(prob, loss, lse, None, dH, dE)
     _check(load_library().cutbce_distill_forward_backward(
         ctypes.byref(prob), ctypes.byref(opts) if opts is not None else None, _ptr(grad_loss), _ptr(loss), _ptr(lse),
         _ptr(dH), _ptr(dE), ws.data_ptr(), ws.numel(), _stream(stream)), "cutbce_distill_forward_backward")
@@ -548,6 +561,7 @@ def cutbce_distill_forward_backward(prob, opts: Optional[cutbce_grad_options], g
 
 def cutbce_preference_forward(prob, loss: Optional[torch.Tensor], logp: Optional[torch.Tensor],
                               lse: Optional[torch.Tensor], ws: torch.Tensor, stream=None) -> None:
+    _head_outputs(prob, loss, lse, logp)
     _check(load_library().cutbce_preference_forward(ctypes.byref(prob), _ptr(loss), _ptr(logp), _ptr(lse),
                                                     ws.data_ptr(), ws.numel(), _stream(stream)),
            "cutbce_preference_forward")
@@ -556,6 +570,7 @@ def cutbce_preference_forward(prob, loss: Optional[torch.Tensor], logp: Optional
 def cutbce_preference_backward(prob, opts: Optional[cutbce_grad_options], lse: torch.Tensor,
                                grad_loss: Optional[torch.Tensor], dH: Optional[torch.Tensor],
                                dE: Optional[torch.Tensor], ws: torch.Tensor, stream=None) -> None:
+    _head_outputs(prob, None, lse, None, dH, dE)
     _check(load_library().cutbce_preference_backward(
         ctypes.byref(prob), ctypes.byref(opts) if opts is not None else None, _ptr(lse), _ptr(grad_loss), _ptr(dH),
         _ptr(dE), ws.data_ptr(), ws.numel(), _stream(stream)), "cutbce_preference_backward")
@@ -565,6 +580,7 @@ def cutbce_preference_forward_backward(prob, opts: Optional[cutbce_grad_options]
                                        loss: Optional[torch.Tensor], logp: Optional[torch.Tensor],
                                        lse: Optional[torch.Tensor], dH: Optional[torch.Tensor],
                                        dE: Optional[torch.Tensor], ws: torch.Tensor, stream=None) -> None:
+    _head_outputs(prob, loss, lse, logp, dH, dE)
     _check(load_library().cutbce_preference_forward_backward(
         ctypes.byref(prob), ctypes.byref(opts) if opts is not None else None, _ptr(grad_loss), _ptr(loss), _ptr(logp),
         _ptr(lse), _ptr(dH), _ptr(dE), ws.data_ptr(), ws.numel(), _stream(stream)),

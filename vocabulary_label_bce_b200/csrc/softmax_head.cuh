@@ -539,6 +539,12 @@ __device__ __forceinline__ double head_block_sum(double v, double* red) {
   return r;
 }
 
+// A call with a data error has no loss: NaN, so that it does not pass unnoticed where
+// the status is not read.
+__device__ __forceinline__ void failed_loss(const HeadParams& p) {
+  if (p.loss != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.loss = NAN;
+}
+
 // ------------------------------------------------------------------ lse
 // Four threads per compacted row: join the (max, sum) partials of the row's splits
 // and slabs (or takes the lse of an earlier forward), writes lse, the exponent
@@ -552,7 +558,10 @@ __global__ void __launch_bounds__(kLseThreads) k_head_lse(const HeadParams p) {
   __shared__ double red[kLseThreads];
   __shared__ int last;
   HeadHeader* hdr = p.hdr;
-  if (hdr->w.status != 0) return;
+  if (hdr->w.status != 0) {
+    failed_loss(p);
+    return;
+  }
   // consecutive threads take consecutive rows, so that a slot's partials are read together
   const int part_of = static_cast<int>(threadIdx.x) / kLseRows;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * kLseRows + threadIdx.x % kLseRows;
@@ -641,7 +650,10 @@ __global__ void __launch_bounds__(kPairThreads) k_head_pairs(const HeadParams p)
   __shared__ double red[kPairThreads];
   __shared__ int last;
   HeadHeader* hdr = p.hdr;
-  if (hdr->w.status != 0) return;
+  if (hdr->w.status != 0) {
+    failed_loss(p);
+    return;
+  }
   const int pr = blockIdx.x;
   double L[2];
 #pragma unroll
