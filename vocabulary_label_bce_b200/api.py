@@ -181,21 +181,25 @@ def _as(t: Optional[torch.Tensor], dtype: torch.dtype) -> Optional[torch.Tensor]
 
 def _workspace(nbytes: int, like: torch.Tensor, given: Optional[torch.Tensor]) -> torch.Tensor:
     if given is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        return like.new_empty(nbytes, dtype=torch.uint8)
     if given.dtype != torch.uint8 or given.device != like.device or not given.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the device of the inputs")
     return given
 
 
-@_there
 def embed_forward(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, status: Optional[torch.Tensor] = None):
     """scale * E[ids] (any shape of ids; -1 gives a zero row), in E's dtype (bf16 or fp32)."""
+    _on_cuda(E)
+    if E.get_device() != _current_device():
+        with torch.cuda.device(E.device):
+            return embed_forward(E, ids, scale, status)
     if E.dim() != 2:
         raise ValueError("E must be [V, D]")
-    _on_cuda(E)
-    X = torch.empty(ids.shape + E.shape[1:], dtype=E.dtype, device=E.device)
+    E, ids = _plain(E), _ids32(ids)
+    # (a tuple of two numbers is the quickest way to an uninitialised tensor)
+    X = E.new_empty((ids.shape[0], E.shape[1]) if ids.dim() == 1 else ids.shape + E.shape[1:])
     if ids.numel() > 0:
-        B.cutbce_embed_forward(_plain(E), _ids32(ids), X, scale, status)
+        B.cutbce_embed_forward(E, ids, X, scale, status)
     return X
 
 
@@ -219,7 +223,7 @@ def embed_backward(dX: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 1
         if out is None:
             return torch.zeros((V, D), dtype=grad_dtype, device=dX.device)
         return out if accumulate else out.zero_()
-    dE = out if out is not None else torch.empty((V, D), dtype=grad_dtype, device=dX.device)
+    dE = out if out is not None else dX.new_empty((V, D), dtype=grad_dtype)
     ws = _workspace(B.cutbce_embed_workspace_size(ids.numel(), V, D), dX, workspace)
     B.cutbce_embed_backward(_plain(dX).view(-1, D), _ids32(ids), dE, ws, scale, accumulate)
     return dE
@@ -322,6 +326,12 @@ def _bits(dH, dE) -> int:
     return (B.OUT_DH if dH is not None else 0) | (B.OUT_DE if dE is not None else 0)
 
 
+def _loss_lse(H):
+    """Uninitialised loss (0-d float64) and log-sum-exps (float32, H.shape[:-1])."""
+    lse = H.new_empty(H.shape[0] if H.dim() == 2 else H.shape[:-1], dtype=torch.float32)
+    return H.new_empty((), dtype=torch.float64), lse
+
+
 def _lse_rows(lse: torch.Tensor, H: torch.Tensor) -> torch.Tensor:
     if lse.dtype != torch.float32 or lse.shape != H.shape[:-1] or lse.device != H.device:
         raise ValueError("lse must be the float32 tensor of a forward on the same inputs")
@@ -337,8 +347,7 @@ def distill_forward(H, E, teacher_ids, teacher_logits, mask=None, weights=None, 
     the teacher's top items and logits of each position; mask 1 = counts; weights a factor per position."""
     prob, keep = _distill_problem(H, E, teacher_ids, teacher_logits, mask, weights, temperature, reduction)
     ws = _workspace(B.cutbce_distill_workspace_size(prob, B.OUT_LOSS), H, workspace)
-    loss = torch.empty((), dtype=torch.float64, device=H.device)
-    lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
+    loss, lse = _loss_lse(H)
     B.cutbce_distill_forward(prob, loss, lse, ws)
     return loss, lse
 
@@ -368,8 +377,7 @@ def distill_forward_backward(H, E, teacher_ids, teacher_logits, mask=None, weigh
     prob, keep = _distill_problem(H, E, teacher_ids, teacher_logits, mask, weights, temperature, reduction)
     dH, dE, opts = _grad_outputs(H, E, want_dH, want_dE, grad_dtype, dE_out, accumulate_dE)
     ws = _workspace(B.cutbce_distill_workspace_size(prob, B.OUT_LOSS | _bits(dH, dE)), H, workspace)
-    loss = torch.empty((), dtype=torch.float64, device=H.device)
-    lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
+    loss, lse = _loss_lse(H)
     g = _scalar_grad(grad_loss, H)
     B.cutbce_distill_forward_backward(prob, opts, g, loss, lse, dH, dE, ws)
     return loss, lse, dH, dE
@@ -387,9 +395,8 @@ def preference_forward(H, E, ids, offsets=None, ref_logp=None, mask=None, beta: 
     that model's H and E), or None for 0."""
     prob, keep = _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction)
     ws = _workspace(B.cutbce_preference_workspace_size(prob, B.OUT_LOSS), H, workspace)
-    loss = torch.empty((), dtype=torch.float64, device=H.device)
-    logp = torch.empty(2 * prob.P, dtype=torch.float32, device=H.device)
-    lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
+    loss, lse = _loss_lse(H)
+    logp = H.new_empty(2 * prob.P, dtype=torch.float32)
     B.cutbce_preference_forward(prob, loss, logp, lse, ws)
     return loss, logp, lse
 
@@ -417,9 +424,8 @@ def preference_forward_backward(H, E, ids, offsets=None, ref_logp=None, mask=Non
     prob, keep = _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction)
     dH, dE, opts = _grad_outputs(H, E, want_dH, want_dE, grad_dtype, dE_out, accumulate_dE)
     ws = _workspace(B.cutbce_preference_workspace_size(prob, B.OUT_LOSS | _bits(dH, dE)), H, workspace)
-    loss = torch.empty((), dtype=torch.float64, device=H.device)
-    logp = torch.empty(2 * prob.P, dtype=torch.float32, device=H.device)
-    lse = torch.empty(H.shape[:-1], dtype=torch.float32, device=H.device)
+    loss, lse = _loss_lse(H)
+    logp = H.new_empty(2 * prob.P, dtype=torch.float32)
     g = _scalar_grad(grad_loss, H)
     B.cutbce_preference_forward_backward(prob, opts, g, loss, logp, lse, dH, dE, ws)
     return loss, logp, lse, dH, dE

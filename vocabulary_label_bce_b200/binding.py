@@ -187,7 +187,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream(stream) -> int:
     if stream is None:
-        if _raw_stream is not None and torch.cuda.is_initialized():
+        if _raw_stream is not None:
+            torch.cuda.init()
             return _raw_stream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -396,14 +397,20 @@ def _same_device(*tensors: Optional[torch.Tensor]) -> None:
 def cutbce_embed_forward(E: torch.Tensor, ids: torch.Tensor, X: torch.Tensor, scale: float = 1.0,
                          status: Optional[torch.Tensor] = None, stream=None) -> None:
     """X[n] = scale * E[ids[n]] (E [V, D] and X ids.shape + [D] bf16 or fp32, ids int32, -1 empty)."""
-    _dense(E, "E", tuple(_DTYPES))
-    _dense(ids, "ids", (torch.int32,))
-    _dense(X, "X", (E.dtype,), ids.shape + E.shape[1:])
-    _dense(status, "status", (torch.int32,))
-    _same_device(E, ids, X, status)
-    _check(load_library().cutbce_embed_forward(E.data_ptr(), E.shape[0], E.shape[1], _DTYPES[E.dtype], ids.data_ptr(),
-                                               ids.numel(), float(scale), X.data_ptr(), _ptr(status),
-                                               _stream(stream)), "cutbce_embed_forward")
+    i, dtype = E.get_device(), E.dtype
+    V, D = E.shape
+    n = ids.numel()
+    if not (dtype in _DTYPES and ids.dtype is torch.int32 and X.dtype is dtype and E.is_contiguous()
+            and ids.is_contiguous() and X.is_contiguous() and X.numel() == n * D and X.shape[-1] == D
+            and ids.get_device() == i and X.get_device() == i and status is None):
+        _dense(E, "E", tuple(_DTYPES))
+        _dense(ids, "ids", (torch.int32,))
+        _dense(X, "X", (dtype,), ids.shape + E.shape[1:])
+        _dense(status, "status", (torch.int32,))
+        _same_device(E, ids, X, status)
+    _check((_LIB or load_library()).cutbce_embed_forward(
+        E.data_ptr(), V, D, _DTYPES[dtype], ids.data_ptr(), n, scale, X.data_ptr(), _ptr(status),
+        _stream(stream)), "cutbce_embed_forward")
 
 
 def cutbce_embed_workspace_size(N: int, V: int, D: int) -> int:
