@@ -58,6 +58,8 @@ struct SoftmaxCfg {
   static constexpr int ACC_COL = kGrad ? 3 * BN : 0;
   static constexpr int S_COL = ACC_COL + DP;
   static constexpr bool S_IN_TMEM = kGrad && S_COL + DP / 2 <= 512;
+  static constexpr int ONES_COL = S_COL + DP / 2;
+  static constexpr bool ONES_IN_TMEM = OFF_MMA && S_IN_TMEM && ONES_COL + 8 <= 512;
   static constexpr int NUM_BARS = 2 + 2 * NX + 3 * NZ + 3 + GROUPS;
   static constexpr uint32_t SMEM_BYTES = 1024 + S_BYTES + NX * (X_BYTES + O_BYTES) + ONES_BYTES + NUM_BARS * 8 + 16 + 64;
   static_assert((!kGrad || ACC_COL + DP <= 512) && NZ * BN <= 512, "TMEM budget");
@@ -296,6 +298,10 @@ __global__ void __launch_bounds__(SoftmaxCfg<DP, kPass>::THREADS, 1)
     const uint32_t tS = tmem_base + Cfg::S_COL;
     uint32_t ic = 0, c = 0, st = 0, ph = 0, zb = 0, zph = 0;
     bool ok = true;
+    if (Cfg::ONES_IN_TMEM) {
+      if (elect_one()) tmem_cp_128x256b(tmem_base + Cfg::ONES_COL, dOne);
+      __syncwarp();
+    }
     for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x, ++ic) {
       int row0, x0, nx, split;
       item(i, row0, x0, nx, split);
@@ -327,7 +333,8 @@ __global__ void __launch_bounds__(SoftmaxCfg<DP, kPass>::THREADS, 1)
             else umma_bf16(tD, dS + static_cast<uint32_t>((ks >> 2) * (kTileM * 8) + (ks & 3) * 2), bd, idesc_z,
                            ks > 0 ? 1u : 0u);
           }
-          if (Cfg::OFF_MMA) umma_bf16(tD, dOne, dO + st * (Cfg::O_BYTES >> 4), idesc_z, 1u);
+          if (Cfg::ONES_IN_TMEM) umma_bf16_tmem_a(tD, tmem_base + Cfg::ONES_COL, dO + st * (Cfg::O_BYTES >> 4), idesc_z, 1u);
+          else if (Cfg::OFF_MMA) umma_bf16(tD, dOne, dO + st * (Cfg::O_BYTES >> 4), idesc_z, 1u);
           umma_commit(bar_zfull + zb);
           if (!kGrad) umma_commit(bar_xempty + st);
           if (!Cfg::S_IN_TMEM && j + 1 == nx) umma_commit(bar_sempty);
