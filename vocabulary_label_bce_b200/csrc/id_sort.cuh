@@ -16,6 +16,13 @@
 // sub-chunks is joined in shared memory, in order; one that crosses blocks leaves
 // one partial per block, and k_segment_join adds those (eight interleaved running
 // sums, then a fixed order).  Hot ids neither serialise nor need atomics.
+//
+// Measured, ids drawn from Zipf laws: N = 12,800, V = 876,000, D = 64 bf16: sort 22 us
+// beside the 112 MB of zeros (17 us at the measured copy rate), sums 8.6, join 2.8.
+// N = 200,003, V = 100,000, D = 200 fp32: keys beside 80 MB of zeros 16 us, two passes
+// 31, sums 48 (160 MB read, 3.5 TB/s: several waves of blocks whose rows are 800 random
+// bytes each), join 10.  The sorts are bound by latency: a few dozen blocks, each a
+// chain of loads, counts and scattered stores.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -280,7 +287,8 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const int* __rest
 // eight CTAs, whose warps own consecutive entries (held in registers over a pass).
 // The CTAs read each other's digit totals from shared memory; the pairs of a pass go
 // through L2.  No launch, histogram or clearing between the passes: 12,800 entries
-// of 20-bit ids take 9 us against 20 us for the kernels above.  ids as there;
+// of 20-bit ids take 18 us with one launch, the kernels above 19 us with four; at
+// 51,200 entries it is 35 against 23.  ids as there;
 // `clear_status`: the status starts here, and bad ids set it.  Clusters past the
 // first fill.
 constexpr int kClusterCtas = 8;

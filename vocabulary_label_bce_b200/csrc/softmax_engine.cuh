@@ -18,8 +18,26 @@
 //          the negate-A bit of the contraction's instruction descriptor.
 //
 // c = log2(e) / tau.  Warp roles, tensor-memory layout and hand-over of the tiles
-// follow the BCE engine: warp 0 loads by TMA, warp 1 issues the MMAs, 16 epilogue
-// warps in two groups take alternate tiles.  Every wait is bounded.
+// follow the BCE engine (warp 0 loads by TMA, 16 epilogue warps in two groups take
+// alternate tiles), with one difference: the logit MMAs and the contractions are
+// issued by two warps with blocking waits instead of one that polls for both.  With
+// no element math at all the dH pass then takes 1.39 ms instead of 2.5 at 9.0e9 logits
+// and D = 64.  Every wait is bounded.
+//
+// What bounds it, at T = 12,800 positions (10,240 count), V = 876,000, D = 64:
+//   kLse   2.01 ms.  One exponential per logit: 1.37 ms of SFU time with 5 of 16 on
+//          the FMA pipe, which the maximum and the polynomial then share with the
+//          sums.  256-item tiles: the hand-over alone takes 0.65 ms, with 128-item
+//          tiles 1.08.
+//   kRows  2.15 ms and kItems 2.09 ms alone, about 2.4 each in a loop of whole steps,
+//          where the card holds its power limit (sw_power_cap).  The MMAs take 1.4 and
+//          1.6 ms (the D = 64 contraction runs at two thirds of the tensor rate), the
+//          exponentials 1.4 of SFU time; three logit buffers are all that fits beside
+//          the accumulator.  Tried and no better: 64-item tiles with six buffers (2.27 /
+//          2.28 ms), one or three epilogue groups, one arrival per warp.
+//   D = 256, T = 8,192 (7,376 count), V = 1,000,000: kRows 5.6 ms, 1,360 TFLOP/s of its
+//          two products, against 1,404 that a library bf16 product sustains on this
+//          card.  Bound by the tensor cores under the power limit.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>

