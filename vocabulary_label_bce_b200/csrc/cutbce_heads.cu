@@ -317,7 +317,7 @@ void plan_head(const HeadProblem& p, bool dH, bool dE, bool lse_pass, HeadPlan& 
   pl.o_lse2 = l.take(4 * Tc);
   pl.o_term = l.take(8 * Tc);
   pl.o_hc = l.take(2 * Tc * pl.DP);
-  pl.o_lpart = l.take(8 * std::max<size_t>(static_cast<size_t>(p.P), Tc / kLseRows));
+  pl.o_lpart = l.take(8 * std::max<size_t>(static_cast<size_t>(p.P), Tc * 32 / kLseThreads));
   pl.o_part = lse_pass ? l.take(8 * static_cast<size_t>(pl.fused ? pl.S : pl.S_lse) * kHeadSlots * Tc) : 0;
   pl.o_wide = pl.fused ? l.take(8 * static_cast<size_t>(pl.S_lse) * kHeadSlots * Tc) : 0;
   pl.o_m2 = pl.fused ? l.take(4 * Tc) : 0;
@@ -504,7 +504,8 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   }
   {
     LaunchScope ls(CUTBCE_KERNEL_HEAD_FINISH, st);
-    k_head_lse<<<static_cast<unsigned>(pl.Tc / kLseRows), kLseThreads, 0, st>>>(hp);
+    if (lse_in == nullptr && hp.slots > kLseManySlots) k_head_lse<32><<<static_cast<unsigned>(pl.Tc * 32 / kLseThreads), kLseThreads, 0, st>>>(hp);
+    else k_head_lse<4><<<static_cast<unsigned>(pl.Tc * 4 / kLseThreads), kLseThreads, 0, st>>>(hp);
     if (p.kind == kHeadPreference) k_head_pairs<<<static_cast<unsigned>(p.P), kPairThreads, 0, st>>>(hp);
     CUTBCE_CK(cudaGetLastError());
   }
@@ -529,7 +530,9 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
     dp.accumulate = (out.accumulate & CUTBCE_ACCUMULATE_DH) != 0;
     dp.hdr = hp.hdr;
     LaunchScope ls(CUTBCE_KERNEL_HEAD_FINISH, st);
-    k_head_dh<<<static_cast<unsigned>(ceil_div(p.T * (p.D / 4), 256)), 256, 0, st>>>(dp);
+    const int64_t groups = p.T * (p.D / 4);
+    if (groups < 148 * 512) k_head_dh<8><<<static_cast<unsigned>(ceil_div(groups, 32)), 256, 0, st>>>(dp);
+    else k_head_dh<1><<<static_cast<unsigned>(ceil_div(groups, 256)), 256, 0, st>>>(dp);
     CUTBCE_CK(cudaGetLastError());
   }
   if (dE) {

@@ -552,43 +552,43 @@ __global__ void __launch_bounds__(SoftmaxCfg<DP, kPass>::THREADS, 1)
               *reinterpret_cast<float4*>(dst + e) = make_float4(__uint_as_float(r[e]), __uint_as_float(r[e + 1]),
                                                                 __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
           } else if (v < p.V) {
+            // eight columns at a time (D is a multiple of 8): 16-byte stores in either dtype
             const int64_t o = static_cast<int64_t>(v) * p.D + col0;
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
+            for (int e = 0; e < 16; e += 8) {
               if (col0 + e >= p.D) continue;
-              float4 g = make_float4(__uint_as_float(r[e]), __uint_as_float(r[e + 1]), __uint_as_float(r[e + 2]),
-                                     __uint_as_float(r[e + 3]));
+              float g[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) g[k] = __uint_as_float(r[e + k]);
               if (sp >= 0) {
-                const float4 s4 = __ldg(reinterpret_cast<const float4*>(p.sparse + sp * p.D + col0 + e));
-                g.x -= s4.x;
-                g.y -= s4.y;
-                g.z -= s4.z;
-                g.w -= s4.w;
+                const float4* s4 = reinterpret_cast<const float4*>(p.sparse + sp * p.D + col0 + e);
+                const float4 lo = __ldg(s4), hi = __ldg(s4 + 1);
+                g[0] -= lo.x, g[1] -= lo.y, g[2] -= lo.z, g[3] -= lo.w;
+                g[4] -= hi.x, g[5] -= hi.y, g[6] -= hi.z, g[7] -= hi.w;
               }
-              g.x = __fmul_rn(g.x, gs);
-              g.y = __fmul_rn(g.y, gs);
-              g.z = __fmul_rn(g.z, gs);
-              g.w = __fmul_rn(g.w, gs);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) g[k] = __fmul_rn(g[k], gs);
               if (p.de_bf16) {
-                uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.dE) + o + e);
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dE) + o + e);
                 if (p.de_acc) {
-                  const uint2 old = *dst;
-                  g.x = __fadd_rn(g.x, __uint_as_float(old.x << 16));
-                  g.y = __fadd_rn(g.y, __uint_as_float(old.x & 0xFFFF0000u));
-                  g.z = __fadd_rn(g.z, __uint_as_float(old.y << 16));
-                  g.w = __fadd_rn(g.w, __uint_as_float(old.y & 0xFFFF0000u));
+                  float old[8];
+                  unpack8(*dst, old);
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) g[k] = __fadd_rn(g[k], old[k]);
                 }
-                *dst = make_uint2(pack_bf16x2(g.x, g.y), pack_bf16x2(g.z, g.w));
+                *dst = make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4], g[5]),
+                                  pack_bf16x2(g[6], g[7]));
               } else {
                 float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.dE) + o + e);
                 if (p.de_acc) {
-                  const float4 old = *dst;
-                  g.x = __fadd_rn(g.x, old.x);
-                  g.y = __fadd_rn(g.y, old.y);
-                  g.z = __fadd_rn(g.z, old.z);
-                  g.w = __fadd_rn(g.w, old.w);
+                  const float4 lo = dst[0], hi = dst[1];
+                  g[0] = __fadd_rn(g[0], lo.x), g[1] = __fadd_rn(g[1], lo.y);
+                  g[2] = __fadd_rn(g[2], lo.z), g[3] = __fadd_rn(g[3], lo.w);
+                  g[4] = __fadd_rn(g[4], hi.x), g[5] = __fadd_rn(g[5], hi.y);
+                  g[6] = __fadd_rn(g[6], hi.z), g[7] = __fadd_rn(g[7], hi.w);
                 }
-                *dst = g;
+                dst[0] = make_float4(g[0], g[1], g[2], g[3]);
+                dst[1] = make_float4(g[4], g[5], g[6], g[7]);
               }
             }
           }

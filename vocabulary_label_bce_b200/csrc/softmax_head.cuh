@@ -551,15 +551,19 @@ __device__ __forceinline__ void failed_loss(const HeadParams& p) {
 }
 
 // ------------------------------------------------------------------ lse
-// Four threads per compacted row: join the (max, sum) partials of the row's splits
+// Several threads per compacted row join the (max, sum) partials of the row's splits
 // and slabs (or takes the lse of an earlier forward), writes lse, the exponent
 // offset of the item-owned pass and the row's share of the distillation loss,
 // which the last block adds up in block order.
+//
+// kLseLanes threads share a row: 4, or 32 where a row has more than 128 partials (few
+// positions, many splits: 14 us with 592 partials and 4 threads).
 constexpr int kLseThreads = 128;
-constexpr int kLseLanes = 4;                      // lanes that share a row's partials
-constexpr int kLseRows = kLseThreads / kLseLanes;
+constexpr int kLseManySlots = 128;
 
+template <int kLseLanes>
 __global__ void __launch_bounds__(kLseThreads) k_head_lse(const HeadParams p) {
+  constexpr int kLseRows = kLseThreads / kLseLanes;
   __shared__ double red[kLseThreads];
   __shared__ int last;
   HeadHeader* hdr = p.hdr;
@@ -721,24 +725,32 @@ struct HeadDhParams {
   const HeadHeader* hdr;
 };
 
+// kLanes threads share four columns and add every kLanes-th split, their sums are
+// then added in order: 1, or 8 where the positions alone leave SMs idle (131 splits of
+// 9 rows took 30 us with one thread each).
+template <int kLanes>
 __global__ void __launch_bounds__(256) k_head_dh(const HeadDhParams p) {
   if (p.hdr->w.status != 0) return;
+  constexpr int kCols = 256 / kLanes;             // groups of four columns per block
+  __shared__ float4 s_part[kLanes > 1 ? kLanes : 1][kLanes > 1 ? kCols : 1];
+  const int part_of = kLanes > 1 ? static_cast<int>(threadIdx.x) / kCols : 0;
   const int per_row = p.D / 4;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kCols + threadIdx.x % kCols;
   const int64_t t = i / per_row;
-  if (t >= p.T) return;
   const int col = static_cast<int>(i - t * per_row) * 4;
-  const int c = p.cidx[t];
+  const int c = t < p.T ? p.cidx[t] : -1;
   float4 g = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   if (c >= 0) {
     const float* src = p.part + static_cast<int64_t>(c) * p.DP + col;
     const int64_t stride = p.Tc * p.DP;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < p.S; s0 += 8) {                     // eight loads in flight, added in split order
+    for (int s0 = part_of; s0 < p.S; s0 += 8 * kLanes) {      // eight loads in flight, added in split order
       float4 v[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        v[u] = s0 + u < p.S ? __ldg(reinterpret_cast<const float4*>(src + (s0 + u) * stride)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int u = 0; u < 8; ++u) {
+        const int s = s0 + u * kLanes;
+        v[u] = s < p.S ? __ldg(reinterpret_cast<const float4*>(src + s * stride)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         a.x += v[u].x;
@@ -747,6 +759,22 @@ __global__ void __launch_bounds__(256) k_head_dh(const HeadDhParams p) {
         a.w += v[u].w;
       }
     }
+  }
+  if (kLanes > 1) {
+    s_part[part_of][threadIdx.x % kCols] = a;
+    __syncthreads();
+    if (part_of != 0) return;
+#pragma unroll
+    for (int q = 1; q < kLanes; ++q) {
+      const float4 v = s_part[q][threadIdx.x % kCols];
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
+    }
+  }
+  if (t >= p.T) return;
+  if (c >= 0) {
     const float4 q = __ldg(reinterpret_cast<const float4*>(p.sparse + static_cast<int64_t>(c) * p.DP + col));
     const float f = p.hdr->w.grad_scale * p.coef[t];
     const float r = p.rescale[c];
