@@ -409,7 +409,7 @@ def cutbce_embed_forward(E: torch.Tensor, ids: torch.Tensor, X: torch.Tensor, sc
         _dense(status, "status", (torch.int32,))
         _same_device(E, ids, X, status)
     _check((_LIB or load_library()).cutbce_embed_forward(
-        E.data_ptr(), V, D, _DTYPES[dtype], ids.data_ptr(), n, scale, X.data_ptr(), _ptr(status),
+        E.data_ptr(), V, D, _DTYPES[dtype], ids.data_ptr(), n, float(scale), X.data_ptr(), _ptr(status),
         _stream(stream)), "cutbce_embed_forward")
 
 

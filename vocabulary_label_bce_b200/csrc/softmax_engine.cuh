@@ -144,6 +144,13 @@ __device__ __forceinline__ float2 exp2_pair(int pair, float2 x) {
   return f2(ex2_approx(x.x), ex2_approx(x.y));
 }
 
+// The largest of three (one instruction; NaN is passed over).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // 32 logits of one row -> their exponentials.  kTail: columns from `valid` on are
 // outside the table and count as -infinity.
 __device__ __forceinline__ void mask_tail(uint32_t (&r)[32], int valid) {
@@ -480,9 +487,9 @@ __global__ void __launch_bounds__(SoftmaxCfg<DP, kPass>::THREADS, 1)
               mx4[k] = fmaxf(__uint_as_float(r[8 * k]), __uint_as_float(r[8 * k + 1]));
 #pragma unroll
               for (int e = 2; e < 8; e += 2)
-                mx4[k] = fmaxf(mx4[k], fmaxf(__uint_as_float(r[8 * k + e]), __uint_as_float(r[8 * k + e + 1])));
+                mx4[k] = max3(mx4[k], __uint_as_float(r[8 * k + e]), __uint_as_float(r[8 * k + e + 1]));
             }
-            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.c2;
+            const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]) * p.c2;
             // the reference moves only when the maximum has grown by 2^8: sums stay far from overflow
             const float mn = mx > m + 8.f ? mx : m;
             sum *= ex2_approx(m - mn);
