@@ -319,7 +319,7 @@ cutbce_status cutbce_embed_forward(const void* E, int64_t V, int64_t D, int32_t 
  * and that is rounded).  accumulate = 1 with the dE of a loss gives the gradient
  * of a table that is both the model's input and its output.  A bad id sets the
  * workspace status word (cutbce_read_status); dE is then unspecified.
- * ws: cutbce_embed_workspace_size bytes (about 16 N + N D / 2), 256-byte aligned. */
+ * ws: cutbce_embed_workspace_size bytes (16 to 42 N, and N D / 2), 256-byte aligned. */
 cutbce_status cutbce_embed_workspace_size(int64_t N, int64_t V, int64_t D, size_t* bytes);
 cutbce_status cutbce_embed_backward(const void* dX, int32_t dtype, const int32_t* ids, int64_t N, int64_t V, int64_t D,
                                     float scale, void* dE, int32_t grad_dtype, int32_t accumulate, void* ws,

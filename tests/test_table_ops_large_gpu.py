@@ -89,3 +89,22 @@ def test_lookup_and_its_gradient(table):
     assert ((dE[rows].double() - want).abs() <= U * (n[:, None] + 2) * size + U * want.abs()).all()
     dE[rows] = 0
     assert not any(dE[v:v + PIECE].any() for v in range(0, V, PIECE))
+
+
+@pytest.mark.parametrize("V", [1, 900, 40_000, 5_000_000])
+@pytest.mark.parametrize("N", [16_384, 16_385, 131_072, 131_073, 262_145, 1_000_003, 4_194_305])
+def test_many_entries(N, V):
+    """Sizes at which the sort takes another form.  A sum of fp32 terms is off by at most u times its
+    longest chain of additions, of the sum of their sizes; the chains here are far shorter than
+    N / 64 + 4096."""
+    g = torch.Generator(device="cuda").manual_seed(43)
+    ids = (torch.rand(N, device="cuda", generator=g) ** 3 * V).int()
+    ids[::17] = -1
+    dX = torch.randn(N, 8, device="cuda", generator=g)
+    dE = api.embed_backward(dX, ids, V, out=torch.full((V, 8), float("nan"), device="cuda"))
+    real = ids >= 0
+    rows = ids[real].long()
+    want = torch.zeros(V, 8, dtype=torch.float64, device="cuda").index_add_(0, rows, dX[real].double())
+    size = torch.zeros(V, 8, dtype=torch.float64, device="cuda").index_add_(0, rows, dX[real].double().abs())
+    assert ((dE.double() - want).abs() <= U * (N / 64 + 4096) * size).all()
+    assert torch.equal(dE, api.embed_backward(dX, ids, V))

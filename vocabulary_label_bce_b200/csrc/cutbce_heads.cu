@@ -89,16 +89,19 @@ cutbce_status run_sort_ipt(const SortBuffers& b, const int32_t* ids, int V, void
   const size_t pass_hist = static_cast<size_t>(sp.nblk) << sp.bits;
   int* hist = at<int>(ws, b.o_hist);
   int* total = at<int>(ws, b.o_total);
-  const int fill_blocks = static_cast<int>(std::min<int64_t>(ceil_div(fill.n, 4 * kSortThreads), 8 * 148));
-  k_sort_keys<IPT><<<sp.nblk + fill_blocks, kSortThreads, 0, st>>>(ids, sp.N, V, sp.bits, hist, status, sp.nblk, fill);
+  // the passes take equal shares of the fill: they last longer than the counting of the keys
+  const int64_t share = ceil_div(fill.n, sp.passes);
+  k_sort_keys<IPT><<<sp.nblk, kSortThreads, 0, st>>>(ids, sp.N, V, sp.bits, hist, status);
   const int2* in = nullptr;
   for (int p = 0; p < sp.passes; ++p) {
     int* h = hist + p * pass_hist;
     int* next = p + 1 < sp.passes ? h + pass_hist : nullptr;
-    if (sp.scan) k_sort_scan<<<static_cast<unsigned>(ceil_div(1 << sp.bits, 128)), 128, 0, st>>>(h, total, 1 << sp.bits, sp.nblk);
+    if (sp.scan) k_sort_scan<<<static_cast<unsigned>(ceil_div(1 << sp.bits, 32)), 32 * kScanWarps, 0, st>>>(h, total, 1 << sp.bits, sp.nblk);
     int2* out = at<int2>(ws, b.o_pairs[p & 1]);
-    k_sort_scatter<IPT><<<sp.nblk, kSortThreads, 0, st>>>(p == 0 ? ids : nullptr, in, sp.N, V, p * sp.bits, sp.bits, sp.nblk,
-                                                          h, sp.scan ? total : nullptr, out, next, status);
+    const FillJob part{fill.dst + p * share, std::max<int64_t>(0, std::min(share, fill.n - p * share)), fill.value};
+    const int fill_blocks = static_cast<int>(std::min<int64_t>(ceil_div(part.n, 4 * kSortThreads), 8 * 148));
+    k_sort_scatter<IPT><<<sp.nblk + fill_blocks, kSortThreads, 0, st>>>(p == 0 ? ids : nullptr, in, sp.N, V, p * sp.bits, sp.bits, sp.nblk,
+                                                          h, sp.scan ? total : nullptr, out, next, status, part);
     in = out;
   }
   *pairs = in;
@@ -122,8 +125,8 @@ cutbce_status run_sort(const SortBuffers& b, const int32_t* ids, int V, void* ws
     return cudaGetLastError() == cudaSuccess ? CUTBCE_OK : CUTBCE_ERR_CUDA;
   }
   if (b.sp.ipt == 4) return run_sort_ipt<4>(b, ids, V, ws, status, fill, st, pairs);
-  if (b.sp.ipt == 16) return run_sort_ipt<16>(b, ids, V, ws, status, fill, st, pairs);
-  return run_sort_ipt<64>(b, ids, V, ws, status, fill, st, pairs);
+  if (b.sp.ipt == 8) return run_sort_ipt<8>(b, ids, V, ws, status, fill, st, pairs);
+  return run_sort_ipt<16>(b, ids, V, ws, status, fill, st, pairs);
 }
 
 template <int VEC, typename TIn, typename TOut>

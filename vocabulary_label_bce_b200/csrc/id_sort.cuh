@@ -3,15 +3,16 @@
 // target part of the softmax losses).
 //
 // Sort: LSD over at most 11 bits a pass, so V up to 2047 takes one pass and V up
-// to 4 M two.  Up to 16,384 entries it is one kernel (k_sort_cluster); beyond, a block owns a tile of consecutive entries; each warp ranks a
-// contiguous part of it with match_any and 16-bit counters in shared memory, so
-// equal ids keep entry order.  Every scatter block forms its own offsets from the
+// to 4 M two.  Up to 16,384 entries it is one kernel (k_sort_cluster); beyond, a block
+// owns a tile of consecutive entries; each warp ranks a contiguous part of it with
+// match_any and 16-bit counters in shared memory, so equal ids keep entry order.
+// Every scatter block forms its own offsets from the
 // tile histograms (they sit in L2), and the scatter of one pass counts the
 // histogram of the next with integer atomics, whose order changes nothing.
 // An entry without a row (an empty id) has the key V and sorts to the end.
 //
 // Sums: a block takes a chunk of consecutive sorted entries, cut into sub-chunks;
-// the lanes of a row add the rows of their sub-chunk in order, eight in flight.  A
+// the lanes of a row add the rows of their sub-chunk in order, four in flight.  A
 // segment (equal ids) inside a sub-chunk is written at once; one that crosses
 // sub-chunks is joined in shared memory, in order; one that crosses blocks leaves
 // one partial per block, and k_segment_join adds those (eight interleaved running
@@ -19,9 +20,9 @@
 //
 // Measured, ids drawn from Zipf laws: N = 12,800, V = 876,000, D = 64 bf16: sort 22 us
 // beside the 112 MB of zeros (17 us at the measured copy rate), sums 8.6, join 2.8.
-// N = 200,003, V = 100,000, D = 200 fp32: keys beside 80 MB of zeros 16 us, two passes
-// 31, sums 48 (160 MB read, 3.5 TB/s: several waves of blocks whose rows are 800 random
-// bytes each), join 10.  The sorts are bound by latency: a few dozen blocks, each a
+// N = 200,003, V = 100,000, D = 200 fp32: keys 6 us, two passes beside 80 MB of zeros
+// 24, sums 48 (160 MB read, 3.5 TB/s: several waves of blocks whose rows are 800 random
+// bytes each), join 9.  The sorts are bound by latency: a few dozen blocks, each a
 // chain of loads, counts and scattered stores.
 #pragma once
 #include <cuda_bf16.h>
@@ -52,8 +53,11 @@ inline void make_sort_plan(int64_t N, int64_t V, SortPlan& s) {
   s.passes = (bits + kSortMaxBits - 1) / kSortMaxBits;
   s.bits = (bits + s.passes - 1) / s.passes;
   if (s.bits < 2) s.bits = 2;                 // a thread of the scatter holds four digits
-  // tiles of 1024 entries while a scatter block can read all histograms cheaply, then 4096, then 16384
-  s.ipt = N <= 65536 ? 4 : N <= 1048576 ? 16 : 64;
+  // Tiles of 1024, 2048 or 4096 entries; past 128 tiles their histograms are scanned.
+  // Lookup gradients over 40,000 ids, D = 8, for 4 / 8 / 16 entries a thread: 100,000
+  // entries 45 / 48 / - us, 200,003 53 / 51 / 54, 1,000,000 111 / 107 / 104, 10,000,000
+  // 739 / 639 / 628 (and half the histograms' memory).
+  s.ipt = N <= 131072 ? 4 : N <= 4194304 ? 8 : 16;
   s.nblk = static_cast<int>(ceil_div(N, int64_t(kSortThreads) * s.ipt));
   s.scan = s.nblk > 128;
   s.hist_bytes = sizeof(int) * static_cast<size_t>(s.passes) * s.nblk * (size_t(1) << s.bits);
@@ -79,16 +83,11 @@ __device__ __forceinline__ void fill_words(const FillJob& f, int64_t block, int6
 }
 
 // Keys from plain ids (lookup gradient): -1 is an empty entry, any other id outside
-// [0, V) sets the status.  Counts the first pass's histogram.  Blocks from nblk on fill.
+// [0, V) sets the status.  Counts the first pass's histogram.
 template <int IPT>
 __global__ void __launch_bounds__(kSortThreads) k_sort_keys(const int32_t* __restrict__ ids, int64_t N, int V,
-                                                            int bits, int* __restrict__ hist, int* status, int nblk,
-                                                            FillJob fill) {
+                                                            int bits, int* __restrict__ hist, int* status) {
   __shared__ int h[kSortMaxBins];
-  if (static_cast<int>(blockIdx.x) >= nblk) {
-    fill_words(fill, static_cast<int>(blockIdx.x) - nblk, static_cast<int>(gridDim.x) - nblk);
-    return;
-  }
   const int bins = 1 << bits;
   for (int d = threadIdx.x; d < bins; d += kSortThreads) h[d] = 0;
   __syncthreads();
@@ -109,74 +108,113 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_keys(const int32_t* __res
 
 // Many tiles (more than 128): hist becomes each digit's exclusive prefix over the
 // tiles, and total its sum, so that a scatter block reads two rows instead of all.
-__global__ void __launch_bounds__(128) k_sort_scan(int* __restrict__ hist, int* __restrict__ total, int bins, int nblk) {
-  const int d = blockIdx.x * 128 + threadIdx.x;
-  if (d >= bins) return;
-  int run = 0;
-  int b = 0;
-  for (; b + 8 <= nblk; b += 8) {
-    int v[8];
+// A block has 32 digits; its warps take consecutive shares of the tiles.
+constexpr int kScanWarps = 16;
+__global__ void __launch_bounds__(32 * kScanWarps) k_sort_scan(int* __restrict__ hist, int* __restrict__ total, int bins,
+                                                               int nblk) {
+  __shared__ int s_sum[kScanWarps][32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int d = blockIdx.x * 32 + lane;
+  const int per = (nblk + kScanWarps - 1) / kScanWarps;
+  const int b0 = min(nblk, w * per), b1 = d < bins ? min(nblk, b0 + per) : b0;
+  // the counts of this share's tiles, eight in flight
+  auto walk = [&](auto each) {
+    for (int b = b0; b < b1; b += 8) {
+      int v[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = hist[static_cast<int64_t>(b + u) * bins + d];
+      for (int u = 0; u < 8; ++u) v[u] = b + u < b1 ? hist[static_cast<int64_t>(b + u) * bins + d] : 0;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      hist[static_cast<int64_t>(b + u) * bins + d] = run;
-      run += v[u];
+      for (int u = 0; u < 8; ++u) each(b + u, v[u]);
     }
-  }
-  for (; b < nblk; ++b) {
-    const int v = hist[static_cast<int64_t>(b) * bins + d];
-    hist[static_cast<int64_t>(b) * bins + d] = run;
+  };
+  int own = 0;
+  walk([&](int, int v) { own += v; });
+  s_sum[w][lane] = own;
+  __syncthreads();
+  int run = 0;
+#pragma unroll
+  for (int k = 0; k < kScanWarps; ++k) run += k < w ? s_sum[k][lane] : 0;
+  if (w == kScanWarps - 1 && d < bins) total[d] = run + own;
+  walk([&](int b, int v) {
+    if (b < b1) hist[static_cast<int64_t>(b) * bins + d] = run;
     run += v;
-  }
-  total[d] = run;
+  });
 }
 
 // One pass over (id, entry index) pairs.  ids (first pass, else null): the plain ids,
 // empty and out-of-range ones counting as V, the index being the entry's own.
-// hist_next (null in the last pass): the next
-// pass's histogram, cleared before the call.
+// hist_next (null in the last pass): the next pass's histogram, cleared before the
+// call.  Blocks from nblk on fill.
+// The bound of two blocks an SM leaves registers for the histogram loads in flight:
+// without it the compiler holds fewer (two passes over 51,200 entries 20.7 us, with
+// it 13.7; over 200,003 29.0 and 24.5).
 template <int IPT>
-__global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const int* __restrict__ ids,
+__global__ void __launch_bounds__(kSortThreads, 2) k_sort_scatter(const int* __restrict__ ids,
                                                                const int2* __restrict__ in, int64_t N, int V,
                                                                int shift, int bits, int nblk,
                                                                const int* __restrict__ hist,
                                                                const int* __restrict__ digit_total,
                                                                int2* __restrict__ out, int* __restrict__ hist_next,
-                                                               const int* __restrict__ status) {
+                                                               const int* __restrict__ status, FillJob fill) {
   __shared__ uint16_t cnt[kSortWarps][kSortMaxBins];
   __shared__ int off[kSortMaxBins];
   __shared__ int wsum[kSortWarps];
+  if (static_cast<int>(blockIdx.x) >= nblk) {
+    fill_words(fill, static_cast<int>(blockIdx.x) - nblk, static_cast<int>(gridDim.x) - nblk);
+    return;
+  }
   const int failed = *status;                       // looked at before anything is written
   const int bins = 1 << bits, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // offset of (digit, this tile): all smaller digits, then this digit in earlier
   // tiles.  A thread holds four consecutive digits (of each 1024), sixteen tiles'
-  // histograms in flight.
+  // histograms in flight; with fewer than 1024 digits, groups of threads share the tiles.
+  const int quads = min(bins / 4, kSortThreads), groups = kSortThreads / quads;
+  int* s_total = reinterpret_cast<int*>(&cnt[0][0]);
   int carry = 0;
   for (int h0 = 0; h0 < bins; h0 += 4 * kSortThreads) {
     const int d0 = h0 + 4 * tid;
     int before[4] = {0, 0, 0, 0}, total[4] = {0, 0, 0, 0};
-    if (d0 < bins) {
-      const int4* src = reinterpret_cast<const int4*>(hist + d0);
+    auto add_tiles = [&](int d, int first, int stride) {
+      const int4* src = reinterpret_cast<const int4*>(hist + d);
       const int step = bins / 4;
-      if (digit_total != nullptr) {
-        const int4 v = src[static_cast<int64_t>(blockIdx.x) * step], t = *reinterpret_cast<const int4*>(digit_total + d0);
+      constexpr int kTiles = 16;                        // tiles in flight; the last group is guarded, not looped
+      for (int b0 = first * kTiles; b0 < nblk; b0 += stride * kTiles) {
+        int4 v[kTiles];
+#pragma unroll
+        for (int u = 0; u < kTiles; ++u)
+          v[u] = b0 + u < nblk ? __ldg(src + static_cast<int64_t>(b0 + u) * step) : make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < kTiles; ++u) {
+          const int keep = b0 + u < static_cast<int>(blockIdx.x) ? -1 : 0;
+          total[0] += v[u].x, total[1] += v[u].y, total[2] += v[u].z, total[3] += v[u].w;
+          before[0] += v[u].x & keep, before[1] += v[u].y & keep, before[2] += v[u].z & keep, before[3] += v[u].w & keep;
+        }
+      }
+    };
+    if (digit_total != nullptr) {
+      if (d0 < bins) {
+        const int4 v = *reinterpret_cast<const int4*>(hist + static_cast<int64_t>(blockIdx.x) * bins + d0);
+        const int4 t = *reinterpret_cast<const int4*>(digit_total + d0);
         before[0] = v.x, before[1] = v.y, before[2] = v.z, before[3] = v.w;
         total[0] = t.x, total[1] = t.y, total[2] = t.z, total[3] = t.w;
-      } else {
-        constexpr int kTiles = 16;                      // tiles in flight; the last group is guarded, not looped
-        for (int b0 = 0; b0 < nblk; b0 += kTiles) {
-          int4 v[kTiles];
+      }
+    } else if (groups == 1) {
+      if (d0 < bins) add_tiles(d0, 0, 1);
+    } else {
+      for (int d = tid; d < bins; d += kSortThreads) off[d] = s_total[d] = 0;
+      __syncthreads();
+      const int d = 4 * (tid & (quads - 1));
+      add_tiles(d, tid / quads, groups);
 #pragma unroll
-          for (int u = 0; u < kTiles; ++u)
-            v[u] = b0 + u < nblk ? __ldg(src + static_cast<int64_t>(b0 + u) * step) : make_int4(0, 0, 0, 0);
+      for (int k = 0; k < 4; ++k) {
+        atomicAdd(off + d + k, before[k]);
+        atomicAdd(s_total + d + k, total[k]);
+      }
+      __syncthreads();
 #pragma unroll
-          for (int u = 0; u < kTiles; ++u) {
-            const int keep = b0 + u < static_cast<int>(blockIdx.x) ? -1 : 0;
-            total[0] += v[u].x, total[1] += v[u].y, total[2] += v[u].z, total[3] += v[u].w;
-            before[0] += v[u].x & keep, before[1] += v[u].y & keep, before[2] += v[u].z & keep, before[3] += v[u].w & keep;
-          }
-        }
+      for (int k = 0; k < 4; ++k) {
+        before[k] = d0 < bins ? off[d0 + k] : 0;
+        total[k] = d0 < bins ? s_total[d0 + k] : 0;
       }
     }
     const int sum = total[0] + total[1] + total[2] + total[3];
@@ -208,42 +246,28 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const int* __rest
   // ranks: warp w owns entries [w * 32 * IPT, (w + 1) * 32 * IPT) of the tile, 32 at a time
   const int64_t wbase = static_cast<int64_t>(blockIdx.x) * kSortThreads * IPT + static_cast<int64_t>(warp) * 32 * IPT;
   const unsigned lt = (1u << lane) - 1u;
-  constexpr int KEEP = IPT <= 16 ? IPT : 1;       // ranks kept in registers, or formed again below
-  int2 key[KEEP];
-  int rank[KEEP];
+  int2 key[IPT];
+  int rank[IPT];
   auto load_pair = [&](int64_t i) {
     if (ids == nullptr) return in[i];
     const int k = ids[i];
     return make_int2((k < 0 || k > V) ? V : k, static_cast<int>(i));
   };
-  if constexpr (KEEP == IPT) {
 #pragma unroll
-    for (int r = 0; r < IPT; ++r) {
-      const int64_t i = wbase + r * 32 + lane;
-      key[r] = i < N ? load_pair(i) : make_int2(0, 0);
-    }
-  }
-  auto count_round = [&](int r, int2& k, int& rk) {
+  for (int r = 0; r < IPT; ++r) {
     const int64_t i = wbase + r * 32 + lane;
-    const bool live = i < N;
-    if constexpr (KEEP != IPT) k = live ? load_pair(i) : make_int2(0, 0);
-    const int d = live ? (k.x >> shift) & (bins - 1) : bins;
+    key[r] = i < N ? load_pair(i) : make_int2(0, 0);
+  }
+#pragma unroll
+  for (int r = 0; r < IPT; ++r) {
+    const bool live = wbase + r * 32 + lane < N;
+    const int d = live ? (key[r].x >> shift) & (bins - 1) : bins;
     const unsigned peers = __match_any_sync(0xffffffffu, d);
     const int old = live ? cnt[warp][d] : 0;
-    rk = old + __popc(peers & lt);
+    rank[r] = old + __popc(peers & lt);
     __syncwarp();
     if (live && (peers & lt) == 0) cnt[warp][d] = static_cast<uint16_t>(old + __popc(peers));
     __syncwarp();
-  };
-#pragma unroll
-  for (int r = 0; r < IPT; ++r) {
-    if constexpr (KEEP == IPT) {
-      count_round(r, key[r], rank[r]);
-    } else {
-      int2 k;
-      int rk;
-      count_round(r, k, rk);
-    }
   }
   __syncthreads();
   // exclusive prefix of the counts over the warps
@@ -258,27 +282,17 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const int* __rest
   }
   __syncthreads();
   if (failed != 0) return;
-  auto put = [&](int r, int2 k, int rk) {
-    const bool live = wbase + r * 32 + lane < N;
-    const int pos = live ? off[(k.x >> shift) & (bins - 1)] + rk : 0;
-    if (live) out[pos] = k;
-    if (hist_next != nullptr) {
-      // one atomic per distinct counter of the warp: entries of a hot id share theirs
-      const int bin = live ? (pos / (kSortThreads * IPT)) * bins + ((k.x >> (shift + bits)) & (bins - 1)) : -1;
-      const unsigned peers = __match_any_sync(0xffffffffu, bin);
-      if (live && (peers & lt) == 0) atomicAdd(hist_next + bin, __popc(peers));
-    }
-  };
 #pragma unroll
   for (int r = 0; r < IPT; ++r) {
-    if constexpr (KEEP == IPT) {
-      put(r, key[r], rank[r] + cnt[warp][(key[r].x >> shift) & (bins - 1)]);
-    } else {
-      // the counters now hold each warp's start: counting again gives start + rank
-      int2 k;
-      int rk;
-      count_round(r, k, rk);
-      put(r, k, rk);
+    const bool live = wbase + r * 32 + lane < N;
+    const int d = (key[r].x >> shift) & (bins - 1);
+    const int pos = live ? off[d] + cnt[warp][d] + rank[r] : 0;
+    if (live) out[pos] = key[r];
+    if (hist_next != nullptr) {
+      // one atomic per distinct counter of the warp: entries of a hot id share theirs
+      const int bin = live ? (pos / (kSortThreads * IPT)) * bins + ((key[r].x >> (shift + bits)) & (bins - 1)) : -1;
+      const unsigned peers = __match_any_sync(0xffffffffu, bin);
+      if (live && (peers & lt) == 0) atomicAdd(hist_next + bin, __popc(peers));
     }
   }
 }
@@ -649,6 +663,7 @@ __global__ void __launch_bounds__(256, VEC == 8 ? 3 : 4) k_segment_sum(const Seg
 }
 
 // One block per chunk whose last segment continues: adds that segment's partials.
+constexpr int kJoinBatch = 8;               // partials in flight per thread
 template <int VEC, typename TOut>
 __global__ void __launch_bounds__(256) k_segment_join(const SegmentParams p, int64_t chunk_entries) {
   __shared__ float red[8][32 * VEC];
@@ -686,15 +701,15 @@ __global__ void __launch_bounds__(256) k_segment_join(const SegmentParams p, int
 #pragma unroll
   for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
   if (col < p.D) {
-    for (int64_t cb = c0 + w; cb <= c1; cb += 32) {
-      RowPiece<VEC, float> q[4];
+    for (int64_t cb = c0 + w; cb <= c1; cb += 8 * kJoinBatch) {
+      RowPiece<VEC, float> q[kJoinBatch];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kJoinBatch; ++u) {
         const int64_t c = min(cb + 8 * u, c1);
         q[u].load(p.part + (2 * c + (c == c0 ? 1 : 0)) * p.D + col);
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kJoinBatch; ++u) {
         float v[VEC];
         q[u].values(v);
         if (cb + 8 * u <= c1) {
