@@ -22,7 +22,7 @@
 // beside the 112 MB of zeros (17 us at the measured copy rate), sums 8.6, join 2.8.
 // N = 200,003, V = 100,000, D = 200 fp32: keys 6 us, two passes beside 80 MB of zeros
 // 24, sums 48 (160 MB read, 3.5 TB/s: several waves of blocks whose rows are 800 random
-// bytes each), join 9.  The sorts are bound by latency: a few dozen blocks, each a
+// bytes each), join 8.  The sorts are bound by latency: a few dozen blocks, each a
 // chain of loads, counts and scattered stores.
 #pragma once
 #include <cuda_bf16.h>
@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(256, VEC == 8 ? 3 : 4) k_segment_sum(const Seg
 // One block per chunk whose last segment continues: adds that segment's partials.
 constexpr int kJoinBatch = 8;               // partials in flight per thread
 template <int VEC, typename TOut>
-__global__ void __launch_bounds__(256) k_segment_join(const SegmentParams p, int64_t chunk_entries) {
+__global__ void __launch_bounds__(256, 4) k_segment_join(const SegmentParams p, int64_t chunk_entries) {
   __shared__ float red[8][32 * VEC];
   if (*p.status != 0) return;
   const int64_t c0 = blockIdx.x, b0 = c0 * chunk_entries, end = b0 + chunk_entries;

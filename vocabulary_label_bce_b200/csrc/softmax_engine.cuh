@@ -25,11 +25,11 @@
 // and D = 64.  Every wait is bounded.
 //
 // What bounds it, at T = 12,800 positions (10,240 count), V = 876,000, D = 64:
-//   kLse   2.01 ms.  One exponential per logit: 1.37 ms of SFU time with 5 of 16 on
+//   kLse   2.02 ms.  One exponential per logit: 1.37 ms of SFU time with 5 of 16 on
 //          the FMA pipe, which the maximum and the polynomial then share with the
 //          sums.  256-item tiles: the hand-over alone takes 0.65 ms, with 128-item
 //          tiles 1.08.
-//   kRows  2.15 ms and kItems 2.09 ms alone, about 2.4 each in a loop of whole steps,
+//   kRows  2.15 ms and kItems 2.05 ms alone, about 2.4 each in a loop of whole steps,
 //          where the card holds its power limit (sw_power_cap).  The MMAs take 1.4 and
 //          1.6 ms (the D = 64 contraction runs at two thirds of the tensor rate), the
 //          exponentials 1.4 of SFU time; three logit buffers are all that fits beside

@@ -729,7 +729,7 @@ struct HeadDhParams {
 // then added in order: 1, or 8 where the positions alone leave SMs idle (131 splits of
 // 9 rows took 30 us with one thread each).
 template <int kLanes>
-__global__ void __launch_bounds__(256) k_head_dh(const HeadDhParams p) {
+__global__ void __launch_bounds__(256, 4) k_head_dh(const HeadDhParams p) {
   if (p.hdr->w.status != 0) return;
   constexpr int kCols = 256 / kLanes;             // groups of four columns per block
   __shared__ float4 s_part[kLanes > 1 ? kLanes : 1][kLanes > 1 ? kCols : 1];
