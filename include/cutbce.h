@@ -332,8 +332,9 @@ cutbce_status cutbce_embed_backward(const void* dX, int32_t dtype, const int32_t
  * 8, at most 256, 16-byte aligned); T < 2^24 - 255, V < 2^31 - 1, T K < 2^28.
  * With p_t = softmax(z_t / tau), every gradient has the form
  *   dz_tv = w_t (p_tv - q_tv),   dH = dz E,   dE = dz^T H.
- * The dense part w p is rounded to bf16 once, as the operand of the second tensor
- * contraction; the sparse part w q stays in fp32.  Deterministic.  All sizes are at
+ * For the items with q_tv = 0, w p is rounded to bf16 once, as the operand of the
+ * second tensor contraction; for the others, w (p - q) is formed and summed in fp32, so
+ * a gradient keeps its relative accuracy where p approaches q.  Deterministic.  All sizes are at
  * least 1.  On a data error (workspace status, cutbce_read_status) the loss is NaN and
  * the other outputs are unspecified.
  *

@@ -245,9 +245,10 @@ struct HeadPlan {
   int DP, BN, S, tps, n_vtiles, n_blk;
   int BN_lse, n_vtiles_lse, S_lse, tps_lse;   // the log-sum-exp pass's tiles and splits
   bool fused;                    // the dH pass takes the row sums: no log-sum-exp pass of its own
+  bool rows_first;               // the dH pass runs ahead of the join of the row sums (fused, or given the lse)
   int64_t Tc;
   size_t o_hdr, o_blk, o_cls, o_cidx, o_orig, o_coef, o_off16, o_b2, o_lse2, o_term, o_hc, o_lpart, o_part, o_wide, o_m2, o_rescale, o_sparse, o_dhpart,
-      o_keys, o_share, o_usum, o_first, total;
+      o_targets, o_tref, o_tsum, o_omp, o_keys, o_share, o_zt, o_usum, o_first, o_columns, total;
   SortBuffers sort;
   size_t clear_bytes;            // header and histograms
 };
@@ -295,6 +296,7 @@ void plan_head(const HeadProblem& p, bool dH, bool dE, bool lse_pass, HeadPlan& 
   pl.n_vtiles = static_cast<int>(ceil_div(p.V, pl.BN));
   pl.n_blk = static_cast<int>(ceil_div(p.T, 256));
   pl.fused = lse_pass && dH && p.T * p.V >= kFusedLogits;
+  pl.rows_first = dH && (pl.fused || !lse_pass);
   pl.Tc = round_up(p.T, kTileM) + kTileM;
   const int64_t nT = ceil_div(p.T, kTileM);
   // dH partials are read at about 5 MB a microsecond, a streamed tile takes about 0.6
@@ -304,31 +306,37 @@ void plan_head(const HeadProblem& p, bool dH, bool dE, bool lse_pass, HeadPlan& 
   pl.n_vtiles_lse = static_cast<int>(ceil_div(p.V, pl.BN_lse));
   pl.S_lse = choose_splits(nT, pl.n_vtiles_lse, pl.BN_lse, 0.1);
   pl.tps_lse = static_cast<int>(ceil_div(pl.n_vtiles_lse, pl.S_lse));
-  const size_t T = static_cast<size_t>(p.T), Tc = static_cast<size_t>(pl.Tc), TK = T * p.K;
+  const size_t T = static_cast<size_t>(p.T), Tc = static_cast<size_t>(pl.Tc), TK = Tc * p.K;
   Layout l;
   pl.o_hdr = l.take(256);
   pl.sort = SortBuffers{};
-  if (dE) plan_sort(p.T * p.K, p.V, p.D, pl.sort, l);
+  if (dE) plan_sort(pl.Tc * p.K, p.V, p.D, pl.sort, l);
   pl.clear_bytes = dE ? pl.sort.o_hist + pl.sort.sp.hist_bytes : 256;
   pl.o_blk = l.take(8 * static_cast<size_t>(pl.n_blk));
   pl.o_cls = l.take(T);
   pl.o_cidx = l.take(4 * T);
   pl.o_orig = l.take(4 * Tc);
-  pl.o_coef = l.take(4 * T);
+  pl.o_coef = l.take(4 * Tc);
   pl.o_off16 = dE && pl.DP <= 128 ? l.take(32 * Tc) : 0;
   pl.o_b2 = dE && pl.DP > 128 ? l.take(4 * Tc) : 0;
   pl.o_lse2 = l.take(4 * Tc);
   pl.o_term = l.take(8 * Tc);
   pl.o_hc = l.take(2 * Tc * pl.DP);
   pl.o_lpart = l.take(8 * std::max<size_t>(static_cast<size_t>(p.P), Tc * 32 / kLseThreads));
-  pl.o_part = lse_pass ? l.take(8 * static_cast<size_t>(pl.fused ? pl.S : pl.S_lse) * kHeadSlots * Tc) : 0;
+  pl.o_part = lse_pass || dH ? l.take(8 * static_cast<size_t>(pl.rows_first ? pl.S : pl.S_lse) * kHeadSlots * Tc) : 0;
   pl.o_wide = pl.fused ? l.take(8 * static_cast<size_t>(pl.S_lse) * kHeadSlots * Tc) : 0;
-  pl.o_m2 = pl.fused ? l.take(4 * Tc) : 0;
+  pl.o_m2 = pl.rows_first ? l.take(4 * Tc) : 0;
   pl.o_rescale = l.take(4 * Tc);
-  pl.o_sparse = dH ? l.take(4 * Tc * pl.DP) : 0;
+  pl.o_targets = l.take(4 * TK);
+  pl.o_tref = l.take(4 * Tc);
+  pl.o_tsum = l.take(4 * Tc);
+  pl.o_omp = l.take(4 * Tc);
+  pl.o_sparse = dH ? l.take(2 * 4 * Tc * pl.DP) : 0;
   pl.o_dhpart = dH ? l.take(4 * static_cast<size_t>(pl.S) * Tc * pl.DP) : 0;
   pl.o_keys = dE ? l.take(4 * TK) : 0;
   pl.o_share = dE ? l.take(4 * TK) : 0;
+  pl.o_zt = dE ? l.take(4 * TK) : 0;
+  pl.o_columns = dE ? l.take(4 * TK) : 0;
   pl.o_usum = dE ? l.take(4 * TK * p.D) : 0;
   pl.o_first = dE ? l.take(16 * static_cast<size_t>(ceil_div(p.V, 4))) : 0;
   pl.total = l.total;
@@ -355,6 +363,13 @@ cudaError_t launch_softmax_dp(int DP, int grid, const CUtensorMap& s, const CUte
     case 256: return launch_softmax<256, kPass>(grid, s, x, o, sp, st);
     default: return cudaErrorInvalidValue;
   }
+}
+
+template <int J, bool kSmall>
+void launch_gather(int DP, unsigned grid, const HeadParams& hp, cudaStream_t st) {
+  if (DP == 64) k_head_gather<8, J, kSmall><<<grid, 256, 0, st>>>(hp);
+  else if (DP == 128) k_head_gather<16, J, kSmall><<<grid, 256, 0, st>>>(hp);
+  else k_head_gather<32, J, kSmall><<<grid, 256, 0, st>>>(hp);
 }
 
 struct HeadOutputs {
@@ -424,16 +439,21 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   hp.sparse = dH ? at<float>(ws, pl.o_sparse) : nullptr;
   hp.keys = dE ? at<int>(ws, pl.o_keys) : nullptr;
   hp.share = dE ? at<float>(ws, pl.o_share) : nullptr;
+  hp.zt = dE ? at<float>(ws, pl.o_zt) : nullptr;
+  hp.targets = at<int>(ws, pl.o_targets);
+  hp.tref = at<float>(ws, pl.o_tref);
+  hp.tsum = at<float>(ws, pl.o_tsum);
+  hp.omp = at<float>(ws, pl.o_omp);
   hp.coef = at<float>(ws, pl.o_coef);
   hp.off16 = dE && pl.DP <= 128 ? at<__nv_bfloat16>(ws, pl.o_off16) : nullptr;
   hp.b2 = dE && pl.DP > 128 ? at<float>(ws, pl.o_b2) : nullptr;
   hp.lse2 = at<float>(ws, pl.o_lse2);
   hp.lse_in = lse_in;
   hp.c2 = kLog2eF / p.tau;
-  hp.m2 = pl.fused ? at<float>(ws, pl.o_m2) : nullptr;
+  hp.m2 = pl.rows_first ? at<float>(ws, pl.o_m2) : nullptr;
   hp.rescale = at<float>(ws, pl.o_rescale);
-  hp.part = lse_in == nullptr ? at<float2>(ws, pl.o_part) : nullptr;
-  hp.slots = kHeadSlots * (pl.fused ? pl.S : pl.S_lse);
+  hp.part = lse_in == nullptr || dH ? at<float2>(ws, pl.o_part) : nullptr;
+  hp.slots = kHeadSlots * (pl.rows_first ? pl.S : pl.S_lse);
   hp.Tc = pl.Tc;
   hp.loss_part = at<double>(ws, pl.o_lpart);
   hp.loss = out.loss;
@@ -445,18 +465,15 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   if (!small) CUTBCE_CK(cudaMemsetAsync(hp.hdr, 0, pl.clear_bytes, st));
   {
     LaunchScope ls(CUTBCE_KERNEL_HEAD_PREP, st);
-    const unsigned grid = static_cast<unsigned>(ceil_div(p.T + 256, 8));
-    if (small) {
-      if (pl.DP == 64) k_head_gather<8, true><<<grid, 256, 0, st>>>(hp);
-      else if (pl.DP == 128) k_head_gather<16, true><<<grid, 256, 0, st>>>(hp);
-      else k_head_gather<32, true><<<grid, 256, 0, st>>>(hp);
-    } else {
+    const unsigned grid = static_cast<unsigned>(pl.Tc / 8);
+    if (!small) {
       const int64_t norm_blocks = pl.fused ? std::min<int64_t>(ceil_div(p.V, 128), 8 * 148) : 0;
       k_head_rows<<<static_cast<unsigned>(pl.n_blk + norm_blocks), 256, 0, st>>>(hp);
-      if (pl.DP == 64) k_head_gather<8, false><<<grid, 256, 0, st>>>(hp);
-      else if (pl.DP == 128) k_head_gather<16, false><<<grid, 256, 0, st>>>(hp);
-      else k_head_gather<32, false><<<grid, 256, 0, st>>>(hp);
     }
+    if (small && p.K <= 32) launch_gather<1, true>(pl.DP, grid, hp, st);
+    else if (small) launch_gather<4, true>(pl.DP, grid, hp, st);
+    else if (p.K <= 32) launch_gather<1, false>(pl.DP, grid, hp, st);
+    else launch_gather<4, false>(pl.DP, grid, hp, st);
     CUTBCE_CK(cudaGetLastError());
   }
   SoftmaxParams sp{};
@@ -469,6 +486,8 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   sp.tiles_per_split = pl.tps;
   sp.n_item_tiles_bn = pl.n_vtiles;
   sp.timeout_ns = kDefaultTimeoutNs;
+  sp.targets = hp.targets;
+  sp.K = hp.K;
   CUtensorMap m_rows_s;                                      // the positions as stationary operand
   if (!make_map(&m_rows_s, hp.Hc, pl.DP, pl.Tc, pl.DP, kTileM)) return CUTBCE_ERR_CUDA;
   auto row_grid = [&](int splits) {                          // persistent: at most one CTA per SM
@@ -496,24 +515,26 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
       CUTBCE_CK(launch_softmax_dp<kPassLse>(pl.DP, row_grid(pl.S_lse), m_rows_s, m_lse_x, m_lse_x, lp, st));
     }
     if (pl.fused) {
-      sp.off2 = hp.m2;
-      sp.part = at<float2>(ws, pl.o_part);
       sp.wide_part = at<float2>(ws, pl.o_wide);
       sp.wide_slots = kHeadSlots * pl.S_lse;
-      CUTBCE_CK(row_pass());
     }
-    sp.part = nullptr;
-    sp.wide_part = nullptr;
   }
+  if (pl.rows_first) {
+    sp.off2 = hp.m2;
+    sp.part = at<float2>(ws, pl.o_part);
+    CUTBCE_CK(row_pass());
+  }
+  sp.part = nullptr;
+  sp.wide_part = nullptr;
   {
     LaunchScope ls(CUTBCE_KERNEL_HEAD_FINISH, st);
-    if (lse_in == nullptr && hp.slots > kLseManySlots) k_head_lse<32><<<static_cast<unsigned>(pl.Tc * 32 / kLseThreads), kLseThreads, 0, st>>>(hp);
+    if (hp.part != nullptr && hp.slots > kLseManySlots) k_head_lse<32><<<static_cast<unsigned>(pl.Tc * 32 / kLseThreads), kLseThreads, 0, st>>>(hp);
     else k_head_lse<4><<<static_cast<unsigned>(pl.Tc * 4 / kLseThreads), kLseThreads, 0, st>>>(hp);
     if (p.kind == kHeadPreference) k_head_pairs<<<static_cast<unsigned>(p.P), kPairThreads, 0, st>>>(hp);
     CUTBCE_CK(cudaGetLastError());
   }
   if (dH) {
-    if (!pl.fused) {
+    if (!pl.rows_first) {
       sp.off2 = hp.lse2;
       CUTBCE_CK(row_pass());
     }
@@ -527,6 +548,7 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
     dp.coef = hp.coef;
     dp.part = at<float>(ws, pl.o_dhpart);
     dp.sparse = hp.sparse;
+    dp.omp = hp.omp;
     dp.rescale = hp.rescale;
     dp.dH = out.dH;
     dp.bf16 = out.grad_dtype == CUTBCE_GRAD_BF16;
@@ -539,14 +561,15 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
     CUTBCE_CK(cudaGetLastError());
   }
   if (dE) {
-    // the sparse part of dE: sum of coef q h over the pairs of each item, in fp32
+    // the targets' part of dE: sum of coef (q - p) h over the pairs of each item, in fp32
     SegmentParams gp{};
     const FillJob none{at<uint4>(ws, pl.o_first), ceil_div(p.V, 4), 0xFFFFFFFFu};
     if ((s = run_sort(pl.sort, hp.keys, hp.V, ws, status, false, none, st, &gp.pairs)) != CUTBCE_OK) return s;
-    gp.N = p.T * p.K;
+    gp.N = pl.Tc * p.K;
     gp.V = hp.V;
     gp.D = hp.D;
-    gp.src = p.H;
+    gp.src = hp.Hc;
+    gp.src_stride = pl.DP;
     gp.K = hp.K;
     gp.share = hp.share;
     gp.row_coef = hp.coef;
@@ -554,9 +577,12 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
     gp.part = at<float>(ws, pl.sort.o_part);
     gp.out = at<float>(ws, pl.o_usum);
     gp.first = at<int>(ws, pl.o_first);
+    gp.columns = at<uint32_t>(ws, pl.o_columns);
     gp.status = status;
     if ((s = run_sums(gp, true, st)) != CUTBCE_OK) return s;
     sp.first = gp.first;
+    sp.columns = gp.columns;
+    sp.n_pairs = static_cast<int>(gp.N);
     sp.sparse = at<float>(ws, pl.o_usum);
     sp.dE = out.dE;
     sp.de_bf16 = out.grad_dtype == CUTBCE_GRAD_BF16;
@@ -579,9 +605,10 @@ cutbce_status head_workspace(const HeadProblem& p, int outputs, size_t* bytes) {
     return CUTBCE_ERR_INVALID_ARG;
   const cutbce_status s = check_head(p, false);
   if (s != CUTBCE_OK) return s;
-  HeadPlan pl;
-  plan_head(p, (outputs & CUTBCE_OUT_DH) != 0, (outputs & CUTBCE_OUT_DE) != 0, true, pl);   // the larger layout
-  *bytes = pl.total;
+  HeadPlan with, without;                          // a pass for the log-sum-exps, or those of a forward
+  plan_head(p, (outputs & CUTBCE_OUT_DH) != 0, (outputs & CUTBCE_OUT_DE) != 0, true, with);
+  plan_head(p, (outputs & CUTBCE_OUT_DH) != 0, (outputs & CUTBCE_OUT_DE) != 0, false, without);
+  *bytes = std::max(with.total, without.total);
   return CUTBCE_OK;
 }
 
@@ -647,6 +674,7 @@ cutbce_status cutbce_embed_backward(const void* dX, int32_t dtype, const int32_t
   p.V = static_cast<int>(V);
   p.D = static_cast<int>(D);
   p.src = dX;
+  p.src_stride = D;
   p.K = 1;
   p.scale = scale;
   p.part = at<float>(ws, pl.sort.o_part);

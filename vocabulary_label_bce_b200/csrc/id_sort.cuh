@@ -437,7 +437,8 @@ struct SegmentParams {
   const int2* pairs;          // sorted (id, entry index): id V has no row; indices ascend within an id
   int64_t N;
   int V, D;
-  const void* src;            // [rows, D] rows to add; entry p reads row p / K
+  const void* src;            // [rows, src_stride] rows to add; entry p reads row p / K
+  int64_t src_stride;
   int K;
   const float* share;         // [N] factor of entry p, or null
   const float* row_coef;      // [rows] factor of its row, or null
@@ -445,6 +446,7 @@ struct SegmentParams {
   float* part;                // [2 * chunks, D]: the chunk's first (continued) and last (continuing) segment
   void* out;                  // by item: [V, D] fp32 or bf16; by segment (first != null): fp32 row at the segment's first index
   int* first;                 // [V] first sorted index of each id's segment (cleared to -1), or null
+  uint32_t* columns;          // [N] row of each sorted entry, 2^31 added to the first of an id, or null
   int out_bf16, accumulate;
   const int* status;
 };
@@ -592,14 +594,15 @@ __global__ void __launch_bounds__(256, VEC == 8 ? 3 : 4) k_segment_sum(const Seg
     for (int64_t i = i0; i < i1; i += kSumBatch) {
       RowPiece<VEC, TIn> x[kSumBatch];
       float w[kSumBatch];
-      int now[kSumBatch];
+      int now[kSumBatch], from[kSumBatch];
 #pragma unroll
       for (int u = 0; u < kSumBatch; ++u) {
         const int64_t row = p.K == 1 ? e[u] : e[u] / p.K;
         w[u] = p.share != nullptr ? __ldg(p.share + e[u]) : 1.f;
         if (p.row_coef != nullptr) w[u] *= __ldg(p.row_coef + row);
-        x[u].load(src + (live ? row * p.D : -col));       // lanes past the row's end read its first element
+        x[u].load(src + (live ? row * p.src_stride : -col));       // lanes past the row's end read its first element
         now[u] = id[u];
+        from[u] = static_cast<int>(row);
       }
       if (i + kSumBatch < i1) load_entries(i + kSumBatch);
 #pragma unroll
@@ -613,6 +616,8 @@ __global__ void __launch_bounds__(256, VEC == 8 ? 3 : 4) k_segment_sum(const Seg
 #pragma unroll
           for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
         }
+        if (p.columns != nullptr && col == 0)
+          p.columns[i + u] = static_cast<uint32_t>(from[u]) | (i + u == start && !open_left ? 0x80000000u : 0u);
         float v[VEC];
         x[u].values(v);
 #pragma unroll

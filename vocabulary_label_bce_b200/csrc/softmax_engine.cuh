@@ -17,6 +17,13 @@
 //          of w_t (the negative ones from a tile boundary on), so the sign is
 //          the negate-A bit of the contraction's instruction descriptor.
 //
+// A row's targets are left out of all three passes (their exponentials are 0 in the
+// sums and in P): p - q of a target is a small difference where the loss is small,
+// and bf16(p) would swamp it.  softmax_head.cuh carries them in fp32.  Each epilogue
+// thread owns a stationary row and walks its targets (kLse, kRows: the row's ids; kItems:
+// the item's positions, from the sorted pairs) with a forward cursor; a tile without one
+// pays a comparison and a vote.
+//
 // c = log2(e) / tau.  Warp roles, tensor-memory layout and hand-over of the tiles
 // follow the BCE engine (warp 0 loads by TMA, 16 epilogue warps in two groups take
 // alternate tiles), with one difference: the logit MMAs and the contractions are
@@ -97,8 +104,12 @@ struct SoftmaxParams {
   int wide_slots;              // their number per row
   int only_wide;               // kLse: run only where hdr->wide is set
   float* dh_part;              // kRows: [splits, Tc, DP]
-  const int* first;            // kItems: [V] row of `sparse` of each item, -1 none
-  const float* sparse;         // kItems: [.., D] sparse part of dE, unscaled
+  const int* targets;          // kLse, kRows: [Tc, K] ids of each row's targets, ascending, then -1
+  int K;
+  const uint32_t* columns;     // kItems: [n_pairs] compacted positions of the sorted pairs, 2^31 added to an item's first
+  int n_pairs;
+  const int* first;            // kItems: [V] first pair of each item, and its row of `sparse`; -1 none
+  const float* sparse;         // kItems: [.., D] sum of (q - p) h over the item's pairs
   void* dE;                    // kItems: [V, D]
   int de_bf16, de_acc;
   int nsplit, tiles_per_split, n_item_tiles_bn;
@@ -151,12 +162,128 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// 32 logits of one row -> their exponentials.  kTail: columns from `valid` on are
-// outside the table and count as -infinity.
-__device__ __forceinline__ void mask_tail(uint32_t (&r)[32], int valid) {
+// Forward-only cursor over the columns that a stationary row leaves out: `next` is the
+// first not yet passed, `ahead` the one behind it (2^31 and above: none is left).  Passing
+// one loads another, which is not looked at before the one after it is passed, so that the
+// load's latency is hidden (waiting for it made the log-sum-exp pass 2.33 ms instead of 2.15
+// at T = 12,800, V = 876,000, K = 16).
+// The list is the row's of `targets`, or the item's run of `columns`.
+constexpr uint32_t kNoTarget = 0xFFFFFFFFu;
+struct TargetCursor {
+  int at;                       // index of `next`: slot of the row's list, or entry of `columns`
+  uint32_t next, ahead;
+};
+
+template <bool kItems>
+__device__ __forceinline__ uint32_t load_target(const SoftmaxParams& p, int s_row, int at) {
+  if (kItems) return at < p.n_pairs ? __ldg(p.columns + at) : kNoTarget;
+  return at < p.K ? static_cast<uint32_t>(__ldg(p.targets + static_cast<int64_t>(s_row) * p.K + at)) : kNoTarget;
+}
+
+// kLse, kRows: starts at the first id of the row's list that is not below col0.  Halved down
+// to eight slots, which are loaded together: one round trip for K <= 8, two for 16.
+__device__ __forceinline__ TargetCursor row_cursor(const SoftmaxParams& p, int s_row, uint32_t col0) {
+  int lo = 0, n = p.K;
+  while (n > 8) {
+    const int half = n >> 1;
+    if (load_target<false>(p, s_row, lo + half) < col0) {
+      lo += half + 1;
+      n -= half + 1;
+    } else {
+      n = half;
+    }
+  }
+  // the answer is one of slots lo .. lo + n
+  uint32_t v[9];
 #pragma unroll
-  for (int e = 0; e < 32; ++e)
-    if (e >= valid) r[e] = 0xFF800000u;
+  for (int i = 0; i < 9; ++i) v[i] = i <= n ? load_target<false>(p, s_row, lo + i) : kNoTarget;
+  TargetCursor cur{lo, kNoTarget, kNoTarget};
+#pragma unroll
+  for (int i = 0; i < 9; ++i) {
+    cur.at += v[i] < col0;
+    if (v[i] >= col0) cur.next = min(cur.next, v[i]);
+  }
+  cur.ahead = load_target<false>(p, s_row, cur.at + 1);
+  return cur;
+}
+
+// The targets in columns [lo, lo + 32 N), lo a multiple of 32, as bits of mask[N]; passes all
+// below the end (those below lo are in another warp's columns).  A list may name a column
+// twice.  Where a row has more than one, up to kBatch others are loaded together; rows of an
+// item that has still more in this tile (an item of many positions) are then taken one by
+// one by the whole warp, 32 entries at a time.  With ids of a Zipf law (4,834 positions, half
+// of them in one tile of items) the dE pass takes 0.154 ms, 0.26 entry by entry, 0.14
+// if nothing were left out.
+template <bool kItems, int N>
+__device__ __forceinline__ void take_targets(TargetCursor& cur, const SoftmaxParams& p, int s_row, uint32_t lo, uint32_t (&mask)[N]) {
+  constexpr int kBatch = 8;
+  const uint32_t hi = lo + 32u * N;
+  const int lane = threadIdx.x & 31;
+  auto set = [&](uint32_t (&m)[N], uint32_t col) {
+#pragma unroll
+    for (int w = 0; w < N; ++w)
+      if (col - (lo + 32u * w) < 32u) m[w] |= 1u << (col & 31u);
+  };
+  bool more = false;
+  if (cur.next < hi) {
+    set(mask, cur.next);
+    cur.next = cur.ahead;
+    ++cur.at;
+    more = cur.next < hi;
+    if (!more) cur.ahead = load_target<kItems>(p, s_row, cur.at + 1);
+  }
+  if (!__any_sync(0xffffffffu, more)) return;
+  if (!kItems) {
+    while (cur.next < hi) {
+      set(mask, cur.next);
+      cur.next = load_target<false>(p, s_row, ++cur.at);
+    }
+    if (more) cur.ahead = load_target<false>(p, s_row, cur.at + 1);
+    return;
+  }
+  const bool again = more;
+  if (more) {
+    set(mask, cur.next);
+    uint32_t col[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) col[u] = load_target<kItems>(p, s_row, cur.at + 1 + u);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (!more) continue;
+      ++cur.at;
+      cur.next = col[u];
+      more = col[u] < hi;
+      if (more) set(mask, col[u]);
+    }
+  }
+  // rows with `more`: the entry cur.at is taken, those behind it are not
+  for (unsigned todo = __ballot_sync(0xffffffffu, more); todo != 0u; todo &= todo - 1u) {
+    const int from = __ffs(todo) - 1;
+    int at = __shfl_sync(0xffffffffu, cur.at, from) + 1;
+    uint32_t bits[N], next;
+#pragma unroll
+    for (int w = 0; w < N; ++w) bits[w] = 0u;
+    while (true) {
+      const uint32_t col = load_target<kItems>(p, s_row, at + lane);
+      // columns ascend up to the next item's first, whose top bit is set; what follows is not this item's
+      const unsigned past = __ballot_sync(0xffffffffu, col >= hi);
+      const int below = past != 0u ? __ffs(past) - 1 : 32;
+      if (lane < below) set(bits, col);
+      at += below;
+      next = __shfl_sync(0xffffffffu, col, below & 31);
+      if (below < 32) break;
+    }
+#pragma unroll
+    for (int w = 0; w < N; ++w) {
+      bits[w] = __reduce_or_sync(0xffffffffu, bits[w]);
+      if (lane == from) mask[w] |= bits[w];
+    }
+    if (lane == from) {
+      cur.at = at;
+      cur.next = next;
+    }
+  }
+  if (again) cur.ahead = load_target<kItems>(p, s_row, cur.at + 1);
 }
 
 template <int DP, int kPass>
@@ -262,7 +389,11 @@ __global__ void __launch_bounds__(SoftmaxCfg<DP, kPass>::THREADS, 1)
   // work item i: a tile of items (kItems), or (vocabulary split, tile of positions), split-major
   auto item = [&](int i, int& s_row0, int& x0, int& nx, int& split) {
     if (kItems) {
-      s_row0 = i * kTileM;
+      // The first round goes from the last CTA to the first: where ids are ranks, the tile
+      // with the most pairs goes to a CTA that has no tile of the last round (0.175 to 0.154 ms
+      // for the dE pass of 4,834 positions of a Zipf law, V = 100,000; 0.166 either way of 51,200
+      // evenly spread pairs).
+      s_row0 = (i < static_cast<int>(gridDim.x) ? static_cast<int>(gridDim.x) - 1 - i : i) * kTileM;
       x0 = 0;
       nx = n_rows / BN;
       split = 0;
@@ -439,6 +570,22 @@ __global__ void __launch_bounds__(SoftmaxCfg<DP, kPass>::THREADS, 1)
     const float2 c2 = f2(p.c2, p.c2);
     uint32_t cnt = 0, ic = 0, acc_reads = 0;
     bool ok = true;
+    // kItems: the item's first pair, read ahead (the next item's beside this one's tiles)
+    auto first_of = [&](int v) { return v < p.V ? __ldg(p.first + v) : -1; };
+    int first = -1;
+    TargetCursor cur{-1, kNoTarget, kNoTarget};
+    auto item_cursor = [&] {                      // at the item's first pair, whose top bit goes
+      cur = TargetCursor{first, kNoTarget, kNoTarget};
+      if (first < 0) return;
+      cur.next = load_target<true>(p, 0, first) & 0x7FFFFFFFu;
+      cur.ahead = load_target<true>(p, 0, first + 1);
+    };
+    if (kItems) {
+      int s_row0, x0, nx, split;
+      item(static_cast<int>(blockIdx.x), s_row0, x0, nx, split);
+      first = first_of(s_row0 + row);
+      item_cursor();
+    }
     for (int i = blockIdx.x; i < n_items && ok; i += gridDim.x, ++ic) {
       int s_row0, x0, n, split;
       item(i, s_row0, x0, n, split);
@@ -459,16 +606,37 @@ __global__ void __launch_bounds__(SoftmaxCfg<DP, kPass>::THREADS, 1)
         }
         off = -m;
       }
+      const int s_row = s_row0 + row;
+      int first_next = -1;
+      if (!kItems) cur = row_cursor(p, s_row, static_cast<uint32_t>(x0) * BN);
+      else if (i + static_cast<int>(gridDim.x) < n_items) first_next = first_of((i + static_cast<int>(gridDim.x)) * kTileM + row);
       const int j0 = static_cast<int>((grp + Cfg::GROUPS - cnt % Cfg::GROUPS) % Cfg::GROUPS);
       for (int j = j0; j < n; j += Cfg::GROUPS) {
         const uint32_t c = cnt + j, bz = c % NZ;
+        const int tile_col0 = (x0 + j) * BN + slab * ZC;      // item (or compacted position) of the slab's first column
+        // columns that count as -infinity: the row's targets, and those past the table's end
+        uint32_t drop[NCH];
+#pragma unroll
+        for (int ch = 0; ch < NCH; ++ch) drop[ch] = 0u;
+        unsigned hit = 0u;                        // chunks that have such a column in some row of the warp
+        if (__any_sync(0xffffffffu, cur.next < static_cast<uint32_t>(tile_col0) + ZC)) {
+          take_targets<kItems>(cur, p, s_row, static_cast<uint32_t>(tile_col0), drop);
+#pragma unroll
+          for (int ch = 0; ch < NCH; ++ch) hit |= __any_sync(0xffffffffu, drop[ch] != 0u) ? 1u << ch : 0u;
+        }
+        if (!kItems && (x0 + j + 1) * static_cast<int64_t>(BN) > p.V) {
+          hit = (1u << NCH) - 1u;
+#pragma unroll
+          for (int ch = 0; ch < NCH; ++ch) {
+            const int valid = p.V - (tile_col0 + ch * 32);
+            if (valid < 32) drop[ch] |= valid <= 0 ? 0xFFFFFFFFu : 0xFFFFFFFFu << valid;
+          }
+        }
         if (!wait_bar_warp(bar_zfull + bz, (c / NZ) & 1, wc, wait_tag(4, 4, c))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const int tile_col0 = (x0 + j) * BN + slab * ZC;      // item (or compacted position) of the slab's first column
-        const bool tail = !kItems && (x0 + j + 1) * static_cast<int64_t>(BN) > p.V;
 #pragma unroll
         for (int ch = 0; ch < NCH; ++ch) {
           uint32_t r[32];
@@ -479,7 +647,11 @@ __global__ void __launch_bounds__(SoftmaxCfg<DP, kPass>::THREADS, 1)
             mbar_arrive(bar_zfree + bz);
           }
           const int col = tile_col0 + ch * 32;
-          if (tail) mask_tail(r, p.V - col);
+          if (hit >> ch & 1u) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (drop[ch] >> e & 1u) r[e] = 0xFF800000u;
+          }
           if constexpr (kPass == kPassLse) {
             float mx4[4];
 #pragma unroll
@@ -528,6 +700,11 @@ __global__ void __launch_bounds__(SoftmaxCfg<DP, kPass>::THREADS, 1)
         }
       }
       if (!ok) break;
+      const int64_t sp = first;                   // kItems: the item's row of `sparse`
+      if (kItems) {
+        first = first_next;
+        item_cursor();
+      }
       if (kPass == kPassLse || (kPass == kPassRows && p.part != nullptr)) {
         const int slot = (split * Cfg::GROUPS + static_cast<int>(grp)) * Cfg::SLABS + slab;
         p.part[static_cast<int64_t>(slot) * p.Tc + s_row0 + row] = make_float2(m, sum);
@@ -540,12 +717,7 @@ __global__ void __launch_bounds__(SoftmaxCfg<DP, kPass>::THREADS, 1)
         ++acc_reads;
         tc_fence_after();
         const int v = s_row0 + row;
-        int64_t sp = -1;
-        float gs = 0.f;
-        if (kItems && v < p.V) {
-          sp = __ldg(p.first + v);
-          gs = hdr->grad_scale;
-        }
+        const float gs = kItems ? hdr->grad_scale : 0.f;
 #pragma unroll 1
         for (int ch = 0; ch < AC / 16; ++ch) {
           uint32_t r[16];

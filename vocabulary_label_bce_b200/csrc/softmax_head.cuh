@@ -4,17 +4,27 @@
 //   rows    which positions count, their class (sign of their gradient's factor),
 //           the checks of ids and offsets, and the normalisation;
 //   gather  compacts the rows of H (positive class first, the negative class from
-//           the next multiple of 128 rows), takes the logits of the sparse
-//           targets and their part of dH in fp32;
-//   lse     joins the log-sum-exp partials of a row, and the distillation loss;
+//           the next multiple of 128 rows), sorts each row's targets, takes their
+//           logits and their part of dH in fp32;
+//   lse     joins the sums of a row's exponentials, forms p - q of its targets, and
+//           the distillation loss;
 //   pairs   the preference loss, from the sums over each sequence;
-//   dh      adds the split partials of dH, subtracts the sparse part, scales.
+//   dh      adds the split partials of dH and the targets' part, scales.
 //
 // With p = softmax(z / tau) and q the sparse target weights of a position, the
-// gradient of every such loss is  dz = w (p - q).  The dense part w p is formed
-// in the tile engine and rounded to bf16 there; the sparse part w q never passes
-// through bf16: it is summed in fp32 (here for dH, over sorted ids for dE) and
-// joined to the dense part before the one rounding of the output.
+// gradient of every such loss is  dz = w (p - q).  Where the losses are small, p is
+// close to q, and p rounded to bf16 would leave only the rounding of that difference
+// (with p = 0.996, 28% to 43% of dH in the norm).  So an item that is a target of a
+// row (q != 0) is left out of that row in the tile engine: its exponential counts as
+// 0 in the sums and in the contractions, which carry w p of the other items alone, each
+// rounded to bf16 relative to itself.  The targets are the sparse side's, in fp32.  With
+// t_k = 2^(x_k - x_max) over the row's targets, T = sum t_k, and R the sum of the
+// other items' exponentials on the same reference,
+//   p_k = t_k / (T + R),  p_k - q_k = (t_k / T - q_k) - omp t_k / T,  omp = R / (T + R):
+// omp = 1 - sum_k p_k comes from a sum, not from a difference, so one dominating
+// target keeps all the bits of 1 - p.  For dH the gather forms sum_k (q_k - t_k / T) e_k
+// and sum_k t_k / T e_k, which the dh kernel joins by omp; for dE the factors
+// q_k - p_k weigh the rows of H in the sums over sorted ids.
 //
 // All of them are short next to the tile passes and bound by memory latency; at
 // T = 12,800, K = 16, V = 876,000, D = 64: rows 7 us, or 32 with the norms of the
@@ -68,19 +78,24 @@ struct HeadParams {
   int* cidx;                     // [T] compacted row or -1
   int* orig;                     // [Tc] position of a compacted row, -1 padding
   __nv_bfloat16* Hc;             // [Tc, DP]
-  double* rowterm;               // [Tc] distillation: sum_k q (ln q - z / tau); preference: z_y
-  float* sparse;                 // [Tc, DP] sum_k q_k e_k, or null
-  int* keys;                     // [T * K] ids of the pairs (-1 none), or null
-  float* share;                  // [T * K] q of the pairs, or null
-  float* coef;                   // [T] signed factor of the row's gradient
+  double* rowterm;               // [Tc] distillation: sum_k q (ln q - (x_k - x_max) ln 2); preference: log p of the target
+  float* sparse;                 // [Tc, 2, DP] sum_k (q_k - t_k / T) e_k, sum_k t_k / T e_k, or null
+  float* tref;                   // [Tc] x_max: the largest x = c2 z of the row's targets
+  float* tsum;                   // [Tc] T
+  float* omp;                    // [Tc] 1 - the targets' probabilities
+  int* targets;                  // [Tc, K] ids of the row's targets, ascending, then -1
+  int* keys;                     // [Tc * K] ids of the pairs (-1 none; an id's first slot has all its weight), or null
+  float* share;                  // [Tc * K] q of the pairs, then q - p, or null
+  float* zt;                     // [Tc * K] x of the pairs, or null
+  float* coef;                   // [Tc] signed factor of the row's gradient
   float* b2;                     // [Tc] log2 |factor| - lse (log2 domain; with dE, wide D), or null
   __nv_bfloat16* off16;          // [Tc, 16] (log2 |factor| - lse) tau in three bf16 pieces, then zeros (with dE), or null
   float* lse2;                   // [Tc] lse in the log2 domain
   const float* lse_in;           // [T] lse of an earlier forward, or null
-  float* m2;                     // [Tc] reference of the row's exponentials in the dH pass, or null
+  float* m2;                     // [Tc] reference of the exponentials in a dH pass that takes the row sums, or null
   float c2;                      // log2(e) / tau
   float* rescale;                // [Tc] 2^(reference - lse): factor of the dense part of dH
-  const float2* part;            // [slots, Tc] (reference, sum) partials in the log2 domain
+  const float2* part;            // [slots, Tc] (reference, sum) of the items that are not targets, log2 domain, or null
   int slots;
   int64_t Tc;                    // rows of the compacted buffers
   double* loss_part;             // per-block (distillation) or per-pair (preference) partials
@@ -279,16 +294,17 @@ __global__ void __launch_bounds__(256) k_head_rows(const HeadParams p) {
 }
 
 // ------------------------------------------------------------------ gather
-// One warp per position, then one warp per padding row (256 of them at most).
+// One warp per position; a warp whose position does not count, or that has none,
+// takes an unused compacted row instead (padding: zeros, no targets).
 // `L` lanes hold a row in 16-byte pieces (8, 16 or 32 for DP = 64, 128 and above),
 // so a warp reads the rows of 32 / L targets at once, kGatherU of those in flight.
 //
 // With m2 it also sets the reference of the row's exponentials in a dH pass that
-// takes the row's sum on the way: m = |h| max|e| c, a bound of every logit
-// (Cauchy-Schwarz), so 2^(x - m) never overflows.  It must not lie too far above
-// the row's largest logit either: terms below 2^-126 are lost, and with a gap of at
-// most 70 (log2) the V < 2^31 lost terms are below 2^-25 of the sum.  The gap is
-// bounded by a logit that the row is known to have, its largest sparse target.
+// takes the row's sum on the way: the lse of an earlier forward, or m = |h| max|e| c, a
+// bound of every logit (Cauchy-Schwarz), so 2^(x - m) never overflows.  It must not lie
+// too far above the row's largest logit either: terms below 2^-126 are lost, and with a
+// gap of at most 70 (log2) the V < 2^31 lost terms are below 2^-25 of the sum.  The gap
+// is bounded by a logit that the row is known to have, its largest sparse target.
 // Rows beyond it set `wide`, and then the log-sum-exp pass runs first and its
 // result is the reference.
 //
@@ -308,7 +324,8 @@ __device__ __forceinline__ void unpack8(uint4 r, float (&x)[8]) {
   }
 }
 
-template <int L, bool kSmall>
+// J: groups of 32 slots (1 for K <= 32, else 4).
+template <int L, int J, bool kSmall>
 __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
   constexpr int G = 32 / L;                     // targets side by side
   const HeadHeader* hdr = p.hdr;
@@ -357,75 +374,71 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
   const int sub = lane % L, grp = lane / L;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + warp;
   const bool piece = 8 * sub < p.DP, real = 8 * sub < p.D;       // this lane's piece of a padded row, and of a row
-  if (t >= p.T) {
-    // padding rows: [n_pos, neg0) and [neg0 + n_neg, n_rows)
-    const int j = static_cast<int>(t - p.T);
-    const int gap = neg0 - n_pos;
-    const int64_t c = j < gap ? n_pos + j : neg0 + n_neg + (j - gap);
-    if (c >= neg0 + (n_neg + kTileM - 1) / kTileM * kTileM) return;
+  if (t >= p.Tc) return;
+  // the rows of each class before t: the prefix of its 256 and those before it in them
+  int cls = 0;
+  int64_t n1 = n_pos, n2 = n_neg;
+  if (t < p.T) {
+    cls = kSmall ? s_cls[t] : p.cls[t];
+    const int b = static_cast<int>(t >> 8), n = static_cast<int>(t & 255);
+    int before = 0;                                              // the second class in the upper half
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = lane + 32 * i;
+      const int o = k < n ? (kSmall ? s_cls[(b << 8) + k] : p.cls[(static_cast<int64_t>(b) << 8) + k]) : 0;
+      before += (o == 1) + ((o == 2) << 16);
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    n1 = before & 0xffff;
+    n2 = before >> 16;
+    if (kSmall) {
+      for (int g = 0; g < b; ++g) n1 += s_cnt[g][0], n2 += s_cnt[g][1];
+    } else {
+      n1 += p.blk[2 * b];
+      n2 += p.blk[2 * b + 1];
+    }
+  }
+  if (cls == 0) {
+    // the unused rows in order: those between the classes, then those behind both
+    const int64_t r = t - n1 - n2, gap = neg0 - n_pos;
+    const int64_t c = r < gap ? n_pos + r : neg0 + n_neg + (r - gap);
     if (grp == 0 && piece) reinterpret_cast<uint4*>(p.Hc + c * p.DP)[sub] = make_uint4(0u, 0u, 0u, 0u);
+    for (int k = lane; k < p.K; k += 32) {
+      p.targets[c * p.K + k] = -1;
+      if (p.keys != nullptr) p.keys[c * p.K + k] = -1;
+    }
     if (lane == 0) {
       p.orig[c] = -1;
       write_offset(p, c, -1e30f);
       p.lse2[c] = 0.f;
       if (p.m2 != nullptr) p.m2[c] = 0.f;
-    }
-    return;
-  }
-  const int cls = kSmall ? s_cls[t] : p.cls[t];
-  const int64_t r = t * p.K;
-  if (cls == 0) {
-    if (p.keys != nullptr)
-      for (int k = lane; k < p.K; k += 32) {
-        p.keys[r + k] = -1;
-        p.share[r + k] = 0.f;
+      if (t < p.T) {
+        p.cidx[t] = -1;
+        if (p.lse_out != nullptr) p.lse_out[t] = 0.f;
       }
-    if (lane == 0) {
-      p.cidx[t] = -1;
-      p.coef[t] = 0.f;
-      if (p.lse_out != nullptr) p.lse_out[t] = 0.f;
     }
     return;
   }
+  const int64_t c = cls == 2 ? neg0 + n2 : n1;
+  const int64_t r = t * p.K, rc = c * p.K;
   // the row, and the ids and logits of its slots (slot k = lane + 32 j), all in flight
   const uint4 hraw = real ? __ldg(reinterpret_cast<const uint4*>(p.H + t * p.D) + sub) : make_uint4(0u, 0u, 0u, 0u);
-  float q[4], lq[4];
-  int id[4];
+  float q[J], lq[J];
+  int id[J];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < J; ++j) {
     const int k = lane + 32 * j;
     id[j] = k < p.K ? __ldg(p.ids + r + k) : -1;
     lq[j] = p.kind == kHeadDistill && k < p.K ? __ldg(p.logits + r + k) : 0.f;
   }
-  // compacted row: this block's prefix plus the rows of the class before t in its 256
-  int64_t c;
-  {
-    const int b = static_cast<int>(t >> 8);
-    const int n = static_cast<int>(t & 255);
-    int before = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int k = lane + 32 * i;
-      if (k < n) before += (kSmall ? s_cls[(b << 8) + k] : p.cls[(static_cast<int64_t>(b) << 8) + k]) == cls;
-    }
-    before = __reduce_add_sync(0xffffffffu, before);
-    c = before + (cls == 2 ? neg0 : 0);
-    if (kSmall) {
-      for (int g = 0; g < b; ++g) c += s_cnt[g][cls - 1];
-    } else {
-      c += p.blk[2 * b + cls - 1];
-    }
-  }
   if (grp == 0 && piece) reinterpret_cast<uint4*>(p.Hc + c * p.DP)[sub] = hraw;
-  float h[8], sp[8];
+  float h[8];
   unpack8(hraw, h);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) sp[k] = 0.f;
   // the targets' weights
   if (p.kind == kHeadDistill) {
     float m = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < J; ++j) {
       lq[j] = id[j] >= 0 ? lq[j] * p.inv_tau : -INFINITY;
       m = fmaxf(m, lq[j]);
     }
@@ -433,7 +446,7 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float s = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < J; ++j) {
       lq[j] -= m;
       q[j] = expf(lq[j]);                        // an empty slot: e^-inf = 0
       s += q[j];
@@ -442,75 +455,172 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     const float ls = logf(s);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < J; ++j) {
       q[j] /= s;
       lq[j] -= ls;
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < J; ++j) {
       q[j] = j == 0 && lane == 0 ? 1.f : 0.f;
       lq[j] = 0.f;
     }
   }
-  double term = 0.0;
-  float zmax = -INFINITY;
+  // The row's targets, the slots with q != 0, in ascending order of id; an id's weights
+  // are added up in its first slot.  A slot's rank: the live ones that sort before it.
+  bool own[J];                                   // a live slot, the first of its id
+  {
+    float all[J];
+    int rank[J], live_n = 0;
+    bool again[J];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int n = min(32, p.K - 32 * j);
-    if (n <= 0) break;
-    if (p.keys != nullptr && lane < n) {
-      p.keys[r + 32 * j + lane] = q[j] == 0.f ? -1 : id[j];
-      p.share[r + 32 * j + lane] = q[j];
+    for (int j = 0; j < J; ++j) {
+      all[j] = 0.f;
+      rank[j] = 0;
+      again[j] = false;
     }
+#pragma unroll
+    for (int i = 0; i < J; ++i) {
+      const unsigned live = __ballot_sync(0xffffffffu, id[i] >= 0 && q[i] != 0.f);
+      live_n += __popc(live);
+#pragma unroll 1
+      for (unsigned todo = live; todo != 0u; todo &= todo - 1u) {
+        const int from = __ffs(todo) - 1;
+        const int v = __shfl_sync(0xffffffffu, id[i], from);
+        const float w = __shfl_sync(0xffffffffu, q[i], from);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const bool earlier = 32 * i + from < lane + 32 * j;
+          if (v == id[j]) {
+            all[j] += w;
+            again[j] |= earlier;
+          }
+          rank[j] += v < id[j] || (v == id[j] && earlier);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int k = lane + 32 * j;
+      const bool live = id[j] >= 0 && q[j] != 0.f;
+      own[j] = live && !again[j];
+      if (live) p.targets[rc + rank[j]] = id[j];
+      if (k >= live_n && k < p.K) p.targets[rc + k] = -1;
+      if (p.keys != nullptr && k < p.K) {
+        p.keys[rc + k] = own[j] ? id[j] : -1;
+        p.share[rc + k] = own[j] ? all[j] : 0.f;
+      }
+    }
+  }
+  // calls what(slots k + u G + grp, their pieces of E) for the slots of group j, kGatherU
+  // rows a lane in flight; rows of weight 0 are zeros
+  auto walk = [&](int j, int n, auto what) {
     for (int k = 0; k < n; k += G * kGatherU) {
       uint4 e[kGatherU];
-      float w[kGatherU], lw[kGatherU], z[kGatherU];
 #pragma unroll
       for (int u = 0; u < kGatherU; ++u) {
         const int slot = k + u * G + grp, from = min(slot, 31);
         const int v = __shfl_sync(0xffffffffu, id[j], from);
-        w[u] = __shfl_sync(0xffffffffu, q[j], from);
-        lw[u] = __shfl_sync(0xffffffffu, lq[j], from);
-        if (slot >= n || v < 0 || v >= p.V) w[u] = 0.f;
-        e[u] = w[u] != 0.f && real ? __ldg(reinterpret_cast<const uint4*>(p.E + static_cast<int64_t>(v) * p.D) + sub)
-                                   : make_uint4(0u, 0u, 0u, 0u);
+        const float w = __shfl_sync(0xffffffffu, q[j], from);
+        const bool load = slot < n && v >= 0 && v < p.V && w != 0.f && real;
+        e[u] = load ? __ldg(reinterpret_cast<const uint4*>(p.E + static_cast<int64_t>(v) * p.D) + sub)
+                    : make_uint4(0u, 0u, 0u, 0u);
       }
+      what(k, e);
+    }
+  };
+  // the logits: lane k keeps x of its slot
+  float x[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    x[j] = 0.f;
+    const int n = min(32, p.K - 32 * j);
+    if (n <= 0) break;
+    walk(j, n, [&](int k, const uint4 (&e)[kGatherU]) {
+      float z[kGatherU];
 #pragma unroll
       for (int u = 0; u < kGatherU; ++u) {
-        float x[8];
-        unpack8(e[u], x);
+        float row[8];
+        unpack8(e[u], row);
         z[u] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          z[u] = fmaf(h[i], x[i], z[u]);
-          sp[i] = fmaf(w[u], x[i], sp[i]);
-        }
+        for (int i = 0; i < 8; ++i) z[u] = fmaf(h[i], row[i], z[u]);
       }
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1)
 #pragma unroll
         for (int u = 0; u < kGatherU; ++u) z[u] += __shfl_xor_sync(0xffffffffu, z[u], o);
+      const int mine = lane - k;                 // its place in this batch
 #pragma unroll
       for (int u = 0; u < kGatherU; ++u) {
-        if (w[u] == 0.f) continue;
-        zmax = fmaxf(zmax, z[u]);
-        term += p.kind == kHeadDistill
-                    ? static_cast<double>(w[u]) * (static_cast<double>(lw[u]) - static_cast<double>(z[u]) * p.inv_tau)
-                    : static_cast<double>(z[u]);
+        const float y = __shfl_sync(0xffffffffu, z[u], (mine & (G - 1)) * L);
+        if (mine >= u * G && mine < (u + 1) * G) x[j] = y * p.c2;
+      }
+    });
+  }
+  // their maximum, and the sum of 2^(x - maximum) over the ids
+  float zref = -3.0e38f, tsum = 0.f;
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+    if (own[j]) zref = fmaxf(zref, x[j]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) zref = fmaxf(zref, __shfl_xor_sync(0xffffffffu, zref, o));
+  float y[J];
+  double term = 0.0;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    y[j] = own[j] ? exp2f(x[j] - zref) : 0.f;
+    tsum += y[j];
+    if (p.kind == kHeadDistill && id[j] >= 0 && q[j] != 0.f)
+      term += static_cast<double>(q[j]) * (static_cast<double>(lq[j]) - (static_cast<double>(x[j]) - zref) * 0.6931471805599453);
+    if (p.zt != nullptr && lane + 32 * j < p.K) p.zt[rc + 32 * j + lane] = own[j] ? x[j] : -INFINITY;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    tsum += __shfl_xor_sync(0xffffffffu, tsum, o);
+    if (p.kind == kHeadDistill) term += __shfl_xor_sync(0xffffffffu, term, o);
+  }
+  if (p.sparse != nullptr) {
+    // sum (q - y / T) e and sum y / T e; the rows come from the caches this time
+    float sp[8], sb[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sp[i] = sb[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int n = min(32, p.K - 32 * j);
+      if (n <= 0) break;
+      y[j] = __fdiv_rn(y[j], tsum);
+      const float d = q[j] - y[j];
+      walk(j, n, [&](int k, const uint4 (&e)[kGatherU]) {
+#pragma unroll
+        for (int u = 0; u < kGatherU; ++u) {
+          const int from = min(k + u * G + grp, 31);
+          const float a = __shfl_sync(0xffffffffu, d, from), b = __shfl_sync(0xffffffffu, y[j], from);
+          float row[8];
+          unpack8(e[u], row);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            sp[i] = fmaf(a, row[i], sp[i]);
+            sb[i] = fmaf(b, row[i], sb[i]);
+          }
+        }
+      });
+    }
+    // the groups' parts, in a fixed order
+#pragma unroll
+    for (int o = L; o < 32; o <<= 1) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sp[i] += __shfl_xor_sync(0xffffffffu, sp[i], o);
+        sb[i] += __shfl_xor_sync(0xffffffffu, sb[i], o);
       }
     }
+    if (grp == 0 && piece) {
+      store_floats<8>(p.sparse + 2 * c * p.DP + 8 * sub, sp);
+      store_floats<8>(p.sparse + (2 * c + 1) * p.DP + 8 * sub, sb);
+    }
   }
-  // the groups' parts, in a fixed order
-#pragma unroll
-  for (int o = L; o < 32; o <<= 1) {
-    term += __shfl_xor_sync(0xffffffffu, term, o);
-    zmax = fmaxf(zmax, __shfl_xor_sync(0xffffffffu, zmax, o));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sp[i] += __shfl_xor_sync(0xffffffffu, sp[i], o);
-  }
-  if (p.sparse != nullptr && grp == 0 && piece) store_floats<8>(p.sparse + c * p.DP + 8 * sub, sp);
-  if (p.m2 != nullptr) {
+  if (p.m2 != nullptr && p.lse_in == nullptr) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s = fmaf(h[i], h[i], s);
@@ -520,14 +630,19 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
       const float bound = sqrtf(s) * sqrtf(__uint_as_float(hdr->emax2)) * p.c2;
       const float m = bound * 1.0001f + 0.01f;               // above the rounding of the norms
       p.m2[c] = m;
-      if (!(m - zmax * p.c2 <= kMaxRefGap)) p.hdr->wide = 1; // NaN counts as wide
+      if (!(m - zref <= kMaxRefGap)) p.hdr->wide = 1;        // NaN counts as wide
     }
   }
   if (lane == 0) {
+    if (p.m2 != nullptr && p.lse_in != nullptr) p.m2[c] = p.lse_in[t] * 1.4426950408889634f;
     p.cidx[t] = static_cast<int>(c);
     p.orig[c] = static_cast<int>(t);
-    p.rowterm[c] = term;
-    if (p.kind == kHeadDistill) p.coef[t] = p.weights != nullptr ? p.weights[t] : 1.f;
+    p.tref[c] = zref;
+    p.tsum[c] = tsum;
+    if (p.kind == kHeadDistill) {
+      p.rowterm[c] = term;
+      p.coef[c] = p.weights != nullptr ? p.weights[t] : 1.f;
+    }
   }
 }
 
@@ -551,10 +666,11 @@ __device__ __forceinline__ void failed_loss(const HeadParams& p) {
 }
 
 // ------------------------------------------------------------------ lse
-// Several threads per compacted row join the (max, sum) partials of the row's splits
-// and slabs (or takes the lse of an earlier forward), writes lse, the exponent
-// offset of the item-owned pass and the row's share of the distillation loss,
-// which the last block adds up in block order.
+// Several threads per compacted row join the (reference, sum) partials of the row's
+// splits and slabs with the sum over its targets (or take the lse of an earlier
+// forward), write lse, the exponent offset of the item-owned pass, q - p of the row's
+// pairs and its share of the distillation loss, which the last block adds up in
+// block order.
 //
 // kLseLanes threads share a row: 4, or 32 where a row has more than 128 partials (few
 // positions, many splits: 14 us with 592 partials and 4 threads).
@@ -576,7 +692,7 @@ __global__ void __launch_bounds__(kLseThreads) k_head_lse(const HeadParams p) {
   const int64_t c = static_cast<int64_t>(blockIdx.x) * kLseRows + threadIdx.x % kLseRows;
   __shared__ float sm[kLseLanes][kLseRows], ss[kLseLanes][kLseRows];
   const int t = c < hdr->n_rows ? p.orig[c] : -1;
-  if (p.lse_in == nullptr) {
+  if (p.part != nullptr) {
     // running (reference, sum) over every kLseLanes-th slot, eight loads in flight
     float m = -3.0e38f, sum = 0.f;
     bool bad = false;
@@ -604,11 +720,17 @@ __global__ void __launch_bounds__(kLseThreads) k_head_lse(const HeadParams p) {
     ss[part_of][threadIdx.x % kLseRows] = sum;
     __syncthreads();
   }
+  __shared__ float s_omp[kLseRows], s_ref[kLseRows], s_sum[kLseRows];
   double row_loss = 0.0;
   if (t >= 0 && part_of == 0) {
-    float l2, ref = 0.f;
-    if (p.lse_in != nullptr) {
-      l2 = p.lse_in[t] * 1.4426950408889634f;
+    const float zref = p.tref[c], tsum = p.tsum[c];
+    double l2;
+    float omp, ref = 0.f;
+    if (p.part == nullptr) {
+      // 1 - p from the lse alone: to half a step of it
+      l2 = static_cast<double>(p.lse_in[t]) * 1.4426950408889634;
+      omp = static_cast<float>(1.0 - tsum * exp2(zref - l2));
+      if (omp < 0.f) omp = 0.f;
     } else {
       float m = sm[0][threadIdx.x], sum = 0.f;
 #pragma unroll
@@ -620,17 +742,40 @@ __global__ void __launch_bounds__(kLseThreads) k_head_lse(const HeadParams p) {
         bad |= mq != mq;
         sum += ss[q][threadIdx.x] * exp2f(mq - m);
       }
-      l2 = bad ? NAN : m + log2f(sum);
+      const float top = fmaxf(m, zref);
+      const double rest = static_cast<double>(sum * exp2f(m - top)), all = rest + static_cast<double>(tsum * exp2f(zref - top));
+      l2 = bad ? NAN : static_cast<double>(top) + log2(all);
+      omp = static_cast<float>(rest / all);
       ref = m;
     }
-    p.rescale[c] = p.m2 != nullptr ? exp2f(ref - l2) : 1.f;
-    p.lse2[c] = l2;
-    const double lse = static_cast<double>(l2) * 0.6931471805599453;
-    if (p.lse_out != nullptr) p.lse_out[t] = static_cast<float>(lse);
+    const float l2f = static_cast<float>(l2);
+    p.rescale[c] = p.m2 != nullptr ? static_cast<float>(exp2(static_cast<double>(ref) - l2)) : 1.f;
+    p.lse2[c] = l2f;
+    p.omp[c] = omp;
+    s_omp[threadIdx.x] = omp;
+    s_ref[threadIdx.x] = zref;
+    s_sum[threadIdx.x] = tsum;
+    if (p.lse_out != nullptr) p.lse_out[t] = static_cast<float>(l2 * 0.6931471805599453);
+    const double above = (l2 - static_cast<double>(zref)) * 0.6931471805599453;      // lse - the largest target's logit
     if (p.kind == kHeadDistill) {
       const float w = p.weights != nullptr ? p.weights[t] : 1.f;
-      write_offset(p, c, (p.weights != nullptr ? log2f(fabsf(w)) : 0.f) - l2);
-      row_loss = static_cast<double>(w) * p.tau * p.tau * (p.rowterm[c] + lse);
+      write_offset(p, c, (p.weights != nullptr ? log2f(fabsf(w)) : 0.f) - l2f);
+      row_loss = static_cast<double>(w) * p.tau * p.tau * (p.rowterm[c] + above);
+    } else {
+      p.rowterm[c] = -above;
+    }
+  }
+  if (p.share != nullptr) {
+    __syncthreads();
+    if (t >= 0) {
+      const int i = static_cast<int>(threadIdx.x) % kLseRows;
+      const float omp = s_omp[i], ref = s_ref[i], sum = s_sum[i];
+#pragma unroll 4
+      for (int k = part_of; k < p.K; k += kLseLanes) {
+        const int64_t e = c * p.K + k;
+        const float y = __fdiv_rn(exp2f(p.zt[e] - ref), sum);
+        p.share[e] = fmaf(omp, y, p.share[e] - y);
+      }
     }
   }
   if (p.kind != kHeadDistill || p.loss == nullptr) return;
@@ -671,7 +816,7 @@ __global__ void __launch_bounds__(kPairThreads) k_head_pairs(const HeadParams p)
     double s = 0.0;
     for (int t = a + static_cast<int>(threadIdx.x); t < b; t += kPairThreads) {
       const int c = p.cidx[t];
-      if (c >= 0) s += p.rowterm[c] - static_cast<double>(p.lse2[c]) * 0.6931471805599453;
+      if (c >= 0) s += p.rowterm[c];
     }
     L[q] = head_block_sum(s, red);
   }
@@ -687,7 +832,7 @@ __global__ void __launch_bounds__(kPairThreads) k_head_pairs(const HeadParams p)
     for (int t = a + static_cast<int>(threadIdx.x); t < b; t += kPairThreads) {
       const int c = p.cidx[t];
       if (c < 0) continue;
-      p.coef[t] = q == 0 ? f : -f;
+      p.coef[c] = q == 0 ? f : -f;
       write_offset(p, c, lf - p.lse2[c]);
     }
   }
@@ -710,15 +855,16 @@ __global__ void __launch_bounds__(kPairThreads) k_head_pairs(const HeadParams p)
 }
 
 // ------------------------------------------------------------------ dh
-// dH[t] = g s w_t (sum over splits of the dense part - the sparse part), four
+// dH[t] = g s w_t (sum over splits of the dense part - sum_k (q_k - p_k) e_k), four
 // columns per thread; rows that do not count are zero.
 struct HeadDhParams {
   int T, D, DP, S;
   int64_t Tc;
   const int* cidx;
-  const float* coef;
+  const float* coef;      // [Tc]
   const float* part;      // [S, Tc, DP]
-  const float* sparse;    // [Tc, DP]
+  const float* sparse;    // [Tc, 2, DP]
+  const float* omp;       // [Tc] factor of the second sparse row
   const float* rescale;   // [Tc] factor of the dense part
   void* dH;
   int bf16, accumulate;
@@ -775,8 +921,12 @@ __global__ void __launch_bounds__(256, 4) k_head_dh(const HeadDhParams p) {
   }
   if (t >= p.T) return;
   if (c >= 0) {
-    const float4 q = __ldg(reinterpret_cast<const float4*>(p.sparse + static_cast<int64_t>(c) * p.DP + col));
-    const float f = p.hdr->w.grad_scale * p.coef[t];
+    const float* sp = p.sparse + static_cast<int64_t>(c) * 2 * p.DP + col;
+    float4 q = __ldg(reinterpret_cast<const float4*>(sp));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(sp + p.DP));
+    const float o = p.omp[c];
+    q = make_float4(fmaf(o, b.x, q.x), fmaf(o, b.y, q.y), fmaf(o, b.z, q.z), fmaf(o, b.w, q.w));
+    const float f = p.hdr->w.grad_scale * p.coef[c];
     const float r = p.rescale[c];
     g = make_float4(__fmul_rn(fmaf(a.x, r, -q.x), f), __fmul_rn(fmaf(a.y, r, -q.y), f),
                     __fmul_rn(fmaf(a.z, r, -q.z), f), __fmul_rn(fmaf(a.w, r, -q.w), f));
