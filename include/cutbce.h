@@ -336,7 +336,9 @@ cutbce_status cutbce_embed_backward(const void* dX, int32_t dtype, const int32_t
  * second tensor contraction; for the others, w (p - q) is formed and summed in fp32, so
  * a gradient keeps its relative accuracy where p approaches q.  Deterministic.  All sizes are at
  * least 1.  On a data error (workspace status, cutbce_read_status) the loss is NaN and
- * the other outputs are unspecified.
+ * the other outputs are unspecified.  NaN goes where the formulas take it: a NaN in E
+ * makes the log-sum-exp of every position that counts NaN, and with it the loss and the
+ * gradients; one in a position's state, factor or reference its own terms, the loss and dE.
  *
  * Gradient options (NULL: fp32, overwrite). */
 typedef struct {

@@ -122,13 +122,28 @@ struct SoftmaxParams {
 // pass for 4 / 5 / 6 / 7: 2.09 / 2.01 / 2.05 / 2.14 ms.
 constexpr int kPolyLse = 5, kPolyRows = 5, kPolyItems = 5;
 
+// The larger (largest) of two (three): NaN if one of them is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // 2^x of a pair on the FMA pipe, x clamped below at -125: as exp2_poly3_pair, with
 // the degree chosen by what the value feeds.  kDegree 3 (relative error 7.5e-5) for
 // values that are rounded to bf16 next, 4 (2.7e-6) for the sums of a log-sum-exp.
+// NaN gives the largest float (its bits 0x7FFFFFFF and, shifted, 0xFF800000 add up to
+// 0x7F7FFFFF): a row's sum then passes 2^64, which no finite row's does, and the join of the
+// sums takes it for NaN.
 template <int kDegree>
 __device__ __forceinline__ float2 exp2_fma_pair(float2 x) {
   constexpr float kShift = 12582912.0f;   // 1.5 * 2^23
-  x = f2(fmaxf(x.x, -125.f), fmaxf(x.y, -125.f));
+  x = f2(max_nan(x.x, -125.f), max_nan(x.y, -125.f));
   const float2 j = __fadd2_rn(x, f2(kShift, kShift));
   const float2 jr = __fadd2_rn(j, f2(-kShift, -kShift));
   const float2 f = __ffma2_rn(jr, f2(-1.f, -1.f), x);
@@ -153,13 +168,6 @@ template <int kPoly, int kDegree>
 __device__ __forceinline__ float2 exp2_pair(int pair, float2 x) {
   if ((pair * kPoly) % 16 < kPoly) return exp2_fma_pair<kDegree>(x);
   return f2(ex2_approx(x.x), ex2_approx(x.y));
-}
-
-// The largest of three (one instruction; NaN is passed over).
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
 }
 
 // Forward-only cursor over the columns that a stationary row leaves out: `next` is the
@@ -656,14 +664,15 @@ __global__ void __launch_bounds__(SoftmaxCfg<DP, kPass>::THREADS, 1)
             float mx4[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              mx4[k] = fmaxf(__uint_as_float(r[8 * k]), __uint_as_float(r[8 * k + 1]));
+              mx4[k] = max_nan(__uint_as_float(r[8 * k]), __uint_as_float(r[8 * k + 1]));
 #pragma unroll
               for (int e = 2; e < 8; e += 2)
-                mx4[k] = max3(mx4[k], __uint_as_float(r[8 * k + e]), __uint_as_float(r[8 * k + e + 1]));
+                mx4[k] = max_nan(mx4[k], __uint_as_float(r[8 * k + e]), __uint_as_float(r[8 * k + e + 1]));
             }
-            const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]) * p.c2;
-            // the reference moves only when the maximum has grown by 2^8: sums stay far from overflow
-            const float mn = mx > m + 8.f ? mx : m;
+            const float mx = max_nan(max_nan(mx4[0], mx4[1], mx4[2]), mx4[3]) * p.c2;
+            // the reference moves only when the maximum has grown by 2^8: sums stay far from
+            // overflow; a NaN moves it, and the sum is NaN from there on
+            const float mn = !(mx <= m + 8.f) ? mx : m;
             sum *= ex2_approx(m - mn);
             m = mn;
             const float2 nm = f2(-m, -m);
@@ -717,7 +726,8 @@ __global__ void __launch_bounds__(SoftmaxCfg<DP, kPass>::THREADS, 1)
         ++acc_reads;
         tc_fence_after();
         const int v = s_row0 + row;
-        const float gs = kItems ? hdr->grad_scale : 0.f;
+        // a row whose probabilities are NaN makes every row of dE NaN
+        const float gs = !kItems ? 0.f : p.hdr->nan_rows != 0 ? __int_as_float(0x7FFFFFFF) : hdr->grad_scale;
 #pragma unroll 1
         for (int ch = 0; ch < AC / 16; ++ch) {
           uint32_t r[16];

@@ -53,6 +53,7 @@ struct HeadHeader {
   int pairs_ticket;
   unsigned emax2;           // bits of max |e_v|^2 (with a dH pass that takes the row sums too)
   int wide;                 // 1: some row's logits may lie too far below its bound (see the gather)
+  int nan_rows;             // 1: some row's factor or probabilities are NaN
 };
 static_assert(sizeof(HeadHeader) <= 256, "the workspace header is 256 bytes");
 
@@ -106,12 +107,14 @@ struct HeadParams {
 
 // The exponent offset b of a row of the item-owned pass (log2 domain): as it is, or
 // u = b / c2 as three bf16 values whose sum is u to 24 bits; clamped to +-1e30 (2^b is
-// 0 there, as for padding).
+// 0 there, as for padding).  NaN is noted in the header: the tile pass would lose it where
+// it clamps.
 __device__ __forceinline__ void write_offset(const HeadParams& p, int64_t c, float b2) {
+  if (b2 != b2) p.hdr->nan_rows = 1;
   if (p.b2 != nullptr) p.b2[c] = b2;
   if (p.off16 == nullptr) return;
   float u = b2 / p.c2;
-  if (u == u) u = fminf(fmaxf(u, -1e30f), 1e30f);
+  u = fminf(fmaxf(u, -1e30f), 1e30f);
   const float a = __bfloat162float(__float2bfloat16_rn(u));
   const float b = __bfloat162float(__float2bfloat16_rn(u - a));
   const float d = (u - a) - b;
@@ -676,6 +679,7 @@ __device__ __forceinline__ void failed_loss(const HeadParams& p) {
 // positions, many splits: 14 us with 592 partials and 4 threads).
 constexpr int kLseThreads = 128;
 constexpr int kLseManySlots = 128;
+constexpr float kMaxRowSum = 18446744073709551616.f;   // 2^64: V terms of at most 2^8 stay below 2^39
 
 template <int kLseLanes>
 __global__ void __launch_bounds__(kLseThreads) k_head_lse(const HeadParams p) {
@@ -742,10 +746,11 @@ __global__ void __launch_bounds__(kLseThreads) k_head_lse(const HeadParams p) {
         bad |= mq != mq;
         sum += ss[q][threadIdx.x] * exp2f(mq - m);
       }
+      bad |= !(sum < kMaxRowSum);                    // a NaN logit (see the tile passes)
       const float top = fmaxf(m, zref);
       const double rest = static_cast<double>(sum * exp2f(m - top)), all = rest + static_cast<double>(tsum * exp2f(zref - top));
       l2 = bad ? NAN : static_cast<double>(top) + log2(all);
-      omp = static_cast<float>(rest / all);
+      omp = bad ? NAN : static_cast<float>(rest / all);
       ref = m;
     }
     const float l2f = static_cast<float>(l2);
