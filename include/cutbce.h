@@ -317,8 +317,9 @@ cutbce_status cutbce_embed_forward(const void* E, int64_t V, int64_t D, int32_t 
  * fixed order, so the result is bit-reproducible and hot ids do not serialise; each
  * output is rounded once (with accumulate the fp32 sum is added to the old value
  * and that is rounded).  accumulate = 1 with the dE of a loss gives the gradient
- * of a table that is both the model's input and its output.  A bad id sets the
- * workspace status word (cutbce_read_status); dE is then unspecified.
+ * of a table that is both the model's input and its output.  An id that is neither -1
+ * nor in [0, V) sets the workspace status word (cutbce_read_status) and adds nothing, as
+ * the lookup gives a zero row for it: dE is the gradient of what the lookup gave.
  * ws: cutbce_embed_workspace_size bytes (16 to 42 N, and N D / 2), 256-byte aligned. */
 cutbce_status cutbce_embed_workspace_size(int64_t N, int64_t V, int64_t D, size_t* bytes);
 cutbce_status cutbce_embed_backward(const void* dX, int32_t dtype, const int32_t* ids, int64_t N, int64_t V, int64_t D,

@@ -188,7 +188,9 @@ def _workspace(nbytes: int, like: torch.Tensor, given: Optional[torch.Tensor]) -
 
 
 def embed_forward(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, status: Optional[torch.Tensor] = None):
-    """scale * E[ids] (any shape of ids; -1 gives a zero row), in E's dtype (bf16 or fp32)."""
+    """scale * E[ids] (any shape of ids; -1 gives a zero row), in E's dtype (bf16 or fp32).
+
+    An id out of range gives a zero row too, and sets `status` (an int32 tensor of one value) if there is one."""
     _on_cuda(E)
     if E.get_device() != _current_device():
         with torch.cuda.device(E.device):
@@ -210,7 +212,8 @@ def embed_backward(dX: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 1
     """dE [V, D] of embed_forward: dE[v] = scale * sum of dX over the entries with id v.
 
     `out` (contiguous, [V, D]) is written instead of a new tensor; with accumulate the
-    sums are added to it and rows without an entry keep their value."""
+    sums are added to it and rows without an entry keep their value.  An id out of range adds
+    nothing and sets the status of the workspace (binding.cutbce_read_status)."""
     D = dX.shape[-1]
     if dX.shape[:-1] != ids.shape:
         raise ValueError("dX must be ids.shape + [D]")
@@ -231,17 +234,17 @@ def embed_backward(dX: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 1
 
 class _Embed(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, E, ids, scale):
+    def forward(ctx, E, ids, scale, status):
         ids = _ids32(ids)
         ctx.save_for_backward(ids)
         ctx.shape, ctx.dtype, ctx.scale = E.shape, E.dtype, scale
-        return embed_forward(E, ids, scale)
+        return embed_forward(E, ids, scale, status)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dX):
         (ids,) = ctx.saved_tensors
-        return embed_backward(dX, ids, ctx.shape[0], ctx.scale, grad_dtype=ctx.dtype), None, None
+        return embed_backward(dX, ids, ctx.shape[0], ctx.scale, grad_dtype=ctx.dtype), None, None, None
 
 
 def _hold_leaves(*tensors):
@@ -264,10 +267,10 @@ def _hold_leaves(*tensors):
     return held
 
 
-def embed(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
-    """Differentiable scale * E[ids]; the gradient with respect to E is dense, in E's dtype."""
+def embed(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Differentiable embed_forward; the gradient with respect to E is dense, in E's dtype."""
     held = _hold_leaves(E)  # noqa: F841  (alive until the graph holds them)
-    return _Embed.apply(E, ids, float(scale))
+    return _Embed.apply(E, ids, float(scale), status)
 
 
 def _rows(H: torch.Tensor, *rest: Optional[torch.Tensor]):

@@ -81,10 +81,10 @@ void plan_sort(int64_t N, int64_t V, int64_t D, SortBuffers& b, Layout& l) {
   b.o_part = l.take(4 * 2 * static_cast<size_t>(ceil_div(N, kMinChunk)) * D);   // the most blocks of any geometry
 }
 
-// Sorts the entries by id into *pairs.
+// Sorts the entries by id into *pairs.  stop: see k_sort_scatter.
 template <int IPT>
-cutbce_status run_sort_ipt(const SortBuffers& b, const int32_t* ids, int V, void* ws, int* status, FillJob fill,
-                           cudaStream_t st, const int2** pairs) {
+cutbce_status run_sort_ipt(const SortBuffers& b, const int32_t* ids, int V, void* ws, int* status, const int* stop,
+                           FillJob fill, cudaStream_t st, const int2** pairs) {
   const SortPlan& sp = b.sp;
   const size_t pass_hist = static_cast<size_t>(sp.nblk) << sp.bits;
   int* hist = at<int>(ws, b.o_hist);
@@ -101,7 +101,7 @@ cutbce_status run_sort_ipt(const SortBuffers& b, const int32_t* ids, int V, void
     const FillJob part{fill.dst + p * share, std::max<int64_t>(0, std::min(share, fill.n - p * share)), fill.value};
     const int fill_blocks = static_cast<int>(std::min<int64_t>(ceil_div(part.n, 4 * kSortThreads), 8 * 148));
     k_sort_scatter<IPT><<<sp.nblk + fill_blocks, kSortThreads, 0, st>>>(p == 0 ? ids : nullptr, in, sp.N, V, p * sp.bits, sp.bits, sp.nblk,
-                                                          h, sp.scan ? total : nullptr, out, next, status, part);
+                                                          h, sp.scan ? total : nullptr, out, next, stop, part);
     in = out;
   }
   *pairs = in;
@@ -110,8 +110,8 @@ cutbce_status run_sort_ipt(const SortBuffers& b, const int32_t* ids, int V, void
 
 // clear_status: the status word is not yet cleared (one-kernel sort only: the others
 // follow a memset of the header and the histograms).
-cutbce_status run_sort(const SortBuffers& b, const int32_t* ids, int V, void* ws, int* status, bool clear_status,
-                       FillJob fill, cudaStream_t st, const int2** pairs) {
+cutbce_status run_sort(const SortBuffers& b, const int32_t* ids, int V, void* ws, int* status, const int* stop,
+                       bool clear_status, FillJob fill, cudaStream_t st, const int2** pairs) {
   LaunchScope ls(CUTBCE_KERNEL_ID_SORT, st);
   if (b.cluster) {
     const size_t smem = size_t(64) << b.sp.bits;           // a 16-bit counter per warp and digit
@@ -124,9 +124,9 @@ cutbce_status run_sort(const SortBuffers& b, const int32_t* ids, int V, void* ws
     *pairs = at<int2>(ws, b.o_pairs[(b.sp.passes - 1) & 1]);
     return cudaGetLastError() == cudaSuccess ? CUTBCE_OK : CUTBCE_ERR_CUDA;
   }
-  if (b.sp.ipt == 4) return run_sort_ipt<4>(b, ids, V, ws, status, fill, st, pairs);
-  if (b.sp.ipt == 8) return run_sort_ipt<8>(b, ids, V, ws, status, fill, st, pairs);
-  return run_sort_ipt<16>(b, ids, V, ws, status, fill, st, pairs);
+  if (b.sp.ipt == 4) return run_sort_ipt<4>(b, ids, V, ws, status, stop, fill, st, pairs);
+  if (b.sp.ipt == 8) return run_sort_ipt<8>(b, ids, V, ws, status, stop, fill, st, pairs);
+  return run_sort_ipt<16>(b, ids, V, ws, status, stop, fill, st, pairs);
 }
 
 template <int VEC, typename TIn, typename TOut>
@@ -564,7 +564,7 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
     // the targets' part of dE: sum of coef (q - p) h over the pairs of each item, in fp32
     SegmentParams gp{};
     const FillJob none{at<uint4>(ws, pl.o_first), ceil_div(p.V, 4), 0xFFFFFFFFu};
-    if ((s = run_sort(pl.sort, hp.keys, hp.V, ws, status, false, none, st, &gp.pairs)) != CUTBCE_OK) return s;
+    if ((s = run_sort(pl.sort, hp.keys, hp.V, ws, status, status, false, none, st, &gp.pairs)) != CUTBCE_OK) return s;
     gp.N = pl.Tc * p.K;
     gp.V = hp.V;
     gp.D = hp.D;
@@ -578,7 +578,7 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
     gp.out = at<float>(ws, pl.o_usum);
     gp.first = at<int>(ws, pl.o_first);
     gp.columns = at<uint32_t>(ws, pl.o_columns);
-    gp.status = status;
+    gp.stop = status;
     if ((s = run_sums(gp, true, st)) != CUTBCE_OK) return s;
     sp.first = gp.first;
     sp.columns = gp.columns;
@@ -668,7 +668,8 @@ cutbce_status cutbce_embed_backward(const void* dX, int32_t dtype, const int32_t
   if (!accumulate && aligned(dE, 16) && de_bytes % 16 == 0) fill = FillJob{static_cast<uint4*>(dE), static_cast<int64_t>(de_bytes / 16), 0u};
   else if (!accumulate) CUTBCE_CK(cudaMemsetAsync(dE, 0, de_bytes, st));
   SegmentParams p{};
-  s = run_sort(pl.sort, ids, static_cast<int>(V), ws, status, true, fill, st, &p.pairs);
+  // an id out of range sets the status and counts as empty: dE is the gradient of what the lookup gave
+  s = run_sort(pl.sort, ids, static_cast<int>(V), ws, status, nullptr, true, fill, st, &p.pairs);
   if (s != CUTBCE_OK) return s;
   p.N = N;
   p.V = static_cast<int>(V);
@@ -681,7 +682,6 @@ cutbce_status cutbce_embed_backward(const void* dX, int32_t dtype, const int32_t
   p.out = dE;
   p.out_bf16 = grad_dtype == CUTBCE_GRAD_BF16;
   p.accumulate = accumulate;
-  p.status = status;
   return run_sums(p, dtype == CUTBCE_BF16, st);
 }
 

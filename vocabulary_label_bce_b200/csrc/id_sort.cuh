@@ -9,7 +9,8 @@
 // Every scatter block forms its own offsets from the
 // tile histograms (they sit in L2), and the scatter of one pass counts the
 // histogram of the next with integer atomics, whose order changes nothing.
-// An entry without a row (an empty id) has the key V and sorts to the end.
+// An entry without a row (an empty id, or one out of range, which also sets the status)
+// has the key V and sorts to the end.
 //
 // Sums: a block takes a chunk of consecutive sorted entries, cut into sub-chunks;
 // the lanes of a row add the rows of their sub-chunk in order, four in flight.  A
@@ -144,7 +145,8 @@ __global__ void __launch_bounds__(32 * kScanWarps) k_sort_scan(int* __restrict__
 // One pass over (id, entry index) pairs.  ids (first pass, else null): the plain ids,
 // empty and out-of-range ones counting as V, the index being the entry's own.
 // hist_next (null in the last pass): the next pass's histogram, cleared before the
-// call.  Blocks from nblk on fill.
+// call.  Blocks from nblk on fill.  With `stop` (or null) the pass is left out where it
+// holds an error.
 // The bound of two blocks an SM leaves registers for the histogram loads in flight:
 // without it the compiler holds fewer (two passes over 51,200 entries 20.7 us, with
 // it 13.7; over 200,003 29.0 and 24.5).
@@ -155,7 +157,7 @@ __global__ void __launch_bounds__(kSortThreads, 2) k_sort_scatter(const int* __r
                                                                const int* __restrict__ hist,
                                                                const int* __restrict__ digit_total,
                                                                int2* __restrict__ out, int* __restrict__ hist_next,
-                                                               const int* __restrict__ status, FillJob fill) {
+                                                               const int* __restrict__ stop, FillJob fill) {
   __shared__ uint16_t cnt[kSortWarps][kSortMaxBins];
   __shared__ int off[kSortMaxBins];
   __shared__ int wsum[kSortWarps];
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(kSortThreads, 2) k_sort_scatter(const int* __r
     fill_words(fill, static_cast<int>(blockIdx.x) - nblk, static_cast<int>(gridDim.x) - nblk);
     return;
   }
-  const int failed = *status;                       // looked at before anything is written
+  const int failed = stop != nullptr ? *stop : 0;   // looked at before anything is written
   const int bins = 1 << bits, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // offset of (digit, this tile): all smaller digits, then this digit in earlier
   // tiles.  A thread holds four consecutive digits (of each 1024), sixteen tiles'
@@ -448,7 +450,7 @@ struct SegmentParams {
   int* first;                 // [V] first sorted index of each id's segment (cleared to -1), or null
   uint32_t* columns;          // [N] row of each sorted entry, 2^31 added to the first of an id, or null
   int out_bf16, accumulate;
-  const int* status;
+  const int* stop;            // nothing is added up where it holds an error, or null
 };
 
 template <int VEC>
@@ -545,7 +547,7 @@ template <int VEC, typename TIn, typename TOut>
 __global__ void __launch_bounds__(256, VEC == 8 ? 3 : 4) k_segment_sum(const SegmentParams p, int lanes, int subs, int rounds) {
   __shared__ float s_first[256 * VEC], s_last[256 * VEC];
   __shared__ int s_kind[64], s_key[64], s_start[64];     // 1: first closes, 2: first goes through, 4: last is open
-  if (*p.status != 0) return;
+  if (p.stop != nullptr && *p.stop != 0) return;
   const int sub = static_cast<int>(threadIdx.x) / lanes, lane = static_cast<int>(threadIdx.x) % lanes;
   const int col = (static_cast<int>(blockIdx.y) * lanes + lane) * VEC;
   const int per = kSumBatch * rounds;
@@ -672,7 +674,7 @@ constexpr int kJoinBatch = 8;               // partials in flight per thread
 template <int VEC, typename TOut>
 __global__ void __launch_bounds__(256, 4) k_segment_join(const SegmentParams p, int64_t chunk_entries) {
   __shared__ float red[8][32 * VEC];
-  if (*p.status != 0) return;
+  if (p.stop != nullptr && *p.stop != 0) return;
   const int64_t c0 = blockIdx.x, b0 = c0 * chunk_entries, end = b0 + chunk_entries;
   if (end >= p.N) return;
   const int id = __ldg(&p.pairs[end - 1].x);
