@@ -179,3 +179,13 @@ def test_every_item_a_target():
     lg = r.standard_normal((T, V)).astype(np.float32)
     for entry in ("fused", "split"):
         check_distill(Hf, H, Ef, E, ids, lg, None, 1.0, V, entry)
+
+
+@pytest.mark.parametrize("entry", ["fused", "split", "dE only"])
+@pytest.mark.parametrize("T,V", [(60, 3000), (430, 20000)])
+def test_a_teacher_far_from_the_student(T, V, entry):
+    """Weights over five decades on items that the student all but rules out: each keeps its own accuracy."""
+    Hf, H, Ef, E, y, r = aligned_rows(T, V, 64, 18, 24, 56)
+    ids = np.stack([(y[t] + 1 + r.permutation(V - 1)[:5]) % V for t in range(T)]).astype(np.int32)
+    lg = np.tile(np.array([0, -3, -6, -9, -12], np.float32), (T, 1))
+    check_distill(Hf, H, Ef, E, ids, lg, None, 1.0, 5, entry)

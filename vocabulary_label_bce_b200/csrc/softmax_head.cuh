@@ -22,7 +22,8 @@
 // other items' exponentials on the same reference,
 //   p_k = t_k / (T + R),  p_k - q_k = (t_k / T - q_k) - omp t_k / T,  omp = R / (T + R):
 // omp = 1 - sum_k p_k comes from a sum, not from a difference, so one dominating
-// target keeps all the bits of 1 - p.  For dH the gather forms sum_k (q_k - t_k / T) e_k
+// target keeps all the bits of 1 - p.  (Where omp is the larger part, that difference would
+// lose a small q, and p_k - q_k is formed as (1 - omp) t_k / T - q_k, 1 - omp = T / (T + R).)  For dH the gather forms sum_k (q_k - t_k / T) e_k
 // and sum_k t_k / T e_k, which the dh kernel joins by omp; for dE the factors
 // q_k - p_k weigh the rows of H in the sums over sorted ids.
 //
@@ -724,15 +725,16 @@ __global__ void __launch_bounds__(kLseThreads) k_head_lse(const HeadParams p) {
     ss[part_of][threadIdx.x % kLseRows] = sum;
     __syncthreads();
   }
-  __shared__ float s_omp[kLseRows], s_ref[kLseRows], s_sum[kLseRows];
+  __shared__ float s_omp[kLseRows], s_mass[kLseRows], s_ref[kLseRows], s_sum[kLseRows];
   double row_loss = 0.0;
   if (t >= 0 && part_of == 0) {
     const float zref = p.tref[c], tsum = p.tsum[c];
     double l2;
-    float omp, ref = 0.f;
+    float omp, mass, ref = 0.f;                  // the probability of the other items, and of the targets
     if (p.part == nullptr) {
       // 1 - p from the lse alone: to half a step of it
       l2 = static_cast<double>(p.lse_in[t]) * 1.4426950408889634;
+      mass = static_cast<float>(tsum * exp2(zref - l2));
       omp = static_cast<float>(1.0 - tsum * exp2(zref - l2));
       if (omp < 0.f) omp = 0.f;
     } else {
@@ -748,9 +750,11 @@ __global__ void __launch_bounds__(kLseThreads) k_head_lse(const HeadParams p) {
       }
       bad |= !(sum < kMaxRowSum);                    // a NaN logit (see the tile passes)
       const float top = fmaxf(m, zref);
-      const double rest = static_cast<double>(sum * exp2f(m - top)), all = rest + static_cast<double>(tsum * exp2f(zref - top));
+      const double rest = static_cast<double>(sum * exp2f(m - top)), own = static_cast<double>(tsum * exp2f(zref - top));
+      const double all = rest + own;
       l2 = bad ? NAN : static_cast<double>(top) + log2(all);
       omp = bad ? NAN : static_cast<float>(rest / all);
+      mass = bad ? NAN : static_cast<float>(own / all);
       ref = m;
     }
     const float l2f = static_cast<float>(l2);
@@ -758,6 +762,7 @@ __global__ void __launch_bounds__(kLseThreads) k_head_lse(const HeadParams p) {
     p.lse2[c] = l2f;
     p.omp[c] = omp;
     s_omp[threadIdx.x] = omp;
+    s_mass[threadIdx.x] = mass;
     s_ref[threadIdx.x] = zref;
     s_sum[threadIdx.x] = tsum;
     if (p.lse_out != nullptr) p.lse_out[t] = static_cast<float>(l2 * 0.6931471805599453);
@@ -774,12 +779,12 @@ __global__ void __launch_bounds__(kLseThreads) k_head_lse(const HeadParams p) {
     __syncthreads();
     if (t >= 0) {
       const int i = static_cast<int>(threadIdx.x) % kLseRows;
-      const float omp = s_omp[i], ref = s_ref[i], sum = s_sum[i];
+      const float omp = s_omp[i], mass = s_mass[i], ref = s_ref[i], sum = s_sum[i];
 #pragma unroll 4
       for (int k = part_of; k < p.K; k += kLseLanes) {
         const int64_t e = c * p.K + k;
         const float y = __fdiv_rn(exp2f(p.zt[e] - ref), sum);
-        p.share[e] = fmaf(omp, y, p.share[e] - y);
+        p.share[e] = omp < mass ? fmaf(omp, y, p.share[e] - y) : fmaf(-mass, y, p.share[e]);
       }
     }
   }
