@@ -438,12 +438,13 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
   if (grp == 0 && piece) reinterpret_cast<uint4*>(p.Hc + c * p.DP)[sub] = hraw;
   float h[8];
   unpack8(hraw, h);
-  // the targets' weights
+  // the targets' weights; the largest logit is subtracted before the division by tau, so that
+  // finite ones of any size stay finite and only their differences are rounded
   if (p.kind == kHeadDistill) {
     float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      lq[j] = id[j] >= 0 ? lq[j] * p.inv_tau : -INFINITY;
+      if (id[j] < 0) lq[j] = -INFINITY;
       m = fmaxf(m, lq[j]);
     }
 #pragma unroll
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      lq[j] -= m;
+      lq[j] = (lq[j] - m) * p.inv_tau;
       q[j] = expf(lq[j]);                        // an empty slot: e^-inf = 0
       s += q[j];
     }
