@@ -157,13 +157,13 @@ def _plain(t: torch.Tensor) -> torch.Tensor:
     return (t.detach() if t.requires_grad else t).contiguous()
 
 
-def _ids32(ids: torch.Tensor) -> torch.Tensor:
+def _ids32(ids: torch.Tensor, name: str = "ids") -> torch.Tensor:
     if ids.dtype == torch.int32:
         return ids.contiguous()
     if ids.dtype not in (torch.int64, torch.int16, torch.int8, torch.uint8):
-        raise ValueError(f"ids must be integers, not {ids.dtype}")
+        raise ValueError(f"{name} must be integers, not {ids.dtype}")
     if ids.dtype == torch.int64:
-        ids = ids.clamp(-2, 2 ** 31 - 1)          # a far id stays out of range instead of wrapping
+        ids = ids.clamp(-2, 2 ** 31 - 1)          # a far value stays out of range instead of wrapping
     return ids.to(torch.int32).contiguous()
 
 
@@ -304,7 +304,7 @@ def _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction):
             raise ValueError("without offsets H must be [2P, N, D]")
         offsets = torch.arange(0, H2.shape[0] + 1, H.shape[1], dtype=torch.int32, device=H.device)
     E2 = _plain(E)
-    off = _as(offsets, torch.int32).contiguous()
+    off = _ids32(offsets, "offsets")
     ref = None if ref_logp is None else _as(_plain(ref_logp), torch.float32).view(-1)
     keep = (H2, E2, ids2, off, ref, m)
     return B.make_preference_problem(H2, E2, ids2, off, ref, m, beta, reduction), keep
