@@ -31,3 +31,23 @@ def test_offsets_are_integers():
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     with pytest.raises(ValueError, match="integers"):
         api.preference_forward(H, E, y, torch.tensor([0.0, 15.0, 30.0], device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [torch.bool, torch.float32, torch.bfloat16, torch.int64, torch.int32])
+def test_masks_of_any_type(dtype):
+    """As for cut_bce, a mask of another type counts where it is not zero."""
+    H, E, y = draw()
+    m = torch.arange(30, device="cuda") % 3 != 0
+    other = m.to(dtype) * (256 if dtype == torch.int64 else 1) if dtype != torch.bool else m
+    off = torch.tensor([0, 15, 30], device="cuda")
+    u8 = m.to(torch.uint8)
+    for a, b in zip(api.preference_forward_backward(H, E, y, off, mask=other),
+                    api.preference_forward_backward(H, E, y, off, mask=u8)):
+        assert torch.equal(a, b)
+    lg = torch.zeros(30, 1, device="cuda")
+    for a, b in zip(api.distill_forward_backward(H, E, y[:, None], lg, other),
+                    api.distill_forward_backward(H, E, y[:, None], lg, u8)):
+        assert torch.equal(a, b)
+    loss = api.distill_loss(H.requires_grad_(), E, y[:, None], lg, other)
+    loss.backward()
+    assert torch.equal(H.grad != 0, m[:, None].expand(30, 64))

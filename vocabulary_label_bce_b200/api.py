@@ -167,6 +167,11 @@ def _ids32(ids: torch.Tensor, name: str = "ids") -> torch.Tensor:
     return ids.to(torch.int32).contiguous()
 
 
+def _counts(mask: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """The mask as the library takes it; one of another type counts where it is not zero."""
+    return mask if mask is None or mask.dtype in (torch.uint8, torch.bool) else mask != 0
+
+
 def _scalar_grad(g: Optional[torch.Tensor], like: torch.Tensor) -> Optional[torch.Tensor]:
     if g is None:
         return None
@@ -290,7 +295,7 @@ def _distill_problem(H, E, ids, logits, mask, weights, temperature, reduction):
     _on_cuda(H)
     if logits.shape != ids.shape:
         raise ValueError("teacher ids and logits must have one shape")
-    H2, ids2, lg, m, w = _rows(H, _ids32(ids), _as(logits, torch.float32), mask, _as(weights, torch.float32))
+    H2, ids2, lg, m, w = _rows(H, _ids32(ids), _as(logits, torch.float32), _counts(mask), _as(weights, torch.float32))
     E2 = _plain(E)
     keep = (H2, E2, ids2, lg, m, w)
     return B.make_distill_problem(H2, E2, ids2, lg, m, w, temperature, reduction), keep
@@ -298,7 +303,7 @@ def _distill_problem(H, E, ids, logits, mask, weights, temperature, reduction):
 
 def _preference_problem(H, E, ids, offsets, ref_logp, mask, beta, reduction):
     _on_cuda(H)
-    H2, ids2, m = _rows(H, _ids32(ids), mask)
+    H2, ids2, m = _rows(H, _ids32(ids), _counts(mask))
     if offsets is None:
         if H.dim() != 3:
             raise ValueError("without offsets H must be [2P, N, D]")
@@ -347,7 +352,7 @@ def distill_forward(H, E, teacher_ids, teacher_logits, mask=None, weights=None, 
     """Distillation loss (0-d float64) and the rows' log-sum-exps of z / temperature (float32, H.shape[:-1]).
 
     H [T, D] or [B, N, D] and E [V, D] bf16; teacher_ids [.., K] (-1 empty) and teacher_logits [.., K]
-    the teacher's top items and logits of each position; mask 1 = counts; weights a factor per position."""
+    the teacher's top items and logits of each position; mask: not 0 = counts; weights a factor per position."""
     prob, keep = _distill_problem(H, E, teacher_ids, teacher_logits, mask, weights, temperature, reduction)
     ws = _workspace(B.cutbce_distill_workspace_size(prob, B.OUT_LOSS), H, workspace)
     loss, lse = _loss_lse(H)
