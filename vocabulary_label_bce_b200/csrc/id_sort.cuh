@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kSortThreads, 2) k_sort_scatter(const int* __r
                                                                const int* __restrict__ digit_total,
                                                                int2* __restrict__ out, int* __restrict__ hist_next,
                                                                const int* __restrict__ stop, FillJob fill) {
-  __shared__ uint16_t cnt[kSortWarps][kSortMaxBins];
+  __shared__ __align__(16) uint16_t cnt[kSortWarps][kSortMaxBins];
   __shared__ int off[kSortMaxBins];
   __shared__ int wsum[kSortWarps];
   if (static_cast<int>(blockIdx.x) >= nblk) {
@@ -327,7 +327,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
     fill_words(fill, static_cast<int>(blockIdx.x) - kClusterCtas, static_cast<int>(gridDim.x) - kClusterCtas);
     return;
   }
-  extern __shared__ uint16_t s_cnt[];                       // [32 warps][bins]
+  extern __shared__ __align__(16) uint16_t s_cnt[];                       // [32 warps][bins]
   __shared__ int tot[kSortMaxBins], off[kSortMaxBins];
   __shared__ int wsum[32];
   const int bins = 1 << bits, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
