@@ -461,7 +461,7 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
   hp.logp_out = out.logp;
   int* status = &hp.hdr->w.status;
 
-  const bool small = p.T <= kSmallRows && p.P <= kSmallRows && pl.clear_bytes <= 256 && !pl.fused;
+  const bool small = p.T <= kSmallRows && p.T * p.K <= kSmallSlots && p.P <= kSmallRows && pl.clear_bytes <= 256 && !pl.fused;
   if (!small) CUTBCE_CK(cudaMemsetAsync(hp.hdr, 0, pl.clear_bytes, st));
   {
     LaunchScope ls(CUTBCE_KERNEL_HEAD_PREP, st);

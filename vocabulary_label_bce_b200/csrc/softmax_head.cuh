@@ -312,12 +312,16 @@ __global__ void __launch_bounds__(256) k_head_rows(const HeadParams p) {
 // Rows beyond it set `wide`, and then the log-sum-exp pass runs first and its
 // result is the reference.
 //
-// kSmall (up to kSmallRows positions): every block works out the classes of all
-// positions itself, and block 0 writes the header, so a short call has neither the
-// row kernel nor a memset before this one (one launch of 4 us less for the host).
+// kSmall (up to kSmallRows positions and kSmallSlots slots in all): every block works out
+// the classes of all positions itself, and block 0 writes the header, so a short call has
+// neither the row kernel nor a memset before this one (one launch of 4 us less for the
+// host).  The blocks' repeated reads grow with T^2 K.  Distillation losses, V = 2,048, D = 64,
+// this way / with the row kernel, us on the device: T = 64, K = 16 18 / 25; T = 1,024, K = 16
+// 27 / 28; T = 256, K = 64 49 / 57; T = 512, K = 64 67 / 57; T = 1,024, K = 64 100 / 57.
 constexpr int kGatherU = 4;
 constexpr float kMaxRefGap = 70.f;
 constexpr int kSmallRows = 1024;
+constexpr int kSmallSlots = 16384;
 
 __device__ __forceinline__ void unpack8(uint4 r, float (&x)[8]) {
   const uint32_t u[4] = {r.x, r.y, r.z, r.w};
