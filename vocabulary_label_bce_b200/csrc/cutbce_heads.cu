@@ -365,11 +365,18 @@ cudaError_t launch_softmax_dp(int DP, int grid, const CUtensorMap& s, const CUte
   }
 }
 
-template <int J, bool kSmall>
+template <int L, bool kSmall>
+void launch_gather_width(unsigned grid, const HeadParams& hp, cudaStream_t st) {
+  if (hp.K <= 32) k_head_gather<L, 1, kSmall><<<grid, 256, 0, st>>>(hp);
+  else if (hp.K <= 64) k_head_gather<L, 2, kSmall><<<grid, 256, 0, st>>>(hp);
+  else k_head_gather<L, 4, kSmall><<<grid, 256, 0, st>>>(hp);
+}
+
+template <bool kSmall>
 void launch_gather(int DP, unsigned grid, const HeadParams& hp, cudaStream_t st) {
-  if (DP == 64) k_head_gather<8, J, kSmall><<<grid, 256, 0, st>>>(hp);
-  else if (DP == 128) k_head_gather<16, J, kSmall><<<grid, 256, 0, st>>>(hp);
-  else k_head_gather<32, J, kSmall><<<grid, 256, 0, st>>>(hp);
+  if (DP == 64) launch_gather_width<8, kSmall>(grid, hp, st);
+  else if (DP == 128) launch_gather_width<16, kSmall>(grid, hp, st);
+  else launch_gather_width<32, kSmall>(grid, hp, st);
 }
 
 struct HeadOutputs {
@@ -470,10 +477,8 @@ cutbce_status run_head(const HeadProblem& p, const float* lse_in, const float* g
       const int64_t norm_blocks = pl.fused ? std::min<int64_t>(ceil_div(p.V, 128), 8 * 148) : 0;
       k_head_rows<<<static_cast<unsigned>(pl.n_blk + norm_blocks), 256, 0, st>>>(hp);
     }
-    if (small && p.K <= 32) launch_gather<1, true>(pl.DP, grid, hp, st);
-    else if (small) launch_gather<4, true>(pl.DP, grid, hp, st);
-    else if (p.K <= 32) launch_gather<1, false>(pl.DP, grid, hp, st);
-    else launch_gather<4, false>(pl.DP, grid, hp, st);
+    if (small) launch_gather<true>(pl.DP, grid, hp, st);
+    else launch_gather<false>(pl.DP, grid, hp, st);
     CUTBCE_CK(cudaGetLastError());
   }
   SoftmaxParams sp{};

@@ -332,7 +332,7 @@ __device__ __forceinline__ void unpack8(uint4 r, float (&x)[8]) {
   }
 }
 
-// J: groups of 32 slots (1 for K <= 32, else 4).
+// J: groups of 32 slots (1, 2 or 4).
 template <int L, int J, bool kSmall>
 __global__ void __launch_bounds__(256) k_head_gather(const HeadParams p) {
   constexpr int G = 32 / L;                     // targets side by side
