@@ -335,7 +335,8 @@ cutbce_status cutbce_embed_backward(const void* dX, int32_t dtype, const int32_t
  *   dz_tv = w_t (p_tv - q_tv),   dH = dz E,   dE = dz^T H.
  * For the items with q_tv = 0, w p is rounded to bf16 once, as the operand of the
  * second tensor contraction; for the others, w (p - q) is formed and summed in fp32, so
- * a gradient keeps its relative accuracy where p approaches q.  Deterministic.  All sizes are at
+ * a gradient keeps its relative accuracy where p approaches q (a backward call without
+ * dH has 1 - p from the float lse alone, to half a step of it).  Deterministic.  All sizes are at
  * least 1.  On a data error (workspace status, cutbce_read_status) the loss is NaN and
  * the other outputs are unspecified.  NaN goes where the formulas take it: a NaN in E
  * makes the log-sum-exp of every position that counts NaN, and with it the loss and the

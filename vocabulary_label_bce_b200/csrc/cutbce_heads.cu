@@ -256,8 +256,8 @@ struct HeadPlan {
 // A call that needs both the log-sum-exps and dH can take the row sums in the dH
 // pass, with a bound as the exponentials' reference (see the gather): it saves the
 // log-sum-exp pass and costs a read of E's norms.
-// Measured for the whole gradient call, D = 64, with / without: 67.6 / 65.6 us at
-// T V = 2.6e6 logits, 79.5 / 81.3 at 1.0e7, 125 / 142 at 6.4e7.
+// Measured for the whole gradient call, V = 20,000, D = 64, K = 8, with / without: 60.0 / 60.3
+// us at T V = 2.6e6 logits, 72.2 / 69.9 at 1.0e7, 85.4 / 87.9 at 2.0e7, 130 / 152 at 6.4e7.
 constexpr int64_t kFusedLogits = 8000000;
 
 // Vocabulary splits of a pass that owns position tiles (nT of them) and streams

@@ -1,8 +1,9 @@
 // Row lookup of the item table with a scale: X[n] = s E[id_n], zero for an empty
 // id.  One 16-byte piece of one output row per thread (a scalar per thread where
-// width or alignment forbid it); it moves 2 N D elements and nothing else, so it
-// is bound by HBM for long batches and by launch latency for short ones: 1.6 us at
-// N = 64, 2.0 us at N = 12,800, D = 64 bf16 (3.3 MB).
+// width or alignment forbid it); it moves 2 N D elements and nothing else.  Short batches
+// are bound by launch latency: 1.8 us at N = 64, 2.1 us at N = 12,800, D = 64 bf16 (3.3 MB).
+// Long ones by the random rows: N = 250,000, D = 256, V = 1,000,000 56 us in bf16 (256 MB, 4.6
+// TB/s) and 103 us in fp32 (5.0 TB/s), 70% and 76% of the copy rate.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>

@@ -32,17 +32,18 @@
 // and D = 64.  Every wait is bounded.
 //
 // What bounds it, at T = 12,800 positions (10,240 count), V = 876,000, D = 64:
-//   kLse   2.02 ms.  One exponential per logit: 1.37 ms of SFU time with 5 of 16 on
+//   kLse   2.15 ms (2.02 with nothing left out).  One exponential per logit: 1.37 ms of SFU time with 5 of 16 on
 //          the FMA pipe, which the maximum and the polynomial then share with the
 //          sums.  256-item tiles: the hand-over alone takes 0.65 ms, with 128-item
 //          tiles 1.08.
-//   kRows  2.15 ms and kItems 2.05 ms alone, about 2.4 each in a loop of whole steps,
-//          where the card holds its power limit (sw_power_cap).  The MMAs take 1.4 and
+//   kRows  2.24 ms and kItems 2.10 ms in a few steps, 2.5 and 2.3 in a loop of them,
+//          where the card holds its power limit (sw_power_cap); without the walk over the
+//          targets 1% to 3% less.  The MMAs take 1.4 and
 //          1.6 ms (the D = 64 contraction runs at two thirds of the tensor rate), the
 //          exponentials 1.4 of SFU time; three logit buffers are all that fits beside
 //          the accumulator.  Tried and no better: 64-item tiles with six buffers (2.27 /
 //          2.28 ms), one or three epilogue groups, one arrival per warp.
-//   D = 256, T = 8,192 (7,376 count), V = 1,000,000: kRows 5.6 ms, 1,360 TFLOP/s of its
+//   D = 256, T = 8,192 (7,376 count), V = 1,000,000: kRows 5.7 ms, 1,330 TFLOP/s of its
 //          two products, against 1,404 that a library bf16 product sustains on this
 //          card.  Bound by the tensor cores under the power limit.
 #pragma once
@@ -117,7 +118,7 @@ struct SoftmaxParams {
 };
 
 // Pairs of every 16 whose exponential runs on the FMA pipe instead of the SFU.
-// Measured at 9.0e9 logits, D = 64, for 2 / 4 / 5 / 6 / 7 pairs: dH pass 2.20 / 2.17 /
+// Measured at 9.0e9 logits, D = 64, nothing left out, for 2 / 4 / 5 / 6 / 7 pairs: dH pass 2.20 / 2.17 /
 // 2.15 / 2.15 / 2.26 ms, dE pass 2.23 / 2.09 / 2.11 / 2.10 / 2.16 ms; log-sum-exp
 // pass for 4 / 5 / 6 / 7: 2.09 / 2.01 / 2.05 / 2.14 ms.
 constexpr int kPolyLse = 5, kPolyRows = 5, kPolyItems = 5;

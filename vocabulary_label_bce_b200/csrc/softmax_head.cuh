@@ -14,7 +14,7 @@
 // With p = softmax(z / tau) and q the sparse target weights of a position, the
 // gradient of every such loss is  dz = w (p - q).  Where the losses are small, p is
 // close to q, and p rounded to bf16 would leave only the rounding of that difference
-// (with p = 0.996, 28% to 43% of dH in the norm).  So an item that is a target of a
+// (with p = 0.996 it was off by half in the norm).  So an item that is a target of a
 // row (q != 0) is left out of that row in the tile engine: its exponential counts as
 // 0 in the sums and in the contractions, which carry w p of the other items alone, each
 // rounded to bf16 relative to itself.  The targets are the sparse side's, in fp32.  With
@@ -22,15 +22,17 @@
 // other items' exponentials on the same reference,
 //   p_k = t_k / (T + R),  p_k - q_k = (t_k / T - q_k) - omp t_k / T,  omp = R / (T + R):
 // omp = 1 - sum_k p_k comes from a sum, not from a difference, so one dominating
-// target keeps all the bits of 1 - p.  (Where omp is the larger part, that difference would
-// lose a small q, and p_k - q_k is formed as (1 - omp) t_k / T - q_k, 1 - omp = T / (T + R).)  For dH the gather forms sum_k (q_k - t_k / T) e_k
-// and sum_k t_k / T e_k, which the dh kernel joins by omp; for dE the factors
-// q_k - p_k weigh the rows of H in the sums over sorted ids.
+// target keeps all the bits of 1 - p.  (Where omp is the larger part, that difference
+// would lose a small q, and p_k - q_k is formed as (1 - omp) t_k / T - q_k, with
+// 1 - omp = T / (T + R).)  For dH the gather forms sum_k (q_k - t_k / T) e_k and
+// sum_k t_k / T e_k, which the dh kernel joins by omp; for dE the factors q_k - p_k
+// weigh the rows of H in the sums over sorted ids.
 //
 // All of them are short next to the tile passes and bound by memory latency; at
 // T = 12,800, K = 16, V = 876,000, D = 64: rows 7 us, or 32 with the norms of the
-// 112 MB table, gather 18 us (205,000 rows of E), lse 11 us, pairs 8 us, dh 15 us (79 MB
-// of partials, mostly from L2).
+// 112 MB table, gather 17 us (164,000 rows of E; 23 with gradients, which read them twice),
+// lse 12 us (15 with q - p of the pairs), pairs 9 to 11 us, dh 20 us (79 MB of partials, mostly
+// from L2).
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
